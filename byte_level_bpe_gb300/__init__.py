@@ -8,6 +8,9 @@ device tensors, in one native call ("Making Kimi K3 Tokenization 18x Faster
 For Million Token Agentic Workloads", "One native call for the whole serving
 path"; no Python lists of ids are ever built).
 
+`kv_plan`, `KVCache.append` and `KVCache.attend` (kv.py) take the encode's
+device ids and offsets on into a paged key/value cache.
+
 torch provides device memory and the current stream; every encode step runs
 in libtk's CUDA kernels. Without a built libtk.so or a CUDA device the calls
 raise.
@@ -15,9 +18,10 @@ raise.
 import numpy as np
 
 from . import native
+from .kv import KVCache, KVPlan, KVWorkspace, kv_plan, rope_table
 from .native import TkError  # noqa: F401
 
-__all__ = ["Tokenizer", "TkError", "native"]
+__all__ = ["Tokenizer", "TkError", "native", "KVCache", "KVPlan", "KVWorkspace", "kv_plan", "rope_table"]
 
 
 def _to_bytes(text):

@@ -1,0 +1,502 @@
+// tk_kv.cu -- placing requests in a paged key/value cache (tk_kv_plan) and
+// storing their rows there (tk_kv_append).
+#include <algorithm>
+#include <new>
+
+#include "tk_kv.cuh"
+
+namespace tk {
+
+// ---------------------------------------------------------------- tk_kv_plan
+
+constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_ITEMS = 4;  // tokens per thread and step: one 16-byte store of positions
+
+struct PlanArgs {
+  const int64_t* off;
+  const int32_t* ctx;
+  int64_t R, T;
+  int log2_bs;
+  int32_t* table;
+  int64_t table_stride, table_width;
+  const int32_t* free_ids;
+  int64_t n_free;
+  const int64_t* cursor;
+  const int32_t* parent;
+  int32_t* pos;
+  int64_t* slot;
+  int32_t* req;
+  int32_t* len;
+  int64_t* mask;
+  int64_t* info;
+  int64_t per_cta;  // tokens of one CTA, a multiple of PLAN_ITEMS
+};
+
+// What request r asks of the free list: blocks, or -1 if it cannot be placed
+// whatever the list holds.
+__device__ __forceinline__ int64_t plan_need(const PlanArgs& a, int64_t n, int64_t ctx) {
+  const int64_t up = (1 << a.log2_bs) - 1;
+  const int64_t want = (ctx + n + up) >> a.log2_bs;
+  if (n < 0 || n > INT32_MAX || ctx < 0 || want > a.table_width || (a.parent && n > KV_TREE_MAX)) return -1;
+  return want - ((ctx + up) >> a.log2_bs);
+}
+
+// Exclusive prefix of x over the block's threads; *total = the sum.
+__device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t* s_warp, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();  // s_warp of an earlier call has been read
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < PLAN_THREADS / 32; w++) {
+    const int64_t v = s_warp[w];
+    if (w < warp) before += v;
+    sum += v;
+  }
+  *total = sum;
+  return before + incl - x;
+}
+
+// Request r takes the free blocks [cursor + sum of the needs before it, + its
+// own), so every CTA finds its requests' blocks from the lengths alone: CTA c
+// writes the tokens [c * per_cta, +per_cta), after adding up the needs of the
+// requests before them (12 bytes a request, from L2).  No CTA waits for another and one launch
+// does it all.  A new block's table entry is written by the token at its first
+// place.  The last CTA writes the lengths and the totals.
+__global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs a) {
+  __shared__ int64_t s_warp[PLAN_THREADS / 32];
+  __shared__ int64_t s_off[PLAN_THREADS + 1];
+  __shared__ int64_t s_base[PLAN_THREADS];  // first entry in free_ids, -1 = not placed
+  __shared__ int32_t s_ctx[PLAN_THREADS];
+  __shared__ int64_t s_first;
+  const int tid = threadIdx.x;
+  const int64_t up = (1 << a.log2_bs) - 1;
+  const int64_t cursor = a.cursor ? min(max(*a.cursor, (int64_t)0), a.n_free) : 0;
+
+  if (blockIdx.x == gridDim.x - 1) {
+    const int64_t per = (a.R + PLAN_THREADS - 1) / PLAN_THREADS;
+    const int64_t r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
+    int64_t sum = 0;
+    for (int64_t r = r0; r < r1; r++) sum += max(plan_need(a, a.off[r + 1] - a.off[r], a.ctx[r]), (int64_t)0);
+    int64_t asked, taken, end = cursor + plan_scan(sum, s_warp, &asked);
+    int64_t took = 0, first = INT64_MAX;
+    for (int64_t r = r0; r < r1; r++) {
+      const int64_t n = a.off[r + 1] - a.off[r], ctx = a.ctx[r], need = plan_need(a, n, ctx);
+      if (need > 0) end += need;
+      const bool placed = need == 0 || (need > 0 && end <= a.n_free);
+      if (placed) took += need;
+      else if (first == INT64_MAX) first = r;
+      a.len[r] = (int32_t)(placed ? ctx + n : ctx);
+    }
+    plan_scan(took, s_warp, &taken);
+    if (tid == 0) s_first = INT64_MAX;
+    __syncthreads();
+    if (first != INT64_MAX) atomicMin((long long*)&s_first, (long long)first);
+    __syncthreads();
+    if (tid == 0) {
+      const int64_t r = s_first;
+      a.info[0] = cursor + taken;
+      a.info[1] = asked;
+      a.info[2] = r == INT64_MAX ? TK_OK
+                  : plan_need(a, a.off[r + 1] - a.off[r], a.ctx[r]) < 0 ? TK_E_LIMIT : TK_E_CAPACITY;
+      a.info[3] = r == INT64_MAX ? -1 : r;
+    }
+    return;
+  }
+
+  const int64_t t0 = (int64_t)blockIdx.x * a.per_cta, t1 = min(a.T, t0 + a.per_cta);
+  // the requests that end at or before t0: how many, and what they need
+  int64_t skip = 0, sum = 0;
+  for (int64_t r = tid; r < a.R; r += PLAN_THREADS) {
+    const int64_t e = a.off[r + 1];
+    if (e > t0) break;
+    skip++;
+    sum += max(plan_need(a, e - a.off[r], a.ctx[r]), (int64_t)0);
+  }
+  int64_t r0, used;
+  plan_scan(skip, s_warp, &r0);
+  plan_scan(sum, s_warp, &used);
+
+  int64_t lo = t0;  // tokens before lo are written
+  while (lo < t1 && r0 < a.R) {
+    const int nr = (int)min((int64_t)PLAN_THREADS, a.R - r0);
+    int64_t need = 0, n = 0, ctx = 0, total;
+    if (tid < nr) {
+      const int64_t o = a.off[r0 + tid];
+      n = a.off[r0 + tid + 1] - o;
+      ctx = a.ctx[r0 + tid];
+      need = plan_need(a, n, ctx);
+      s_off[tid] = o;
+      s_ctx[tid] = (int32_t)ctx;
+      if (tid == nr - 1) s_off[nr] = o + n;
+    }
+    const int64_t base = cursor + used + plan_scan(max(need, (int64_t)0), s_warp, &total);
+    if (tid < nr) s_base[tid] = (need == 0 || (need > 0 && base + need <= a.n_free)) ? base : -1;
+    __syncthreads();
+    const int64_t hi = min(t1, s_off[nr]);
+    for (int64_t g = (lo & ~(int64_t)(PLAN_ITEMS - 1)) + (int64_t)tid * PLAN_ITEMS; g < hi;
+         g += (int64_t)PLAN_THREADS * PLAN_ITEMS) {
+      int32_t pos[PLAN_ITEMS], req[PLAN_ITEMS];
+      int64_t slot[PLAN_ITEMS], mask[PLAN_ITEMS];
+      // the request of the first token: the last that starts at or before it and is not empty
+      int k = 0;
+      for (int b = nr, at = max(g, lo) >= s_off[0]; at && b > 1;) {
+        const int h = b >> 1;
+        if (s_off[k + h] <= max(g, lo)) k += h;
+        b -= h;
+      }
+#pragma unroll
+      for (int j = 0; j < PLAN_ITEMS; j++) {
+        const int64_t t = g + j;
+        if (t < lo || t >= hi) continue;
+        while (k + 1 < nr && s_off[k + 1] <= t) k++;
+        const int64_t i = t - s_off[k], c = s_ctx[k], b0 = s_base[k];
+        const int64_t spot = c + i, blk = spot >> a.log2_bs, have = (c + up) >> a.log2_bs;
+        req[j] = (int32_t)(r0 + k);
+        pos[j] = (int32_t)spot;
+        slot[j] = -1;
+        if (b0 >= 0 && i >= 0 && blk < a.table_width) {
+          int32_t* entry = a.table + (r0 + k) * a.table_stride + blk;
+          int32_t id = -1;
+          if (blk < have) {
+            id = *entry;
+          } else if (b0 + blk - have < a.n_free) {
+            id = a.free_ids[b0 + blk - have];
+            if ((spot & up) == 0) *entry = id;
+          }
+          slot[j] = (int64_t)id * (up + 1) + (spot & up);
+        }
+        if (a.parent) {
+          uint64_t m = 0;
+          int depth = 0;
+          if (i >= 0 && i < KV_TREE_MAX && s_off[k] >= 0) {
+            int at = (int)i;
+            m = 1ull << at;
+            for (int p = a.parent[t]; p >= 0 && p < at; p = a.parent[s_off[k] + p]) {
+              m |= 1ull << p;
+              at = p;
+              depth++;
+            }
+          }
+          mask[j] = (int64_t)m;
+          pos[j] = (int32_t)(c + depth);
+        }
+      }
+      if (g >= lo && g + PLAN_ITEMS <= hi) {
+        *reinterpret_cast<int4*>(a.pos + g) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        *reinterpret_cast<int4*>(a.req + g) = make_int4(req[0], req[1], req[2], req[3]);
+        *reinterpret_cast<longlong2*>(a.slot + g) = make_longlong2(slot[0], slot[1]);
+        *reinterpret_cast<longlong2*>(a.slot + g + 2) = make_longlong2(slot[2], slot[3]);
+        if (a.parent) {
+          *reinterpret_cast<longlong2*>(a.mask + g) = make_longlong2(mask[0], mask[1]);
+          *reinterpret_cast<longlong2*>(a.mask + g + 2) = make_longlong2(mask[2], mask[3]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < PLAN_ITEMS; j++) {
+          const int64_t t = g + j;
+          if (t < lo || t >= hi) continue;
+          a.pos[t] = pos[j];
+          a.req[t] = req[j];
+          a.slot[t] = slot[j];
+          if (a.parent) a.mask[t] = mask[j];
+        }
+      }
+    }
+    lo = max(lo, hi);
+    used += total;
+    r0 += nr;
+    __syncthreads();  // the batch's shared arrays have been read
+  }
+  for (int64_t t = lo + tid; t < t1; t += PLAN_THREADS) {  // padding: tokens of no request
+    a.pos[t] = 0;
+    a.req[t] = -1;
+    a.slot[t] = -1;
+    if (a.parent) a.mask[t] = 0;
+  }
+}
+
+// -------------------------------------------------------------- tk_kv_append
+
+constexpr int APPEND_THREADS = 256;
+constexpr int APPEND_PASSES = 4;  // 16-byte loads in flight per lane
+
+struct AppendArgs {
+  const void* qkv;
+  int64_t row_stride, T;
+  int hq, hk, dim;
+  const float* q_gain;
+  const float* k_gain;
+  float eps;
+  const float* rope;
+  int64_t rope_len;
+  int rot;
+  const int32_t* pos;
+  const int64_t* slot;
+  void* q;
+  void* k;
+  void* v;
+  int64_t s_block, s_head, s_token, n_slots;
+  int log2_bs;
+  int chunks;  // warps per token
+};
+
+// One warp takes APPEND_PASSES * (32 / LANES) heads of one token; LANES lanes
+// hold a head, 8 elements each.  y = x * rsqrt(mean(x^2) + eps) * gain, then
+// (a, b) -> (a cos - b sin, b cos + a sin) on the first rot elements; values
+// are copied.  The (cos, sin) of a lane's elements are read once for all its heads.
+template <class T, int LANES, bool NEIGHBOURS>
+__global__ void __launch_bounds__(APPEND_THREADS) k_kv_append(AppendArgs a) {
+  using P = Pair<T>;
+  using T2 = typename P::type;
+  constexpr int HEADS = 32 / LANES;
+  const int lane = threadIdx.x & 31, l = lane % LANES;
+  const int64_t w = ((int64_t)blockIdx.x * APPEND_THREADS + threadIdx.x) >> 5;
+  const int64_t t = w / a.chunks;
+  if (t >= a.T) return;
+  const int all = a.hq + 2 * a.hk, turned = a.hq + a.hk;
+  const int h0 = (int)(w - t * a.chunks) * (HEADS * APPEND_PASSES) + lane / LANES;
+  const int e0 = l * 8;
+  const bool in_dim = e0 < a.dim;
+  const T* row = static_cast<const T*>(a.qkv) + t * a.row_stride + e0;
+
+  union Vec {
+    uint4 u;
+    T2 p[4];
+  };
+  Vec x[APPEND_PASSES];
+#pragma unroll
+  for (int i = 0; i < APPEND_PASSES; i++) {
+    const int h = h0 + i * HEADS;
+    x[i].u = (in_dim && h < all) ? *reinterpret_cast<const uint4*>(row + (int64_t)h * a.dim) : make_uint4(0, 0, 0, 0);
+  }
+
+  const bool rotated = e0 < a.rot;
+  const int half = a.rot >> 1;
+  float cs[8], sn[8];
+  if (rotated) {
+    const int64_t p = a.pos[t];
+    if (p < 0 || p >= a.rope_len) {
+#pragma unroll
+      for (int j = 0; j < 8; j++) cs[j] = sn[j] = __int_as_float(0x7fffffff);
+    } else {
+      const int f0 = NEIGHBOURS ? e0 >> 1 : (e0 < half ? e0 : e0 - half);
+      const float4* src = reinterpret_cast<const float4*>(a.rope + (p * half + f0) * 2);
+#pragma unroll
+      for (int j = 0; j < (NEIGHBOURS ? 2 : 4); j++) {
+        const float4 f = __ldg(src + j);
+        if (NEIGHBOURS) {
+          cs[4 * j] = cs[4 * j + 1] = f.x;
+          sn[4 * j] = sn[4 * j + 1] = f.y;
+          cs[4 * j + 2] = cs[4 * j + 3] = f.z;
+          sn[4 * j + 2] = sn[4 * j + 3] = f.w;
+        } else {
+          cs[2 * j] = f.x;
+          sn[2 * j] = f.y;
+          cs[2 * j + 1] = f.z;
+          sn[2 * j + 1] = f.w;
+        }
+      }
+    }
+    // the partner's sign: the first of a pair gets -b sin, the second +a sin
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+      if (NEIGHBOURS ? (j & 1) == 0 : e0 < half) sn[j] = -sn[j];
+  }
+  const int64_t slot = a.slot[t];
+  const bool stored = slot >= 0 && slot < a.n_slots;
+  const int64_t place = (slot >> a.log2_bs) * a.s_block + (slot & ((1 << a.log2_bs) - 1)) * a.s_token + e0;
+  // the lane that holds the other halves of the pairs
+  const int partner = (lane - l) + (e0 < half ? l + half / 8 : l - half / 8);
+
+#pragma unroll
+  for (int i = 0; i < APPEND_PASSES; i++) {
+    const int h = h0 + i * HEADS;
+    float y[8];
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const float2 f = P::up(x[i].p[j]);
+      y[2 * j] = f.x;
+      y[2 * j + 1] = f.y;
+      ss += f.x * f.x + f.y * f.y;
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float* gain = h < a.hq ? a.q_gain : a.k_gain;
+    if (gain && in_dim && h < turned) {
+      const float inv = 1.f / sqrtf(ss / (float)a.dim + a.eps);
+      const float4 g0 = __ldg(reinterpret_cast<const float4*>(gain + e0)),
+                   g1 = __ldg(reinterpret_cast<const float4*>(gain + e0) + 1);
+      y[0] *= inv * g0.x; y[1] *= inv * g0.y; y[2] *= inv * g0.z; y[3] *= inv * g0.w;
+      y[4] *= inv * g1.x; y[5] *= inv * g1.y; y[6] *= inv * g1.z; y[7] *= inv * g1.w;
+    }
+    if (a.rot) {
+      float z[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) z[j] = NEIGHBOURS ? y[j ^ 1] : __shfl_sync(0xffffffffu, y[j], partner & 31);
+      if (rotated && h < turned)
+#pragma unroll
+        for (int j = 0; j < 8; j++) y[j] = y[j] * cs[j] + z[j] * sn[j];
+    }
+    if (in_dim && h < all) {
+      Vec o;
+      if (h < turned) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) o.p[j] = P::down(y[2 * j], y[2 * j + 1]);
+      } else {
+        o.u = x[i].u;
+      }
+      if (h < a.hq)
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.q) + (t * a.hq + h) * a.dim + e0) = o.u;
+      else if (stored && h < turned)
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.k) + place + (h - a.hq) * a.s_head) = o.u;
+      else if (stored)
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.v) + place + (h - turned) * a.s_head) = o.u;
+    }
+  }
+}
+
+template <class T, int LANES>
+static void append_launch(const AppendArgs& a, bool neighbours, cudaStream_t st) {
+  const int64_t warps = a.T * a.chunks;
+  const unsigned grid = (unsigned)((warps * 32 + APPEND_THREADS - 1) / APPEND_THREADS);
+  if (neighbours) k_kv_append<T, LANES, true><<<grid, APPEND_THREADS, 0, st>>>(a);
+  else k_kv_append<T, LANES, false><<<grid, APPEND_THREADS, 0, st>>>(a);
+}
+
+template <class T>
+static void append_lanes(AppendArgs& a, bool neighbours, cudaStream_t st) {
+  const int lanes = a.dim <= 64 ? 8 : a.dim <= 128 ? 16 : 32;
+  const int heads = 32 / lanes * APPEND_PASSES;
+  a.chunks = (a.hq + 2 * a.hk + heads - 1) / heads;
+  if (lanes == 8) append_launch<T, 8>(a, neighbours, st);
+  else if (lanes == 16) append_launch<T, 16>(a, neighbours, st);
+  else append_launch<T, 32>(a, neighbours, st);
+}
+
+}  // namespace tk
+
+static int kv_arg(const char* where, const char* what) {
+  tk_set_error("%s: %s", where, what);
+  return TK_E_ARG;
+}
+
+static bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+extern "C" int tk_kv_plan(const int64_t* d_off, const int32_t* d_ctx, int64_t R, int64_t T, int block_size,
+                          int32_t* d_table, int64_t table_stride, int64_t table_width,
+                          const int32_t* d_free, int64_t n_free, const int64_t* d_cursor,
+                          const int32_t* d_parent, int32_t* d_pos, int64_t* d_slot, int32_t* d_req,
+                          int32_t* d_len, int64_t* d_mask, int64_t* d_info, void* cuda_stream) {
+  using namespace tk;
+  if (R < 0 || T < 0 || R > INT32_MAX || T > INT32_MAX || n_free < 0 || table_width < 0 || table_stride < table_width)
+    return kv_arg("tk_kv_plan", "bad size");
+  if (!kv_block_size_ok(block_size)) return kv_arg("tk_kv_plan", "block_size is not a power of two from 16 to 128");
+  if (!d_info || (R > 0 && (!d_off || !d_ctx || !d_len || (table_width > 0 && !d_table))) ||
+      (T > 0 && (!d_pos || !d_slot || !d_req || (d_parent && !d_mask))) || (n_free > 0 && !d_free))
+    return kv_arg("tk_kv_plan", "null pointer");
+  if (!aligned16(d_pos) || !aligned16(d_slot) || !aligned16(d_req) || !aligned16(d_mask))
+    return kv_arg("tk_kv_plan", "an output is not 16-byte aligned");
+  int dev = 0, sms = 1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) {
+    tk_set_error("tk_kv_plan: %s", cudaGetErrorString(e));
+    return TK_E_CUDA;
+  }
+  PlanArgs a = {d_off, d_ctx, R, T, kv_log2(block_size), d_table, table_stride, table_width, d_free, n_free,
+                d_cursor, d_parent, d_pos, d_slot, d_req, d_len, d_mask, d_info, 0};
+  // one step of every thread, or an even share of a few CTAs per SM
+  const int64_t step = PLAN_THREADS * PLAN_ITEMS;
+  const int64_t ctas = std::min<int64_t>((T + step - 1) / step, (int64_t)sms * 2);
+  a.per_cta = ctas ? ((T + ctas - 1) / ctas + PLAN_ITEMS - 1) / PLAN_ITEMS * PLAN_ITEMS : 0;
+  k_kv_plan<<<(unsigned)ctas + 1, PLAN_THREADS, 0, (cudaStream_t)cuda_stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    tk_set_error("tk_kv_plan: %s", cudaGetErrorString(e));
+    return TK_E_CUDA;
+  }
+  return TK_OK;
+}
+
+extern "C" int tk_kv_cache_create(void* d_k, void* d_v, int type, int64_t n_blocks, int n_heads, int block_size,
+                                  int head_dim, const int64_t* stride, tk_kv_cache** out) {
+  using namespace tk;
+  const char* where = "tk_kv_cache_create";
+  if (!out || !d_k || !d_v) return kv_arg(where, "null pointer");
+  *out = nullptr;
+  if (type != TK_BF16 && type != TK_F16) return kv_arg(where, "type is neither TK_BF16 nor TK_F16");
+  if (n_blocks < 1 || n_blocks > INT32_MAX || n_heads < 1 || n_heads > 1024) return kv_arg(where, "bad size");
+  if (!kv_block_size_ok(block_size)) return kv_arg(where, "block_size is not a power of two from 16 to 128");
+  if (head_dim < 16 || head_dim > 256 || head_dim % 16) return kv_arg(where, "head_dim is not a multiple of 16 up to 256");
+  int64_t st[3] = {(int64_t)n_heads * block_size * head_dim, (int64_t)block_size * head_dim, head_dim};
+  for (int i = 0; i < 3 && stride; i++) {
+    st[i] = stride[i];
+    if (st[i] < head_dim || st[i] % 8 || st[i] >= (int64_t)1 << 38)
+      return kv_arg(where, "a stride is below head_dim, no multiple of 8 elements, or 2^38 and more");
+  }
+  if (!aligned16(d_k) || !aligned16(d_v)) return kv_arg(where, "keys or values are not 16-byte aligned");
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) {
+    tk_set_error("%s: %s", where, cudaGetErrorString(e));
+    return TK_E_CUDA;
+  }
+  tk_kv_cache* c = new (std::nothrow) tk_kv_cache();
+  if (!c) {
+    tk_set_error("%s: out of memory", where);
+    return TK_E_NOMEM;
+  }
+  c->device = dev;
+  c->type = type;
+  c->n_blocks = n_blocks;
+  c->n_heads = n_heads;
+  c->block_size = block_size;
+  c->log2_block = kv_log2(block_size);
+  c->head_dim = head_dim;
+  for (int i = 0; i < 3; i++) c->stride[i] = st[i];
+  c->k = d_k;
+  c->v = d_v;
+  *out = c;
+  return TK_OK;
+}
+
+extern "C" void tk_kv_cache_free(tk_kv_cache* cache) { delete cache; }
+
+extern "C" int tk_kv_append(const tk_kv_cache* cache, const void* d_qkv, int64_t row_stride, int64_t T, int n_q_heads,
+                            const float* d_q_gain, const float* d_k_gain, float eps, const float* d_rope,
+                            int64_t rope_len, int rot_dim, int neighbours, const int32_t* d_pos,
+                            const int64_t* d_slot, void* d_q, void* cuda_stream) {
+  using namespace tk;
+  const char* where = "tk_kv_append";
+  if (!cache) return kv_arg(where, "null cache");
+  if (T < 0 || T > 1 << 26 || n_q_heads < 1 || n_q_heads > 1024 || rope_len < 0) return kv_arg(where, "bad size");
+  if (row_stride < (int64_t)(n_q_heads + 2 * cache->n_heads) * cache->head_dim || row_stride % 8)
+    return kv_arg(where, "row_stride is below a row's elements or no multiple of 8");
+  if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16 || (rot_dim > 0 && !d_rope))
+    return kv_arg(where, "rot_dim is not a multiple of 16 up to head_dim, or has no table");
+  if (!(eps >= 0.f)) return kv_arg(where, "eps is negative");
+  if (T == 0) return TK_OK;
+  if (!d_qkv || !d_slot || !d_q || (rot_dim > 0 && !d_pos)) return kv_arg(where, "null pointer");
+  if (!aligned16(d_qkv) || !aligned16(d_q) || !aligned16(d_rope) || !aligned16(d_q_gain) || !aligned16(d_k_gain))
+    return kv_arg(where, "a buffer is not 16-byte aligned");
+  AppendArgs a = {d_qkv, row_stride, T, n_q_heads, cache->n_heads, cache->head_dim, d_q_gain, d_k_gain, eps, d_rope,
+                  rope_len, rot_dim, d_pos, d_slot, d_q, cache->k, cache->v, cache->stride[0], cache->stride[1],
+                  cache->stride[2], cache->n_blocks << cache->log2_block, cache->log2_block, 0};
+  if (cache->type == TK_BF16) append_lanes<__nv_bfloat16>(a, neighbours != 0, (cudaStream_t)cuda_stream);
+  else append_lanes<__half>(a, neighbours != 0, (cudaStream_t)cuda_stream);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    tk_set_error("%s: %s", where, cudaGetErrorString(e));
+    return TK_E_CUDA;
+  }
+  return TK_OK;
+}

@@ -20,6 +20,8 @@ TK_E_NOMEM = -6
 TK_E_TIMEOUT = -7
 TK_E_BADID = -8
 TK_E_LIMIT = -9
+TK_BF16 = 1
+TK_F16 = 2
 TK_PATTERN_CL100K = 1
 TK_PATTERN_R50K_DIGITS = 2
 
@@ -27,6 +29,7 @@ TK_PATTERN_R50K_DIGITS = 2
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
+_F32 = ctypes.c_float
 SIGNATURES = {
     "tk_load": (_INT, [_P, _P, _P, _I64, _P, _P, _P, _I64, _INT, ctypes.POINTER(_P)]),
     "tk_free": (None, [_P]),
@@ -54,6 +57,14 @@ SIGNATURES = {
     "tk_cache_stats": (_INT, [_P, ctypes.POINTER(_I64), ctypes.POINTER(_I64), ctypes.POINTER(_I64)]),
     "tk_workspace_set_cache": (_INT, [_P, _P]),
     "tk_last_cache_stats": (_INT, [_P, ctypes.POINTER(_I64), ctypes.POINTER(_I64)]),
+    "tk_kv_plan": (_INT, [_P, _P, _I64, _I64, _INT, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "tk_kv_cache_create": (_INT, [_P, _P, _INT, _I64, _INT, _INT, _INT, ctypes.POINTER(_I64), ctypes.POINTER(_P)]),
+    "tk_kv_cache_free": (None, [_P]),
+    "tk_kv_append": (_INT, [_P, _P, _I64, _I64, _INT, _P, _P, _F32, _P, _I64, _INT, _INT, _P, _P, _P, _P]),
+    "tk_kv_workspace_create": (_INT, [ctypes.POINTER(_P)]),
+    "tk_kv_workspace_free": (None, [_P]),
+    "tk_kv_attend": (_INT, [_P, _P, _P, _I64, _INT, _P, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _F32, _P, _P, _P]),
+    "tk_kv_status": (_INT, [_P, ctypes.POINTER(_I64), _P]),
     "tk_status_string": (ctypes.c_char_p, [_INT]),
     "tk_last_error": (ctypes.c_char_p, []),
 }
@@ -243,3 +254,58 @@ def tk_last_cache_stats(ws):
     a, b = _I64(0), _I64(0)
     check(load().tk_last_cache_stats(ws, ctypes.byref(a), ctypes.byref(b)), "tk_last_cache_stats")
     return a.value, b.value
+
+
+def tk_kv_plan(d_off, d_ctx, R, T, block_size, d_table, table_stride, table_width, d_free, n_free, d_cursor,
+               d_parent, d_pos, d_slot, d_req, d_len, d_mask, d_info, stream):
+    """Device pointers (ints)."""
+    check(load().tk_kv_plan(d_off, d_ctx, R, T, block_size, d_table, table_stride, table_width, d_free, n_free,
+                            d_cursor, d_parent, d_pos, d_slot, d_req, d_len, d_mask, d_info, stream), "tk_kv_plan")
+
+
+def tk_kv_cache_create(d_k, d_v, type, n_blocks, n_heads, block_size, head_dim, stride=None):
+    """stride: three ints (block, head, token, in elements) or None. Returns the handle."""
+    h = _P()
+    st = (_I64 * 3)(*stride) if stride is not None else None
+    check(load().tk_kv_cache_create(d_k, d_v, type, n_blocks, n_heads, block_size, head_dim, st, ctypes.byref(h)),
+          "tk_kv_cache_create")
+    return h
+
+
+def tk_kv_cache_free(cache):
+    if cache:
+        load().tk_kv_cache_free(cache)
+
+
+def tk_kv_append(cache, d_qkv, row_stride, T, n_q_heads, d_q_gain, d_k_gain, eps, d_rope, rope_len, rot_dim,
+                 neighbours, d_pos, d_slot, d_q, stream):
+    """Device pointers (ints)."""
+    check(load().tk_kv_append(cache, d_qkv, row_stride, T, n_q_heads, d_q_gain, d_k_gain, eps, d_rope, rope_len,
+                              rot_dim, 1 if neighbours else 0, d_pos, d_slot, d_q, stream), "tk_kv_append")
+
+
+def tk_kv_workspace_create():
+    h = _P()
+    check(load().tk_kv_workspace_create(ctypes.byref(h)), "tk_kv_workspace_create")
+    return h
+
+
+def tk_kv_workspace_free(ws):
+    if ws:
+        load().tk_kv_workspace_free(ws)
+
+
+def tk_kv_attend(cache, ws, d_q, q_stride, n_q_heads, d_off, R, T, max_new, d_len, d_table, table_stride,
+                 table_width, d_mask, scale, d_out, d_lse, stream):
+    """Device pointers (ints)."""
+    check(load().tk_kv_attend(cache, ws, d_q, q_stride, n_q_heads, d_off, R, T, max_new, d_len, d_table,
+                              table_stride, table_width, d_mask, scale, d_out, d_lse, stream), "tk_kv_attend")
+
+
+def tk_kv_status(ws, stream, raise_on_error=True):
+    """Returns (status, the request it was met at or -1)."""
+    r = _I64(-1)
+    rc = load().tk_kv_status(ws, ctypes.byref(r), stream)
+    if raise_on_error:
+        check(rc, "tk_kv_status")
+    return rc, r.value

@@ -267,6 +267,146 @@ int tk_workspace_set_cache(tk_workspace* ws, tk_cache* cache);
 int tk_last_cache_stats(const tk_workspace* ws, int64_t* hits, int64_t* inserts);
 
 /*
+ * From device ids to a paged key/value cache.  The encode leaves a batch's
+ * ids and their offsets on the device; the three calls below take those
+ * offsets on: tk_kv_plan places every request's new tokens in the cache's
+ * blocks, tk_kv_append stores their keys and values there, tk_kv_attend reads
+ * them back for the new tokens, which may be drafted trees.  The pages have
+ * no counterpart: these are engineering entry points of this library.
+ *
+ * They only queue work on cuda_stream: none waits for the device, allocates
+ * or copies to the host, and all may be captured into a CUDA graph.  What is
+ * wrong with the arguments comes back as TK_E_ARG / TK_E_LIMIT; what is wrong
+ * with the data is found on the device, never reads or writes outside the
+ * buffers, and is reported where each call says.
+ */
+enum { TK_BF16 = 1, TK_F16 = 2 };
+
+/*
+ * tk_kv_plan -- block tables and slot maps from request lengths.
+ *
+ *   d_off[R+1]: request r's new tokens are d_off[r] .. d_off[r+1) (the encode's
+ *       d_out_offsets); d_off[0] = 0, non-decreasing, d_off[R] <= T.  Tokens past
+ *       d_off[R] are padding: position 0, slot -1, request -1, mask 0.
+ *   d_ctx[R]: tokens of r already in the cache.  d_table[R][table_stride]: its
+ *       blocks in order, the first ceil(ctx/block_size) of them filled in.
+ *   d_free[n_free]: ids of free blocks; d_cursor: the first unused entry (one
+ *       int64, e.g. an earlier call's d_info; NULL = 0).
+ *   d_parent[T]: NULL, or the tokens are drafted trees: the parent of a token
+ *       as an index among its request's new tokens (before the token itself;
+ *       any other value = the token continues the context).  At most 64 new
+ *       tokens a request then.
+ *   block_size: a power of two, 16 to 128.
+ *
+ * In the order of the requests each takes the free blocks that its new tokens
+ * need.  A request is placed if d_ctx[r] >= 0, its blocks fit table_width, a
+ * tree holds at most 64 tokens, and the free list reaches; the others take no
+ * part in what follows (slots -1, their table rows as they were).  R, T < 2^31.
+ *
+ *   d_table: the new blocks are written behind the filled ones.
+ *   d_slot[T]: block * block_size + place in the block of every new token, or
+ *       -1.  Token i of a request is stored at ctx + i, drafted or not.
+ *   d_pos[T]: ctx + i, for trees ctx + depth (the token's position in its text).
+ *   d_req[T]: the token's request.
+ *   d_len[R]: tokens in the cache afterwards: ctx + new, or ctx if not placed.
+ *   d_mask[T]: with d_parent only: bit j = new token j is the token itself or
+ *       above it.
+ *   d_info[4]: cursor after the call, free blocks asked for by all requests,
+ *       status of the first request not placed (TK_E_LIMIT, TK_E_CAPACITY; 0
+ *       if all were), that request (-1).
+ */
+int tk_kv_plan(const int64_t* d_off, const int32_t* d_ctx, int64_t R, int64_t T, int block_size,
+               int32_t* d_table, int64_t table_stride, int64_t table_width, const int32_t* d_free,
+               int64_t n_free, const int64_t* d_cursor, const int32_t* d_parent, int32_t* d_pos,
+               int64_t* d_slot, int32_t* d_req, int32_t* d_len, int64_t* d_mask, int64_t* d_info,
+               void* cuda_stream);
+
+/*
+ * A paged cache: the caller's memory for n_blocks blocks of block_size tokens,
+ * n_heads heads and head_dim elements, keys and values each.
+ *
+ *   d_k, d_v: element (block b, head h, token s, x) is at b * stride[0] +
+ *       h * stride[1] + s * stride[2] + x, in elements (stride NULL = the
+ *       packed [n_blocks][n_heads][block_size][head_dim]).  16-byte aligned,
+ *       strides multiples of 8 elements.
+ *   block_size: a power of two, 16 to 128.  head_dim: a multiple of 16, at
+ *       most 256 (tk_kv_attend: 64 or 128).  type: TK_BF16 or TK_F16.
+ *
+ * At most 1,024 heads.  The handle holds the geometry only and belongs to the
+ * current device; one per layer, over one set of block tables.
+ */
+typedef struct tk_kv_cache tk_kv_cache;
+int tk_kv_cache_create(void* d_k, void* d_v, int type, int64_t n_blocks, int n_heads, int block_size,
+                       int head_dim, const int64_t* stride, tk_kv_cache** out);
+void tk_kv_cache_free(tk_kv_cache* cache);
+
+/*
+ * tk_kv_append -- norm of queries and keys for each head, rotation by
+ * position, and the store into the cache, in one pass over the projection.
+ *
+ *   d_qkv[T][row_stride]: a token's n_q_heads query heads, then the cache's
+ *       n_heads key heads, then as many value heads (cache type).
+ *   d_q_gain, d_k_gain [head_dim] fp32: y = x / sqrt(mean(x^2) + eps) * gain
+ *       for each head (NULL = that side has no norm).  Means, norms and
+ *       rotations are computed in fp32 and rounded once.  n_q_heads <= 1,024, T <= 2^26.
+ *   d_rope[rope_len][rot_dim/2][2] fp32: (cos, sin) of every position, for the
+ *       first rot_dim elements of a head (a multiple of 16; NULL with rot_dim
+ *       0 = none).  neighbours = 0 turns the pairs (i, i + rot_dim/2), 1 the
+ *       pairs (2i, 2i + 1).
+ *   d_pos[T] (with d_rope), d_slot[T]: as tk_kv_plan writes them.  A slot that
+ *       is negative or past the cache stores nothing.  A position outside
+ *       [0, rope_len) gives NaN in the rotated elements.
+ *   d_q[T][n_q_heads][head_dim]: the queries, packed.
+ */
+int tk_kv_append(const tk_kv_cache* cache, const void* d_qkv, int64_t row_stride, int64_t T,
+                 int n_q_heads, const float* d_q_gain, const float* d_k_gain, float eps,
+                 const float* d_rope, int64_t rope_len, int rot_dim, int neighbours,
+                 const int32_t* d_pos, const int64_t* d_slot, void* d_q, void* cuda_stream);
+
+/* Scratch of one tk_kv_attend in flight (about 40 MB, whatever the sizes). */
+typedef struct tk_kv_workspace tk_kv_workspace;
+int tk_kv_workspace_create(tk_kv_workspace** out);
+void tk_kv_workspace_free(tk_kv_workspace* ws);
+
+/*
+ * tk_kv_attend -- attention of each request's new tokens over its cache, for
+ * drafted trees, single tokens and chunks of a prompt.
+ *
+ *   d_q[T]: head h of token t is at t * q_stride + h * head_dim (the cache's type,
+ *       16-byte aligned, q_stride a multiple of 8); n_q_heads is a multiple of
+ *       the cache's n_heads, and query head h reads the cache's head
+ *       h / (n_q_heads / n_heads).
+ *   d_off[R+1], d_len[R], d_table: as tk_kv_plan has them; d_len counts the
+ *       new tokens, which are stored already.
+ *   max_new: no request has more new tokens than this (T always holds).
+ *   d_mask[T]: NULL = new token i sees the context and the new tokens up to
+ *       itself.  Else it sees the context and those new tokens j whose bit j
+ *       is set, itself included only if its own bit is (requests of at most
+ *       64 new tokens).
+ *   scale > 0: the factor on q.k before the softmax.
+ *   d_out[T][n_q_heads][head_dim] (the cache's type), d_lse[T][n_q_heads]
+ *       (fp32, NULL = not wanted): the natural log of the row's sum of
+ *       exponentials.  A row that sees nothing gives 0 and -infinity.
+ *       Scores, softmax and sums are fp32; the weights are rounded to the
+ *       cache's type for the product with the values.  Tokens that the mask
+ *       hides, and cache places past d_len, have no influence, whatever they hold.
+ *
+ * Found on the device: a request with more than max_new new tokens, with more
+ * than 64 under a mask, with d_len below its new tokens, or past table_width
+ * blocks.  Its rows are 0 (lse -infinity), and tk_kv_status tells of it.  A
+ * block id outside the cache reads as zeros.
+ * tk_kv_status waits for cuda_stream and gives what the workspace's calls
+ * since the last tk_kv_status met first: TK_OK, TK_E_LIMIT (h_request: the
+ * request) or TK_E_TIMEOUT.
+ */
+int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const void* d_q, int64_t q_stride,
+                 int n_q_heads, const int64_t* d_off, int64_t R, int64_t T, int64_t max_new,
+                 const int32_t* d_len, const int32_t* d_table, int64_t table_stride,
+                 int64_t table_width, const int64_t* d_mask, float scale, void* d_out, float* d_lse,
+                 void* cuda_stream);
+int tk_kv_status(tk_kv_workspace* ws, int64_t* h_request, void* cuda_stream);
+
+/*
  * Per-kernel timing of encodes on a workspace, for benchmarks.  With
  * profiling on, every kernel launch of tk_encode_segments /
  * tk_encode_segments_host / tk_decode is bracketed by CUDA events recorded on
