@@ -14,7 +14,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD_DIR, "libtk.so")
 SOURCES = ["tk_encode.cu", "tk_scan.cu", "tk_tokenizer.cu", "tk_noalloc.cu", "tk_kv.cu", "tk_attend.cu"]
-HEADERS = ["tk_internal.cuh", "tk_kv.cuh", "tk_unicode_table.h"]
+HEADERS = ["tk_internal.cuh", "tk_kv.cuh", "tk_blackwell.cuh", "tk_unicode_table.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

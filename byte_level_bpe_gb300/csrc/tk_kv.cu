@@ -427,6 +427,26 @@ extern "C" int tk_kv_plan(const int64_t* d_off, const int32_t* d_ctx, int64_t R,
   return TK_OK;
 }
 
+// The cache as a tensor (element, token, head, block) whose box is one block of
+// one head and 64 elements: 128-byte rows, swizzled as the tensor cores read them.
+static bool kv_map(const tk_kv_cache* c, void* mem, CUtensorMap* map) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess)
+    return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->block_size, (cuuint64_t)c->n_heads, (cuuint64_t)c->n_blocks};
+  const cuuint64_t strides[3] = {(cuuint64_t)c->stride[2] * 2, (cuuint64_t)c->stride[1] * 2, (cuuint64_t)c->stride[0] * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)c->block_size, 1, 1}, step[4] = {1, 1, 1, 1};
+  return reinterpret_cast<Encode>(fn)(map, c->type == TK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                                      4, mem, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 extern "C" int tk_kv_cache_create(void* d_k, void* d_v, int type, int64_t n_blocks, int n_heads, int block_size,
                                   int head_dim, const int64_t* stride, tk_kv_cache** out) {
   using namespace tk;
@@ -465,6 +485,13 @@ extern "C" int tk_kv_cache_create(void* d_k, void* d_v, int type, int64_t n_bloc
   for (int i = 0; i < 3; i++) c->stride[i] = st[i];
   c->k = d_k;
   c->v = d_v;
+  if (head_dim == 64 || head_dim == 128) {
+    if (!kv_map(c, d_k, &c->map_k) || !kv_map(c, d_v, &c->map_v)) {
+      delete c;
+      tk_set_error("%s: the driver takes no tensor map of this layout", where);
+      return TK_E_CUDA;
+    }
+  }
   *out = c;
   return TK_OK;
 }

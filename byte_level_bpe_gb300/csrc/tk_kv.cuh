@@ -29,12 +29,14 @@ struct Pair;
 template <>
 struct Pair<__nv_bfloat16> {
   using type = __nv_bfloat162;
+  static constexpr bool BF = true;
   static __device__ float2 up(type x) { return __bfloat1622float2(x); }
   static __device__ type down(float a, float b) { return __floats2bfloat162_rn(a, b); }
 };
 template <>
 struct Pair<__half> {
   using type = __half2;
+  static constexpr bool BF = false;
   static __device__ float2 up(type x) { return __half22float2(x); }
   static __device__ type down(float a, float b) { return __floats2half2_rn(a, b); }
 };
@@ -49,10 +51,13 @@ struct tk_kv_cache {
   int64_t stride[3];  // block, head, token, in elements
   void* k;
   void* v;
+  CUtensorMap map_k, map_v;  // for tk_kv_attend; head_dim 64 and 128 only
 };
 
 struct tk_kv_workspace {
   int device;
   int sms;
+  float* part;         // partial outputs of divided units (the allocation's start)
+  unsigned* counters;  // their finished pieces
   tk::KvStatus* status;
 };

@@ -454,8 +454,9 @@ def _check_attend(tk, q, k, v, off, lens, table, masks=None, scale=None, max_new
     fin = torch.isfinite(lse)
     assert torch.equal(torch.isneginf(got_lse.cpu()), ~fin)
     assert bool(((got_lse.cpu().double() - lse).abs()[fin] <= (2.0 ** -16 * (1 + big))[fin]).all())
-    again = cache.attend(c(q), c(off), c(lens), c(table), ws, masks=c(masks), scale=scale)
-    assert torch.equal(again, got)  # the same bits, whatever bound max_new gave
+    again = cache.attend(c(q), c(off), c(lens), c(table), ws, masks=c(masks), scale=scale, max_new=max_new)
+    assert torch.equal(again, got)  # the same bits
+    _close(cache.attend(c(q), c(off), c(lens), c(table), ws, masks=c(masks), scale=scale), o, tol, "no max_new")
     return got
 
 
