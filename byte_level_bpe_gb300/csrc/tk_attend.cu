@@ -21,10 +21,11 @@
 
 namespace tk {
 
-constexpr int AT_KEYS = 128;      // keys of a tile
-constexpr int AT_THREADS = 384;   // 4 warps of producer, products and none; 2 x 4 softmax warps
-constexpr int AT_UNIT_COST = 1;   // what starting a unit costs, in tiles
-constexpr int AT_MIN_SHARE = 4;   // least share of a CTA, in tiles
+constexpr int AT_KEYS = 128;     // keys of a tile
+constexpr int AT_THREADS = 384;  // loads and products of two streams (4 warps), their softmax (2 x 4 warps)
+constexpr int AT_UNIT_COST = 1;  // what starting a unit costs, in tiles
+constexpr int AT_MIN_SHARE = 4;  // least share of a worker, in tiles
+constexpr int AT_SNAP = 2;       // a unit is not cut nearer to its ends than this, in tiles
 
 struct AttendArgs {
   const void* q;
@@ -40,69 +41,135 @@ struct AttendArgs {
   void* out;
   float* lse;
   KvStatus* status;
-  const uint8_t* v;
+  const void* v;
   int64_t n_blocks, s_block, s_head, s_token;
   int log2_bs;
   float* part;         // partial outputs, see part_at
-  unsigned* counters;  // [gridDim.x] pieces of a divided unit that are done, by its first CTA
+  unsigned* counters;  // [2 gridDim.x][2] of a divided unit, by its first stream: pieces that are done, joined
 };
 
 // A request as the schedule sees it.
 struct Request {
-  int64_t t0;   // its first row of q
-  int32_t n, ctx, len;
-  int tiles_m;  // row tiles
+  int t0;  // its first row of q
+  int n, ctx, len;
   bool good;
 };
 
-template <int ROWS>
 __device__ __forceinline__ Request load_request(const AttendArgs& a, int64_t r) {
   Request q;
-  q.t0 = a.off[r];
-  const int64_t n = a.off[r + 1] - q.t0, len = a.len[r];
+  int64_t t0 = a.off[r];
+  const int64_t n = a.off[r + 1] - t0, len = a.len[r];
   q.good = n >= 0 && n <= a.max_new && (!a.mask || n <= KV_TREE_MAX) && len >= n && len <= a.table_width << a.log2_bs &&
-           q.t0 >= 0 && q.t0 + n <= a.T;
+           t0 >= 0 && t0 + n <= a.T;
   // rows that cannot be taken are written as zeros, inside the output whatever the offsets say
-  if (q.t0 < 0) q.t0 = 0;
-  q.n = (int32_t)max((int64_t)0, min(n, a.T - q.t0));
-  q.len = q.good ? (int32_t)len : 0;
-  q.ctx = q.good ? (int32_t)(len - n) : 0;
-  q.tiles_m = (int)(((int64_t)q.n * a.group + ROWS - 1) / ROWS);
+  t0 = max((int64_t)0, min(t0, a.T));
+  q.t0 = (int)t0;
+  q.n = (int)max((int64_t)0, min(n, a.T - t0));
+  q.len = q.good ? (int)len : 0;
+  q.ctx = q.good ? (int)(len - n) : 0;
   return q;
 }
 
-// Keys that row tile m reads, and their tiles (at least one: it writes the rows).
+// Keys that the rows [row0, row0 + ROWS) of a request read, and their tiles (at
+// least one: it writes the rows).
 template <int ROWS>
-__device__ __forceinline__ int unit_keys(const AttendArgs& a, const Request& q, int m) {
+__device__ __forceinline__ int unit_keys(const AttendArgs& a, const Request& q, int row0) {
   if (a.mask || !q.good) return q.len;
-  const int64_t last = min((int64_t)q.n * a.group, (int64_t)(m + 1) * ROWS) - 1;
-  return q.ctx + (int)(last / a.group) + 1;
+  return q.ctx + (min(q.n * a.group, row0 + ROWS) - 1) / a.group + 1;
 }
 __device__ __forceinline__ int key_tiles(int keys) { return max(1, (keys + AT_KEYS - 1) / AT_KEYS); }
 
 template <int ROWS>
 __device__ __forceinline__ int64_t request_cost(const AttendArgs& a, const Request& q) {
   int64_t c = 0;
-  if (a.mask || !q.good) c = (int64_t)q.tiles_m * (key_tiles(q.len) + AT_UNIT_COST);
+  const int rows = q.n * a.group;
+  if (a.mask || !q.good || rows <= ROWS) c = (int64_t)((rows + ROWS - 1) / ROWS) * (key_tiles(q.len) + AT_UNIT_COST);
   else
-    for (int m = 0; m < q.tiles_m; m++) c += key_tiles(unit_keys<ROWS>(a, q, m)) + AT_UNIT_COST;
+    for (int row0 = 0; row0 < rows; row0 += ROWS) c += key_tiles(unit_keys<ROWS>(a, q, row0)) + AT_UNIT_COST;
   return c * a.hk;
 }
 
 // The work is one line of units (request, row tile, key head), each AT_UNIT_COST
-// + its key tiles long; CTA c takes [c * share, (c + 1) * share) of it, so that
-// a long cache is divided over CTAs and short ones are gathered in one.  A warp
-// walks the CTA's part of the line and hands the pieces to the other roles.
+// + its key tiles long.  Worker w takes it from w * share to (w + 1) * share, so
+// that a long cache is divided over workers and short ones are gathered in one; a cut
+// within AT_SNAP of a unit's start or end moves there.
 struct Piece {
-  int t0, r, h;        // first row of q, request, key head
-  int row0, rows;      // rows of the unit among the request's tokens x group
-  int n, ctx, len;     // of the request; ctx = len = 0 if it cannot be taken
-  int open;            // keys that every row of the unit sees
-  int keys, lo, hi;    // keys of the unit; tiles of this piece
-  int first, pieces;   // the CTA with the unit's tile 0; CTAs it is divided over
-  int valid;           // 0 = no more
+  int t0, r, h;       // first row of q, request, key head
+  int row0, rows;     // rows of the unit among the request's tokens x group
+  int n, ctx, len;    // of the request; ctx = len = 0 if it cannot be taken
+  int open;           // keys that every row of the unit sees
+  int keys, lo, hi;   // keys of the unit; tiles of this piece
+  int first, pieces;  // the worker with the unit's tile 0; workers it is divided over
+  int valid;          // 0 = no more, 1 = a request that cannot be taken
 };
 constexpr int AT_PIECES = 4;  // handed over ahead
+
+template <int ROWS>
+struct Walk {
+  int64_t from, to, share;  // the worker's part of the line
+  int64_t u, r;             // where the next unit starts, and its request
+  Request q;
+  int row0, h;
+  bool loaded;
+
+  __device__ __forceinline__ bool next(const AttendArgs& a, Piece& x) {
+    while (u < to && r < a.R) {
+      if (!loaded) {
+        q = load_request(a, r);
+        row0 = h = 0;
+        loaded = true;
+      }
+      if (row0 >= q.n * a.group) {
+        r++;
+        loaded = false;
+        continue;
+      }
+      const int keys = unit_keys<ROWS>(a, q, row0), tiles = key_tiles(keys), cost = tiles + AT_UNIT_COST;
+      if (h == 0 && u + (int64_t)cost * a.hk <= from) {  // all heads are before this worker
+        u += (int64_t)cost * a.hk;
+        row0 += ROWS;
+        continue;
+      }
+      const int lo = cut(from, cost), hi = cut(to, cost);
+      const bool mine = hi > lo && u + cost > from;
+      if (mine) {
+        x.t0 = q.t0;
+        x.r = (int)r;
+        x.h = h;
+        x.row0 = row0;
+        x.rows = min(ROWS, q.n * a.group - row0);
+        x.n = q.n;
+        x.ctx = q.ctx;
+        x.len = q.len;
+        x.open = !q.good ? 0 : a.mask ? q.ctx : q.ctx + row0 / a.group + 1;
+        x.keys = keys;
+        x.lo = max(0, lo - AT_UNIT_COST);
+        x.hi = hi - AT_UNIT_COST;
+        x.first = 0;
+        x.pieces = 1;
+        if (lo > 0 || hi < cost) {
+          x.first = (int)((u + AT_SNAP) / share);
+          x.pieces = (int)((u + cost - AT_SNAP - 1) / share) - x.first + 1;
+        }
+        x.valid = 1 + q.good;
+      }
+      u += cost;
+      if (++h == a.hk) {
+        h = 0;
+        row0 += ROWS;
+      }
+      if (mine) return true;
+    }
+    x.valid = 0;
+    return false;
+  }
+  // a cut at `at` of the line, inside the unit at u
+  __device__ __forceinline__ int cut(int64_t at, int cost) const {
+    const int64_t in = at - u;
+    if (in <= AT_SNAP && in < cost) return 0;
+    return in >= cost - AT_SNAP ? cost : (int)in;
+  }
+};
 
 // The keys of a row among 32 from `first` on, as bits.
 struct Seen {
@@ -141,87 +208,93 @@ __device__ __forceinline__ uint32_t nonfinite2<__half>(uint32_t w) {
   return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
 }
 
-template <int D, int TILES>
-struct AttendSmem {
-  static constexpr int STAGE = AT_KEYS * D * 2;
-  static constexpr int Q = TILES * 128 * D * 2;
-  static constexpr int STAGES = D == 64 ? 12 : (TILES == 1 ? 6 : 5);
-  static constexpr int BARS = Q + STAGES * STAGE;
-  static constexpr int SMALL = BARS + 8 * (2 * STAGES + 8 + 2 * AT_PIECES);
-  // tmem, abort, non-finite values (2), last piece, start of the walk (2 x 8); sums of the warps; pieces; then m and l
-  // of both streams
-  static constexpr int PIECES = SMALL + 48 + 8 * (AT_THREADS / 32);
-  static constexpr int ML = PIECES + AT_PIECES * (int)sizeof(Piece);
-  static constexpr int TOTAL = ML + 2 * 128 * 8;
-  static_assert(TOTAL <= 227 * 1024, "shared memory of one CTA");
+// MODE 0 and 1: a CTA's two streams are workers of their own, with units of at
+// most 32 or 128 rows (0: less room for queries, more for tiles in flight).  MODE
+// 2: a CTA is one worker with units of 256 rows, each stream has 128 of them and both
+// read every tile.
+template <int D, int MODE>
+struct AttendShape {
+  static constexpr int RINGS = MODE == 2 ? 1 : 2, ROWS = MODE == 0 ? 32 : MODE == 1 ? 128 : 256;
+  static constexpr int Q_ROWS = MODE == 0 ? 32 : 128;  // of a stream
+  static constexpr int Q = Q_ROWS * D * 2, STAGE = AT_KEYS * D * 2;
+  static constexpr int STAGES = D == 64 ? (MODE == 2 ? 12 : 6) : MODE == 0 ? 3 : MODE == 1 ? 2 : 5;  // of a ring
+  static constexpr int RING = 2 * Q;
+  // barriers: full and empty of the stages; pieces handed over and taken; per stream q, s, p (2), o ready, o free; drain (2)
+  static constexpr int BARS = RING + RINGS * STAGES * STAGE;
+  static constexpr int N_BARS = RINGS * (2 * STAGES + 2 * AT_PIECES) + 2 * 6 + 2;
+  static constexpr int PIECES = BARS + 8 * N_BARS;
+  static constexpr int SMALL = PIECES + RINGS * AT_PIECES * (int)sizeof(Piece);
+  // start of the walk (2 x 2 x 8), sums of the warps, tensor memory, abort, non-finite values (2 x 8)
+  static constexpr int TOTAL = SMALL + 32 + 8 * (AT_THREADS / 32) + 72;
+  static_assert(SMALL % 8 == 0 && TOTAL <= 227 * 1024, "shared memory of one CTA");
 };
 
-// Partial output of a piece: [row][D] normalised, then [row] log2 of the sum.
-// A CTA has at most two: slot 1 = it holds the unit's first tile.
-template <int D, int ROWS>
-__device__ __forceinline__ float* part_at(const AttendArgs& a, int64_t cta, int slot) {
-  return a.part + (cta * 2 + slot) * (ROWS * (D + 1));
+// Partial output of a piece: [D / 4][128 rows][4] normalised, then [128] log2 of
+// the row's sum: lanes are rows, and neighbours in memory.  A stream has at most two: slot 1
+// if it holds the unit's first tile.
+template <int D>
+__device__ __forceinline__ float* part_at(float* part, int stream, int slot) {
+  return part + (int64_t)(stream * 2 + slot) * (128 * (D + 1));
 }
 
-// Warp 0 loads, warp 1 issues the products, warps 4-7 and 8-11 are two softmax
-// streams with scores and outputs of their own in tensor memory (S 0-127 and
-// 128-255, O from 256 and 384; P over the first half of S).  TILES = 1: both
-// work on the same 128 rows, one on the even and one on the odd key tiles, and are
-// joined at the end.  TILES = 2: each has 128 rows, both read every tile.  While
-// one stream is in its softmax the other's products run.
-template <class T, int D, int TILES>
+// Warps 0 and 3 load (one per ring), warps 1 and 2 issue the products of streams
+// 0 and 1, warps 4-7 and 8-11 are their softmax, a thread per row.  Tensor memory:
+// S at 0 and 128 (P over the first half of it), O at 256 and 384.  While one stream
+// is in its softmax the other's products run.
+template <class T, int D, int MODE>
 __global__ void __launch_bounds__(AT_THREADS, 1)
 k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
-  using L = AttendSmem<D, TILES>;
-  constexpr int ROWS = TILES * 128, HALVES = D / 64, NST = L::STAGES;
+  using L = AttendShape<D, MODE>;
+  constexpr int ROWS = L::ROWS, HALVES = D / 64, NST = L::STAGES;
   constexpr bool BF = Pair<T>::BF;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle goes by address bits
-  const uint32_t base = smem_addr(smem), s_q = base, s_ring = base + L::Q;
-  const uint32_t b_full = base + L::BARS, b_empty = b_full + 8 * NST, b_q = b_empty + 8 * NST, b_s = b_q + 8, b_p = b_s + 16,
-                 b_o = b_p + 16, b_drain = b_o + 8, b_piece = b_drain + 8, b_taken = b_piece + 8 * AT_PIECES;
-  int* small = reinterpret_cast<int*>(smem + L::SMALL);
-  volatile int* abort = small + 1;
-  volatile int* s_bad = small + 2;    // [2] non-finite values among the drafted tokens, by parity of the unit
-  volatile int* s_last = small + 4;
-  int64_t* s_walk = reinterpret_cast<int64_t*>(small + 8);  // first request, where it starts
-  int64_t* s_sum = reinterpret_cast<int64_t*>(small + 12);
-  Piece* s_piece = reinterpret_cast<Piece*>(smem + L::PIECES);
-  float2* s_ml = reinterpret_cast<float2*>(smem + L::ML);
+  const uint32_t base = smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int stream = warp < 4 ? (warp >> 1) : (warp - 4) >> 2;  // warps 0, 1 | 2, 3
+  const int ring = MODE == 2 ? 0 : stream;
+  const uint32_t s_ring = base + L::RING + ring * (NST * L::STAGE), s_q = base + stream * L::Q;
+  const uint32_t b_full = base + L::BARS + ring * 8 * (2 * NST + 2 * AT_PIECES), b_empty = b_full + 8 * NST,
+                 b_piece = b_empty + 8 * NST, b_taken = b_piece + 8 * AT_PIECES;
+  const uint32_t b_q = base + L::BARS + L::RINGS * 8 * (2 * NST + 2 * AT_PIECES) + stream * 56, b_s = b_q + 8, b_p = b_s + 8,
+                 b_o = b_p + 16, b_free = b_o + 8, b_drain = b_free + 8;
+  Piece* s_piece = reinterpret_cast<Piece*>(smem + L::PIECES) + ring * AT_PIECES;
+  int64_t* s_walk = reinterpret_cast<int64_t*>(smem + L::SMALL);  // of each worker: first request, where it starts
+  int64_t* s_sum = s_walk + 4;
+  volatile int* s_int = reinterpret_cast<volatile int*>(s_sum + AT_THREADS / 32);
+  volatile int* abort = s_int + 1;
+  volatile int* s_bad = s_int + 2 + 8 * ring;  // by piece
 
   if (base & 1023) {  // never: the swizzle would not hold
     if (tid == 0) a.status->code = TK_E_CUDA;
     return;
   }
-  if (tid == 0) {
-    for (int i = 0; i < NST; i++) {
-      bar_init(b_full + 8 * i, 1);
-      bar_init(b_empty + 8 * i, 1);
-    }
-    bar_init(b_q, 256);
-    bar_init(b_s, 1);
-    bar_init(b_s + 8, 1);
-    bar_init(b_p, 4);
-    bar_init(b_p + 8, 4);
-    bar_init(b_o, 1);
-    bar_init(b_drain, 1);
-    for (int i = 0; i < AT_PIECES; i++) {
-      bar_init(b_piece + 8 * i, 1);
-      bar_init(b_taken + 8 * i, 10);  // loads, products, 8 softmax warps
+  if (warp == 2) {
+    for (int i = lane; i < L::N_BARS; i += 32) {
+      int count = 1;
+      const int in = i % (2 * NST + 2 * AT_PIECES), st = i - L::RINGS * (2 * NST + 2 * AT_PIECES);
+      if (st < 0) {
+        if (in >= NST && in < 2 * NST) count = MODE == 2 ? 2 : 1;                // empty: the streams that read the stage
+        else if (in >= 2 * NST + AT_PIECES) count = MODE == 2 ? 10 : 5;          // taken: products and softmax warps
+      } else {
+        const int k = st % 7;
+        count = k == 0 ? 128 : k == 2 || k == 3 || k == 5 ? 4 : 1;               // q, p, p, o free
+      }
+      bar_init(base + L::BARS + 8 * i, count);
     }
     fence_bar_init();
-    small[1] = small[2] = small[3] = 0;
   }
-  if (warp == 1) tmem_alloc(smem_addr(small));
+  if (tid < 17) s_int[1 + tid] = 0;
+  if (warp == 1) tmem_alloc(smem_addr(const_cast<int*>(s_int)));
 
-  // where this CTA starts: the requests' costs added up, each thread a run of them
-  int64_t share, x0, total;
+  // where the workers start: the requests' costs added up, each thread a run of them
+  constexpr int WORKERS = MODE == 2 ? 1 : 2;  // of a CTA
+  int64_t share, total = 0;
   {
     const int64_t per = (a.R + AT_THREADS - 1) / AT_THREADS;
     const int64_t r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
     int64_t sum = 0;
     for (int64_t r = r0; r < r1; r++) {
-      const Request q = load_request<ROWS>(a, r);
+      const Request q = load_request(a, r);
       if (!q.good && blockIdx.x == 0 && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = r;
       sum += request_cost<ROWS>(a, q);
     }
@@ -234,294 +307,239 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
     int64_t before = incl - sum;
-    total = 0;
+#pragma unroll
     for (int w = 0; w < AT_THREADS / 32; w++) {
       const int64_t y = s_sum[w];
       if (w < warp) before += y;
       total += y;
     }
-    share = max((int64_t)AT_MIN_SHARE, (total + gridDim.x - 1) / gridDim.x);
-    x0 = blockIdx.x * share;
-    if (x0 >= before && x0 < before + sum) {
+    const unsigned workers = gridDim.x * WORKERS;
+    share = total >> 31 ? (total + workers - 1) / workers : ((unsigned)total + workers - 1) / workers;
+    share = max((int64_t)AT_MIN_SHARE, share);
+    for (int w = 0; w < WORKERS; w++) {
+      const int64_t x = (blockIdx.x * WORKERS + w) * share;
+      if (x < before || x >= before + sum) continue;
       int64_t r = r0, at = before;
       for (; r < r1 - 1; r++) {
-        const int64_t c = request_cost<ROWS>(a, load_request<ROWS>(a, r));
-        if (x0 < at + c) break;
+        const int64_t c = request_cost<ROWS>(a, load_request(a, r));
+        if (x < at + c) break;
         at += c;
       }
-      s_walk[0] = r;
-      s_walk[1] = at;
+      s_walk[2 * w] = r;
+      s_walk[2 * w + 1] = at;
     }
   }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(small);
-  // the next piece, for a whole role; false at the end
-  uint32_t taken = 0;
-  Piece p;
-  auto next = [&]() {
-    if (!bar_wait(b_piece + 8 * (taken % AT_PIECES), (taken / AT_PIECES) & 1, abort)) return false;
-    p = s_piece[taken % AT_PIECES];
-    return p.valid != 0;
-  };
-  auto release = [&]() { bar_arrive(b_taken + 8 * (taken++ % AT_PIECES)); };
+  // all columns are ours, so they start at 0
+  if (tid == 0 && s_int[0] != 0) *abort = 1;
 
-  // registers: 384 x 168 at launch = 128 x 56 + 256 x 224
+  // the pieces, for the roles that follow the loads
+  uint32_t taken = 0;
+  auto coming = [&]() {  // waits for the next one; false when there is none
+    if (!__all_sync(0xffffffffu, bar_wait(b_piece + 8 * (taken % AT_PIECES), (taken / AT_PIECES) & 1, abort))) return false;
+    return s_piece[taken % AT_PIECES].valid != 0;
+  };
+  auto release = [&]() {
+    __syncwarp();
+    if (lane == 0) bar_arrive(b_taken + 8 * (taken % AT_PIECES));
+    taken++;
+  };
+
+  // registers: 384 x 168 at launch = 128 x 72 + 256 x 216
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  if (warp == 0) {
-    // ---- loads: one box per page and 64 elements; lanes hold the ids of 32 pages, and of the next 32
-    uint32_t pos = 0;
-    const int ppt = AT_KEYS >> a.log2_bs;  // pages of a tile
-    bool ok = true;
-    while (ok && __all_sync(0xffffffffu, next())) {
-      __syncwarp();
-      if (lane == 0) release();
-      else taken++;
-      const int n = p.hi - p.lo, pages = (p.keys + (1 << a.log2_bs) - 1) >> a.log2_bs;
-      const int32_t* row = a.table + (int64_t)p.r * a.table_stride;
-      int window = (p.lo * ppt) & ~31;
-      // keys run ahead of values: two id windows each
-      int ids_k = window + lane < pages ? row[window + lane] : 0, win_k = window;
-      int nxt_k = window + 32 + lane < pages ? row[window + 32 + lane] : 0;
-      int ids_v = ids_k, nxt_v = nxt_k, win_v = window;
-      const int loads = 2 * n;
-      for (int i = 0; i < loads; i++, pos++) {
-        // order of use: TILES 1: K0 K1 V0 K2 V1 K3 ...; TILES 2: K0 V0 K1 V1 ...
-        bool value;
-        int t;
-        if (TILES == 2) {
-          value = i & 1;
-          t = i >> 1;
-        } else {
-          const int lead = min(n, 2);
-          if (i < lead) value = false, t = i;
-          else if (i == loads - 1) value = true, t = n - 1;
-          else value = ((i - lead) & 1) == 0, t = value ? (i - lead) >> 1 : ((i - lead) >> 1) + 2;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0 || (warp == 3 && MODE != 2)) {
+      // ---- loads, in the order of their use: K0 V0 K1 V1 ...
+      Walk<ROWS> walk;
+      walk.share = share;
+      walk.from = (blockIdx.x * WORKERS + ring) * share;
+      walk.to = min(total, walk.from + share);
+      walk.r = walk.from < total ? s_walk[2 * ring] : a.R;
+      walk.u = walk.from < total ? s_walk[2 * ring + 1] : total;
+      walk.loaded = false;
+      uint32_t at = 0, pos = 0;
+      bool ok = true;
+      auto hand = [&](const Piece& x) {
+        ok = at < AT_PIECES || bar_wait(b_taken + 8 * (at % AT_PIECES), (at / AT_PIECES + 1) & 1, abort);
+        ok = __all_sync(0xffffffffu, ok) != 0;
+        if (ok && lane == 0) {
+          s_piece[at % AT_PIECES] = x;
+          bar_arrive(b_piece + 8 * (at % AT_PIECES));
         }
-        const int page0 = (p.lo + t) * ppt;
-        if (value) {
-          if (page0 >= win_v + 32) {
-            win_v += 32;
-            ids_v = nxt_v;
-            nxt_v = win_v + 32 + lane < pages ? row[win_v + 32 + lane] : 0;
-          }
-        } else if (page0 >= win_k + 32) {
-          win_k += 32;
-          ids_k = nxt_k;
-          nxt_k = win_k + 32 + lane < pages ? row[win_k + 32 + lane] : 0;
-        }
-        const int np = max(0, min(ppt, pages - page0));
-        const uint32_t st = pos % NST, dst = s_ring + st * L::STAGE;
-        ok = pos < NST || bar_wait(b_empty + 8 * st, (pos / NST + 1) & 1, abort);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) bar_expect(b_full + 8 * st, (uint32_t)np * (HALVES * 128u << a.log2_bs));
-        const int src = (page0 + lane) & 31;
-        const int id = __shfl_sync(0xffffffffu, value ? ids_v : ids_k, src);
         __syncwarp();
-        if (lane < np) {
+        at++;
+      };
+      const int ppt = AT_KEYS >> a.log2_bs;  // pages of a tile
+      Piece nx;
+      walk.next(a, nx);
+      hand(nx);
+      while (ok && nx.valid) {
+        const int r = nx.r, h = nx.h, lo = nx.lo, n = nx.hi - nx.lo, pages = (nx.keys + (1 << a.log2_bs) - 1) >> a.log2_bs;
+        // the next piece is known to the softmax before this one's loads wait for it
+        walk.next(a, nx);
+        hand(nx);
+        // lanes hold the ids of 32 pages, and of the next 32
+        const int32_t* row = a.table + (int64_t)r * a.table_stride;
+        int window = (lo * ppt) & ~31;
+        int ids = window + lane < pages ? row[window + lane] : 0, ids2 = window + 32 + lane < pages ? row[window + 32 + lane] : 0;
+        for (int t = lo; ok && t < lo + n; t++) {
+          const int page0 = t * ppt;
+          if (page0 >= window + 32) {
+            window += 32;
+            ids = ids2;
+            ids2 = window + 32 + lane < pages ? row[window + 32 + lane] : 0;
+          }
+          const int np = max(0, min(ppt, pages - page0));
+          const int id = __shfl_sync(0xffffffffu, ids, (page0 + lane) & 31);
 #pragma unroll
-          for (int s = 0; s < HALVES; s++)
-            tma_load_4d(dst + s * (AT_KEYS * 128) + (lane * 128 << a.log2_bs), value ? &map_v : &map_k, b_full + 8 * st, s * 64,
-                        0, p.h, id);
+          for (int kv = 0; kv < 2; kv++, pos++) {
+            const uint32_t st = pos % NST, dst = s_ring + st * L::STAGE;
+            ok = pos < NST || bar_wait(b_empty + 8 * st, (pos / NST + 1) & 1, abort);
+            if (!(ok = __all_sync(0xffffffffu, ok) != 0)) break;
+            if (lane == 0) bar_expect(b_full + 8 * st, (uint32_t)np * (HALVES * 128u << a.log2_bs));
+            __syncwarp();
+            if (lane < np) {
+#pragma unroll
+              for (int s = 0; s < HALVES; s++)  // a box: one page, 64 elements
+                tma_load_4d(dst + s * (AT_KEYS * 128) + (lane * 128 << a.log2_bs), kv ? &map_v : &map_k, b_full + 8 * st, s * 64,
+                            0, h, id);
+            }
+          }
         }
       }
-    }
-    // given up: the copies in flight land before the CTA ends
-    if (*abort)
-      for (uint32_t k = pos > NST ? pos - NST : 0; k < pos; k++)
-        for (uint32_t i = 0; i < 1u << 16 && !bar_try(b_full + 8 * (k % NST), (k / NST) & 1); i++) {}
-  } else if (warp == 1) {
-    // ---- products, issued by one lane
-    if (lane == 0) {
+      // given up: the copies in flight land before the CTA ends
+      if (*abort)
+        for (uint32_t k = pos > NST ? pos - NST : 0; k < pos; k++)
+          for (uint32_t i = 0; i < 1u << 16 && !bar_try(b_full + 8 * (k % NST), (k / NST) & 1); i++) {}
+    } else if (warp == 1 || warp == 2) {
+      // ---- products: the warp waits as one, one lane issues (with a branch of its own for
+      // the lane every operand would be a divergent one: 120 cycles a product instead of 64)
       constexpr uint32_t KIND_S = mma_kind(BF, 128, AT_KEYS, false), KIND_O = mma_kind(BF, 128, D, true);
-      uint32_t pos = 0, units = 0, np[2] = {0, 0};
+      uint32_t pos = 0, units = 0, nt = 0;
       bool ok = true;
-      auto scores = [&](int stream, uint32_t at, int tile) {  // S = Q K^T
-        const uint32_t k = mma_desc(s_ring + (at % NST) * L::STAGE, 16), q = mma_desc(s_q + tile * (128 * D * 2), 16);
-#pragma unroll
-        for (int i = 0; i < D / 16; i++) {
-          const uint32_t o = (i >> 2) * (128 * 128) + (i & 3) * 32;
-          mma_ss(tmem + stream * 128, q + (o >> 4), k + (o >> 4), KIND_S, i > 0);
-        }
-      };
-      auto outputs = [&](int stream, uint32_t at, bool add) {  // O += P V
-        const uint32_t v = mma_desc(s_ring + (at % NST) * L::STAGE, AT_KEYS * 128);
-#pragma unroll
-        for (int i = 0; i < AT_KEYS / 16; i++)
-          mma_ts(tmem + 256 + stream * 128, tmem + stream * 128 + i * 8, v + i * (2048 >> 4), KIND_O,
-                 add || i > 0);
-      };
-      auto full = [&](uint32_t at) { return bar_wait(b_full + 8 * (at % NST), (at / NST) & 1, abort); };
-      auto weights = [&](int stream) { return bar_wait(b_p + 8 * stream, np[stream]++ & 1, abort); };
-      while (ok && next()) {
-        release();
-        const int n = p.hi - p.lo;
-        ok = bar_wait(b_q, units & 1, abort);
-        units++;
-        if (!ok) break;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        const bool r = __all_sync(0xffffffffu, bar_wait(bar, parity, abort)) != 0;
         tmem_fence_after();
-        if (TILES == 1) {
-          for (int t = 0; ok && t < min(n, 2); t++) {
-            if (!(ok = full(pos))) break;
-            tmem_fence_after();
-            scores(t, pos, 0);
-            mma_commit(b_empty + 8 * (pos % NST));
-            mma_commit(b_s + 8 * t);
-            pos++;
-          }
-          for (int t = 0; ok && t < n; t++) {
-            const int s = t & 1;
-            if (!(ok = full(pos) && weights(s))) break;
-            tmem_fence_after();
-            outputs(s, pos, t >= 2);
-            mma_commit(b_empty + 8 * (pos % NST));
-            pos++;
-            if (t + 2 < n) {
-              if (!(ok = full(pos))) break;
-              tmem_fence_after();
-              scores(s, pos, 0);
-              mma_commit(b_empty + 8 * (pos % NST));
-              mma_commit(b_s + 8 * s);
-              pos++;
-            }
-          }
-        } else {
-          const bool two = p.rows > 128;
-          if (!(ok = full(pos))) break;
-          tmem_fence_after();
-          for (int s = 0; s < (two ? 2 : 1); s++) {
-            scores(s, pos, s);
-            mma_commit(b_s + 8 * s);
-          }
+        return r;
+      };
+      auto full = [&]() { return wait(b_full + 8 * (pos % NST), (pos / NST) & 1); };
+      auto scores = [&]() {  // S = Q K^T
+        const uint32_t k = mma_desc(s_ring + (pos % NST) * L::STAGE, 16), q = mma_desc(s_q, 16);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < D / 16; i++)
+            mma_ss(stream * 128, q + (((i >> 2) * (L::Q_ROWS * 128) + (i & 3) * 32) >> 4),
+                   k + (((i >> 2) * (AT_KEYS * 128) + (i & 3) * 32) >> 4), KIND_S, i > 0);
+          mma_commit(b_s);
           mma_commit(b_empty + 8 * (pos % NST));
-          pos++;
-          for (int t = 0; ok && t < n; t++) {
-            const uint32_t pv = pos, pk = pos + 1;
-            const bool more = t + 1 < n;
-            if (!(ok = full(pv) && (!more || full(pk)))) break;
-            for (int s = 0; s < (two ? 2 : 1); s++) {
-              if (!(ok = weights(s))) break;
-              tmem_fence_after();
-              outputs(s, pv, t > 0);
-              if (s == (two ? 1 : 0)) mma_commit(b_empty + 8 * (pv % NST));
-              if (more) {
-                scores(s, pk, s);
-                if (s == (two ? 1 : 0)) mma_commit(b_empty + 8 * (pk % NST));
-                mma_commit(b_s + 8 * s);
-              }
+        }
+        __syncwarp();
+        pos++;
+      };
+      while (ok && coming()) {
+        const Piece& p = s_piece[taken % AT_PIECES];
+        const int n = __shfl_sync(0xffffffffu, p.hi - p.lo, 0), rows = __shfl_sync(0xffffffffu, p.rows, 0);
+        release();
+        if (MODE == 2 && stream * 128 >= rows) {  // no rows for this stream
+          for (int i = 0; ok && i < 2 * n; i++, pos++) {
+            ok = full();
+            if (ok && lane == 0) bar_arrive(b_empty + 8 * (pos % NST));
+          }
+          continue;
+        }
+        if (!(ok = wait(b_q, units & 1) && full())) break;
+        scores();
+        for (int t = 0; t < n; t++) {
+          if (!(ok = full() && (t > 0 || units == 0 || wait(b_free, (units + 1) & 1)))) break;
+          // O += P V, the first keys as soon as their weights are there
+          const uint32_t v = mma_desc(s_ring + (pos % NST) * L::STAGE, AT_KEYS * 128);
+#pragma unroll
+          for (int half = 0; half < 2; half++) {
+            if (!(ok = wait(b_p + 8 * half, nt & 1))) break;
+            if (elect_one()) {
+#pragma unroll
+              for (int i = half * (AT_KEYS / 32); i < (half + 1) * (AT_KEYS / 32); i++)
+                mma_ts(256 + stream * 128, stream * 128 + i * 8, v + i * (2048 >> 4), KIND_O, t > 0 || i > 0);
+              if (half) mma_commit(b_empty + 8 * (pos % NST));
+              if (half && t == n - 1) mma_commit(b_o);
             }
-            pos += more ? 2 : 1;
+            __syncwarp();
+          }
+          if (!ok) break;
+          nt++;
+          pos++;
+          if (t + 1 < n) {
+            if (!(ok = full())) break;
+            scores();
           }
         }
-        mma_commit(b_o);
+        units++;
       }
       // given up: what was issued ends before tensor memory is freed
       if (*abort) {
-        mma_commit(b_drain);
+        if (elect_one()) mma_commit(b_drain);
+        __syncwarp();
         for (uint32_t i = 0; i < 1u << 16 && !bar_try(b_drain, 0); i++) {}
       }
     }
     __syncwarp();
-  } else if (warp == 2) {
-    // ---- the walk
-    if (lane == 0) {
-      uint32_t at = 0;
-      bool ok = true;
-      auto hand = [&](const Piece& x) {
-        // a piece may take long: this wait has the longer limit (10 s and more)
-        ok = at < AT_PIECES;
-        for (uint32_t i = 0; !ok && i < 1u << 26 && !*abort; i++) {
-          ok = bar_try(b_taken + 8 * (at % AT_PIECES), (at / AT_PIECES + 1) & 1);
-          if (!ok) __nanosleep(200);
-        }
-        if (!ok) {
-          *abort = 1;
-          return;
-        }
-        s_piece[at % AT_PIECES] = x;
-        bar_arrive(b_piece + 8 * (at % AT_PIECES));
-        at++;
-      };
-      Piece x = {};
-      const int64_t end = min(total, x0 + share);
-      int64_t u = x0 < total ? s_walk[1] : end;  // where a request, then a unit starts
-      for (int64_t r = x0 < total ? s_walk[0] : a.R; ok && u < end && r < a.R; r++) {
-        const Request q = load_request<ROWS>(a, r);
-        for (int m = 0; ok && u < end && m < q.tiles_m; m++) {
-          const int keys = unit_keys<ROWS>(a, q, m), tiles = key_tiles(keys), cost = tiles + AT_UNIT_COST;
-          if (u + (int64_t)cost * a.hk <= x0) {
-            u += (int64_t)cost * a.hk;
-            continue;
-          }
-          for (int h = 0; ok && u < end && h < a.hk; h++, u += cost) {
-            const int64_t t = u + AT_UNIT_COST;  // tile 0
-            const int lo = (int)max((int64_t)0, min((int64_t)tiles, x0 - t)), hi = (int)min((int64_t)tiles, end - t);
-            if (hi <= lo) continue;
-            x.t0 = (int)q.t0;
-            x.r = (int)r;
-            x.h = h;
-            x.row0 = m * ROWS;
-            x.rows = min(ROWS, q.n * a.group - x.row0);
-            x.n = q.n;
-            x.ctx = q.ctx;
-            x.len = q.len;
-            x.open = !q.good ? 0 : a.mask ? q.ctx : q.ctx + x.row0 / a.group + 1;
-            x.keys = keys;
-            x.lo = lo;
-            x.hi = hi;
-            x.first = (int)(t / share);
-            x.pieces = (int)((t + tiles - 1) / share) - x.first + 1;
-            x.valid = 1 + q.good;
-            hand(x);
-          }
-        }
-      }
-      x.valid = 0;
-      hand(x);
-    }
-    __syncwarp();
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- softmax: a thread has one row
-    const int stream = (warp - 4) >> 2, wq = warp & 3, row = wq * 32 + lane, sid = tid - 128;
-    const uint32_t t_lane = (uint32_t)(wq * 32) << 16;
-    const uint32_t t_s = tmem + t_lane + stream * 128, t_o = tmem + t_lane + 256;
+    const int wq = warp & 3, row = wq * 32 + lane;  // row = also its lane of tensor memory
+    const uint32_t t_s = ((uint32_t)(wq * 32) << 16) + stream * 128, t_o = t_s + 256;
     const float c = a.scale_log2;
-    uint32_t ns = 0, ring = 0, units = 0;
+    const int me = blockIdx.x * 2 + stream;
+    uint32_t nt = 0, units = 0, stages = 0;
     bool ok = true;
+    int joins = 0, join_first[2], join_pieces[2], join_rows[2];
+    int64_t join_out[2];
+    int join_g[2];
     auto wait = [&](uint32_t bar, uint32_t parity) {  // one answer for the warp
       return __all_sync(0xffffffffu, bar_wait(bar, parity, abort)) != 0;
     };
-    while (ok && __all_sync(0xffffffffu, next())) {
-      __syncwarp();
-      if (lane == 0) release();
-      else taken++;
-      const int n = p.hi - p.lo, rows = p.rows, row0 = p.row0, open = p.open;
-      // queries into 128-byte swizzled rows
-      {
-        const T* q = static_cast<const T*>(a.q);
-        for (int i = sid; i < rows * (D / 8); i += 256) {
-          const int rr = i / (D / 8), ch = i % (D / 8);
-          const int gr = row0 + rr, tok = gr / a.group;
-          const uint4 x = *reinterpret_cast<const uint4*>(q + (p.t0 + tok) * a.q_stride +
-                                                          (p.h * a.group + (gr - tok * a.group)) * D + ch * 8);
-          const int tile = rr >> 7, r7 = rr & 127;
-          *reinterpret_cast<uint4*>(smem + tile * (128 * D * 2) + (ch >> 3) * (128 * 128) + r7 * 128 + (((ch & 7) ^ (r7 & 7)) << 4)) = x;
-        }
-        fence_async_smem();
-        tmem_fence_before();  // the last unit's output has been read
-        bar_arrive(b_q);
+    // queries of the next piece, 16 bytes a copy, into 128-byte swizzled rows
+    auto fetch = [&]() {
+      const Piece& x = s_piece[taken % AT_PIECES];
+      const int row0 = x.row0 + (MODE == 2 ? stream * 128 : 0), rows = min(128, x.rows - (MODE == 2 ? stream * 128 : 0));
+      const T* q = static_cast<const T*>(a.q) + x.t0 * a.q_stride + x.h * a.group * D;
+#pragma unroll 4
+      for (int i = row; i < rows * (D / 8); i += 128) {
+        const int rr = i / (D / 8), ch = i % (D / 8), gr = row0 + rr, tok = gr / a.group;
+        const T* src = q + tok * a.q_stride + (gr - tok * a.group) * D + ch * 8;
+        const uint32_t dst = s_q + (ch >> 3) * (L::Q_ROWS * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
       }
-      const int my = (TILES == 2 ? stream * 128 : 0) + row;
-      const bool live = my < rows;
-      const bool active = (TILES == 2 ? stream * 128 : 0) + wq * 32 < rows;  // of the warp
-      const int gr = row0 + my, tok = live ? gr / a.group : 0;
+    };
+    auto fetched = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_async_smem();
+      bar_arrive(b_q);
+    };
+    bool more = coming();
+    if (more && !(MODE == 2 && stream * 128 >= s_piece[taken % AT_PIECES].rows)) {
+      fetch();
+      fetched();
+    }
+    while (more) {
+      const Piece p = s_piece[taken % AT_PIECES];
+      release();
+      const uint32_t no = taken - 1;
+      const int n = p.hi - p.lo, skip = MODE == 2 ? stream * 128 : 0, rows = min(128, p.rows - skip), open = p.open;
+      const uint32_t v0 = stages + 1;  // stage of the first values
+      stages += 2 * n;
+      if (MODE == 2 && rows <= 0) {  // nothing for this stream
+        if (!(more = coming())) break;
+        if (s_piece[taken % AT_PIECES].rows > skip) {
+          fetch();
+          fetched();
+        }
+        continue;
+      }
+      const bool live = row < rows, active = wq * 32 < rows;  // the row's, the warp's
+      const int gr = p.row0 + skip + row, tok = live ? gr / a.group : 0;
       Seen seen;
       seen.tree = a.mask != nullptr;
       seen.ctx = p.ctx;
@@ -532,15 +550,18 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         if (p.n < 64) seen.mask &= (1ull << p.n) - 1;
       }
       float m = -INFINITY, l = 0.f;
-      const bool idle = TILES == 2 && stream * 128 >= rows;  // no second row tile
 
-      for (int t = TILES == 1 ? stream : 0; !idle && t < n; t += TILES == 1 ? 2 : 1) {
+      for (int t = 0; t < n; t++, nt++) {
         const int k0 = (p.lo + t) * AT_KEYS;
         const bool masked = k0 + AT_KEYS > open;
-        if (!(ok = wait(b_s + 8 * stream, ns++ & 1))) break;
+        if (!(ok = wait(b_s, nt & 1))) break;
         tmem_fence_after();
+        if (t == n - 1) {  // the queries have been read for the last time: the next ones come in meanwhile
+          more = coming();
+          if (more && !(MODE == 2 && s_piece[taken % AT_PIECES].rows <= skip)) fetch();
+        }
+        uint32_t s[128];
         if (active) {
-          uint32_t s[128];
 #pragma unroll
           for (int i = 0; i < 4; i++) tmem_ld32(s + 32 * i, t_s + 32 * i);
           tmem_wait_ld();
@@ -553,126 +574,112 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
                 if (!((w >> e) & 1)) s[32 * i + e] = 0xff800000u;
             }
           }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float top[4];
 #pragma unroll
-          for (int i = 0; i < 128; i++) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(s[i]));
+          for (int i = 0; i < 4; i++) top[i] = fmaxf(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+#pragma unroll
+          for (int i = 8; i < 128; i += 2)
+            top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
           const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          const bool first = t < (TILES == 1 ? 2 : 1);  // the stream's first tile
           const bool grow = live && mx > m && !((mx - m) * c <= 8.f);
-          if (!first && __any_sync(0xffffffffu, grow)) {
+          if (t > 0 && __any_sync(0xffffffffu, grow)) {
             // the products before S are done: O is ours
             const float f = grow ? exp2_fast((m - mx) * c) : 1.f;
 #pragma unroll
             for (int i = 0; i < D / 32; i++) {
               uint32_t o[32];
-              tmem_ld32(o, t_o + stream * 128 + 32 * i);
+              tmem_ld32(o, t_o + 32 * i);
               tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(t_o + stream * 128 + 32 * i, o);
+              tmem_st32(t_o + 32 * i, o);
             }
             l *= f;
           }
-          if (first || grow) m = mx;
-          const float mc = m == -INFINITY ? 0.f : m * c;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          if (t == 0 || grow) m = mx;
+        }
+        if (masked) {
+          // Values of keys past the request's end become 0; so do infinities and NaN of
+          // keys that only some rows see: 0 * inf in a product would reach the others.
+          // (Rows that do see them get them back below.)  Streams that share a tile leave it to the first.
+          if (MODE != 2 || stream == 0) {
+            const uint32_t at = v0 + 2 * t;
+            if (!(ok = wait(b_full + 8 * (at % NST), (at / NST) & 1))) break;
+            const int key = k0 + row;
+            if (key >= open) {
+              uint8_t* v = smem + (s_ring - base) + (at % NST) * L::STAGE + row * 128;
+              bool bad = false;
 #pragma unroll
-          for (int i = 0; i < 2; i++) {
+              for (int i = 0; i < D / 8; i++) {
+                uint4* x = reinterpret_cast<uint4*>(v + (i >> 3) * (AT_KEYS * 128) + (((i & 7) ^ (row & 7)) << 4));
+                if (key >= p.len) {
+                  *x = make_uint4(0, 0, 0, 0);
+                } else {
+                  uint4 y = *x;
+                  uint32_t* z = reinterpret_cast<uint32_t*>(&y);
+                  const uint32_t any = nonfinite2<T>(z[0]) | nonfinite2<T>(z[1]) | nonfinite2<T>(z[2]) | nonfinite2<T>(z[3]);
+                  if (any) {
+                    bad = true;
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                      const uint32_t b = nonfinite2<T>(z[e]);
+                      if (b & 0x8000u) z[e] &= 0xffff0000u;
+                      if (b & 0x80000000u) z[e] &= 0x0000ffffu;
+                    }
+                    *x = y;
+                  }
+                }
+              }
+              if (bad) s_bad[no & 7] = 1;
+            }
+            fence_async_smem();
+          }
+          if (MODE == 2 && p.rows > 128) asm volatile("bar.sync 3, 256;" ::: "memory");
+        }
+        const float mc = m == -INFINITY ? 0.f : m * c;
+        const uint64_t c2 = pair64(c, c), mc2 = pair64(-mc, -mc);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          if (active) {
             uint32_t w[32];
 #pragma unroll
             for (int e = 0; e < 32; e++) {
-              const float p0 = exp2_fast(fmaf(__uint_as_float(s[64 * i + 2 * e]), c, -mc));
-              const float p1 = exp2_fast(fmaf(__uint_as_float(s[64 * i + 2 * e + 1]), c, -mc));
-              sum[(2 * e) & 3] += p0;
-              sum[(2 * e + 1) & 3] += p1;
+              const float2 x = unpair64(fma2(pair64(s[64 * i + 2 * e], s[64 * i + 2 * e + 1]), c2, mc2));
+              const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
+              sum[e & 1] = add2(sum[e & 1], pair64(p0, p1));
               w[e] = pack2<T>(p0, p1);
             }
             tmem_st32(t_s + 32 * i, w);
+            tmem_wait_st();
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_wait_st();
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(b_p + 8 * i);
         }
-        if (masked && (TILES == 1 || stream == 0)) {
-          // Values of keys past the request's end become 0; so do infinities and NaN of
-          // keys that only some rows see: 0 * inf in a product would reach the others.
-          // (rows that do see them get them back below)
-          const uint32_t at = ring + (TILES == 2 ? 2 * t + 1 : n < 2 ? 1 : t == n - 1 ? 2 * n - 1 : 2 + 2 * t);
-          if (!(ok = wait(b_full + 8 * (at % NST), (at / NST) & 1))) break;
-          const int key = k0 + row;
-          if (key >= open) {
-            uint8_t* v = smem + L::Q + (at % NST) * L::STAGE + row * 128;
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < D / 8; i++) {
-              uint4* x = reinterpret_cast<uint4*>(v + (i >> 3) * (AT_KEYS * 128) + (((i & 7) ^ (row & 7)) << 4));
-              if (key >= p.len) {
-                *x = make_uint4(0, 0, 0, 0);
-              } else {
-                uint4 y = *x;
-                uint32_t* z = reinterpret_cast<uint32_t*>(&y);
-                const uint32_t any = nonfinite2<T>(z[0]) | nonfinite2<T>(z[1]) | nonfinite2<T>(z[2]) | nonfinite2<T>(z[3]);
-                if (any) {
-                  bad = true;
-#pragma unroll
-                  for (int e = 0; e < 4; e++) {
-                    const uint32_t b = nonfinite2<T>(z[e]);
-                    if (b & 0x8000u) z[e] &= 0xffff0000u;
-                    if (b & 0x80000000u) z[e] &= 0x0000ffffu;
-                  }
-                  *x = y;
-                }
-              }
-            }
-            if (bad) s_bad[units & 1] = 1;
-          }
-          fence_async_smem();
-        }
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(b_p + 8 * stream);
+        const float2 l2 = unpair64(add2(sum[0], sum[1]));
+        l += l2.x + l2.y;
       }
-      ring += 2 * n;
-      if (!ok || !(ok = wait(b_o, units & 1))) break;
+      if (!ok) break;
+      if (more && !(MODE == 2 && s_piece[taken % AT_PIECES].rows <= skip)) fetched();
+      if (!(ok = wait(b_o, units & 1))) break;
       tmem_fence_after();
-      if (sid == 0) s_bad[(units + 1) & 1] = 0;  // read by all in the unit before, written from the next on
 
       const bool whole = p.pieces == 1;
-      float f0 = 1.f, f1 = 0.f;
-      int d0 = 0, d1 = D;
-      if (TILES == 1) {
-        // both streams' rows: 2^(c m) l each, O in their own columns; a stream writes half of the columns
-        s_ml[stream * 128 + row] = make_float2(m, l);
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        const float2 x = s_ml[row], y = s_ml[128 + row];
-        m = fmaxf(x.x, y.x);
-        f0 = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : exp2_fast((x.x - m) * c);
-        f1 = y.x == -INFINITY ? (y.y == 0.f ? 0.f : 1.f) : exp2_fast((y.x - m) * c);
-        l = x.y * f0 + (n > 1 ? y.y * f1 : 0.f);
-        d0 = stream * (D / 2);
-        d1 = d0 + D / 2;
-      }
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * c) + log2f(l);
-      const bool bad = s_bad[units & 1] != 0;
-      float* part = part_at<D, ROWS>(a, blockIdx.x, p.lo == 0);
+      const bool bad = s_bad[no & 7] != 0;
+      float* part = part_at<D>(a.part, me, p.lo == 0);
       const int64_t o_at = (int64_t)(p.t0 + tok) * a.hq + p.h * a.group + (gr - tok * a.group);
-      if (active && !idle) {
-        for (int d = d0; d < d1; d += 32) {
+      if (active) {
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
           uint32_t x[32];
-          tmem_ld32(x, t_o + (TILES == 2 ? stream * 128 : 0) + d);
+          tmem_ld32(x, t_o + d);
           tmem_wait_ld();
-          float o[32];
-#pragma unroll
-          for (int e = 0; e < 32; e++) o[e] = l == 0.f ? 0.f : __uint_as_float(x[e]) * f0;
-          if (TILES == 1 && n > 1) {
-            tmem_ld32(x, t_o + 128 + d);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; e++) o[e] = l == 0.f ? 0.f : fmaf(__uint_as_float(x[e]), f1, o[e]);
-          }
           if (live) {
+            float o[32];
 #pragma unroll
-            for (int e = 0; e < 32; e++) o[e] *= inv;
+            for (int e = 0; e < 32; e++) o[e] = l == 0.f ? 0.f : __uint_as_float(x[e]) * inv;
             if (bad) {
               // the values taken out above, for the rows that see them: any weight makes them infinite or NaN
               const int from = max(open, p.lo * AT_KEYS), to = min(p.len, p.hi * AT_KEYS);
@@ -680,7 +687,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
                 if (!seen.has(j)) continue;
                 const int64_t id = a.table[(int64_t)p.r * a.table_stride + (j >> a.log2_bs)];
                 if (id < 0 || id >= a.n_blocks) continue;
-                const T* v = reinterpret_cast<const T*>(a.v) + id * a.s_block + p.h * a.s_head +
+                const T* v = static_cast<const T*>(a.v) + id * a.s_block + p.h * a.s_head +
                              (j & ((1 << a.log2_bs) - 1)) * a.s_token + d;
 #pragma unroll
                 for (int e = 0; e < 32; e++) {
@@ -693,62 +700,93 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
               T* dst = static_cast<T*>(a.out) + o_at * D + d;
 #pragma unroll
               for (int e = 0; e < 4; e++)
-                *reinterpret_cast<uint4*>(dst + 8 * e) = make_uint4(pack2<T>(o[8 * e], o[8 * e + 1]), pack2<T>(o[8 * e + 2], o[8 * e + 3]),
-                                                                    pack2<T>(o[8 * e + 4], o[8 * e + 5]), pack2<T>(o[8 * e + 6], o[8 * e + 7]));
+                *reinterpret_cast<uint4*>(dst + 8 * e) =
+                    make_uint4(pack2<T>(o[8 * e], o[8 * e + 1]), pack2<T>(o[8 * e + 2], o[8 * e + 3]),
+                               pack2<T>(o[8 * e + 4], o[8 * e + 5]), pack2<T>(o[8 * e + 6], o[8 * e + 7]));
             } else {
-              float4* dst = reinterpret_cast<float4*>(part + (int64_t)my * D + d);
+              float4* dst = reinterpret_cast<float4*>(part) + (d / 4) * 128 + row;
 #pragma unroll
-              for (int e = 0; e < 8; e++) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              for (int e = 0; e < 8; e++) __stcg(dst + e * 128, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
             }
           }
           __syncwarp();
         }
-        if (live && (TILES == 2 || stream == 0)) {
-          if (!whole) part[ROWS * D + my] = lse2;
+        if (live) {
+          const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * c) + log2f(l);
+          if (!whole) __stcg(part + 128 * D + row, lse2);
           else if (a.lse) a.lse[o_at] = lse2 * 0.69314718055994531f;
         }
       }
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(b_free);
+      // two pieces ahead; streams that share it are at most AT_PIECES apart
+      if (row == 0 && (MODE != 2 || stream == 0)) s_bad[(no + 2) & 7] = 0;
       if (!whole) {
-        // the CTA that finishes a divided unit last joins its pieces, always in their order on the line
         __threadfence();
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        const int np = p.pieces, first = p.first;
-        if (sid == 0) {
-          const unsigned done = atomicAdd(a.counters + first, 1u);
-          *s_last = done == (unsigned)np - 1;
-          if (done == (unsigned)np - 1) a.counters[first] = 0;
-          __threadfence();
-        }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (*s_last) {
-          for (int i = sid; i < rows * (D / 4); i += 256) {
-            const int rr = i / (D / 4), ch = i % (D / 4);
-            float top = -INFINITY;
-            for (int k = 0; k < np; k++) top = fmaxf(top, __ldcg(part_at<D, ROWS>(a, first + k, k == 0) + ROWS * D + rr));
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            float w = 0.f;
-            for (int k = 0; k < np; k++) {
-              const float* src = part_at<D, ROWS>(a, first + k, k == 0);
-              const float e = __ldcg(src + ROWS * D + rr);
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)rr * D) + ch);
-              if (e == -INFINITY) continue;
-              const float f = exp2_fast(e - top);
-              w += f;
-              o.x = fmaf(f, x.x, o.x);
-              o.y = fmaf(f, x.y, o.y);
-              o.z = fmaf(f, x.z, o.z);
-              o.w = fmaf(f, x.w, o.w);
-            }
-            const float wi = w == 0.f ? 0.f : 1.f / w;
-            const int g = row0 + rr, tk = g / a.group;
-            const int64_t to = (int64_t)(p.t0 + tk) * a.hq + p.h * a.group + (g - tk * a.group);
-            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + to * D + ch * 4) =
-                make_uint2(pack2<T>(o.x * wi, o.y * wi), pack2<T>(o.z * wi, o.w * wi));
-            if (a.lse && ch == 0) a.lse[to] = w == 0.f ? -INFINITY : (top + log2f(w)) * 0.69314718055994531f;
-          }
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + stream) : "memory");
+        const int key = MODE == 2 ? p.first * 2 + stream : p.first;
+        if (row == 0) atomicAdd(a.counters + 2 * key, 1u);
+        if (joins < 2) {
+          join_first[joins] = key;
+          join_pieces[joins] = p.pieces;
+          join_rows[joins] = rows;
+          join_g[joins] = p.row0 + skip;
+          join_out[joins] = (int64_t)p.t0 * a.hq + p.h * a.group;
+          joins++;
         }
       }
       units++;
+    }
+    // The streams that a unit is divided over join it together, each some of its
+    // rows, the pieces always in their order on the line.  They wait for one another:
+    // the launch is cooperative, so all are resident, and each ends its pieces first.
+    for (int k = 0; k < joins && ok; k++) {
+      constexpr int STEP = MODE == 2 ? 2 : 1;  // from one piece's stream to the next one's
+      const int key = join_first[k], np = join_pieces[k], mine = (me - key) / STEP;
+      if (row == 0) {
+        const volatile unsigned* done = a.counters + 2 * key;
+        for (uint32_t i = 0; *done < (unsigned)np && !*abort; i++) {
+          if (i > 1u << 24) *abort = 1;
+          __nanosleep(20);
+        }
+        __threadfence();
+      }
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + stream) : "memory");
+      if (*abort) break;
+      const int each = (join_rows[k] + np - 1) / np, from = mine * each, n = max(0, min(join_rows[k] - from, each));
+      for (int i = row; i < n * (D / 4); i += 128) {
+        const int rr = from + i % n, ch = i / n;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < np; j++) top = fmaxf(top, __ldcg(part_at<D>(a.part, key + j * STEP, j == 0) + 128 * D + rr));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int j = 0; j < np; j++) {
+          const float* src = part_at<D>(a.part, key + j * STEP, j == 0);
+          const float e = __ldcg(src + 128 * D + rr);
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src) + ch * 128 + rr);
+          if (e != -INFINITY) {  // a piece without weight may hold anything
+            const float w = exp2_fast(e - top);
+            sum += w;
+            o.x = fmaf(w, x.x, o.x);
+            o.y = fmaf(w, x.y, o.y);
+            o.z = fmaf(w, x.z, o.z);
+            o.w = fmaf(w, x.w, o.w);
+          }
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int g = join_g[k] + rr, tk = g / a.group;
+        const int64_t to = join_out[k] + (int64_t)tk * a.hq + (g - tk * a.group);
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + to * D + ch * 4) =
+            make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+        if (a.lse && ch == 0) a.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+      }
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + stream) : "memory");
+      if (row == 0 && atomicAdd(a.counters + 2 * key + 1, 1u) == (unsigned)np - 1) {
+        a.counters[2 * key] = 0;  // all have seen it
+        a.counters[2 * key + 1] = 0;
+      }
     }
   }
   if (*abort && lane == 0 && atomicCAS(&a.status->code, 0, TK_E_TIMEOUT) == 0) a.status->request = -1;
@@ -756,28 +794,37 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
   __syncthreads();
   if (warp == 1) {
     tmem_fence_after();
-    tmem_free(tmem);
+    tmem_free(0);
   }
 }
 
-template <class T, int D, int TILES>
+template <class T, int D, int MODE>
 static cudaError_t attend_launch(const AttendArgs& a, const tk_kv_cache* cache, int grid, cudaStream_t st) {
-  constexpr int bytes = AttendSmem<D, TILES>::TOTAL;
+  constexpr int bytes = AttendShape<D, MODE>::TOTAL;
   static bool set[64];  // by device
   if (cache->device >= 64 || !set[cache->device]) {
-    const cudaError_t e = cudaFuncSetAttribute(k_kv_attend<T, D, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = cudaFuncSetAttribute(k_kv_attend<T, D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     if (cache->device < 64) set[cache->device] = true;
   }
-  k_kv_attend<T, D, TILES><<<grid, AT_THREADS, bytes, st>>>(a, cache->map_k, cache->map_v);
-  return cudaGetLastError();
+  cudaLaunchAttribute coop;
+  coop.id = cudaLaunchAttributeCooperative;
+  coop.val.cooperative = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(AT_THREADS);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cfg.attrs = &coop;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_kv_attend<T, D, MODE>, a, cache->map_k, cache->map_v);
 }
 
-template <class T>
-static cudaError_t attend_pick(const AttendArgs& a, const tk_kv_cache* cache, bool two, int grid, cudaStream_t st) {
-  if (cache->head_dim == 64)
-    return two ? attend_launch<T, 64, 2>(a, cache, grid, st) : attend_launch<T, 64, 1>(a, cache, grid, st);
-  return two ? attend_launch<T, 128, 2>(a, cache, grid, st) : attend_launch<T, 128, 1>(a, cache, grid, st);
+template <class T, int D>
+static cudaError_t attend_pick(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, int grid, cudaStream_t st) {
+  if (rows <= 32) return attend_launch<T, D, 0>(a, cache, grid, st);
+  if (rows <= 128) return attend_launch<T, D, 1>(a, cache, grid, st);
+  return attend_launch<T, D, 2>(a, cache, grid, st);
 }
 
 }  // namespace tk
@@ -799,8 +846,9 @@ extern "C" int tk_kv_workspace_create(tk_kv_workspace** out) {
   }
   cudaError_t e = cudaGetDevice(&ws->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&ws->sms, cudaDevAttrMultiProcessorCount, ws->device);
-  // one block: the partial outputs of two pieces of every CTA, its counter, the status
-  const size_t part = sizeof(float) * 2 * 256 * (128 + 1) * (size_t)ws->sms, counters = sizeof(unsigned) * (size_t)ws->sms;
+  // one allocation: the partial outputs of two pieces of every stream, its counters, the status
+  const size_t part = sizeof(float) * 2 * 2 * 128 * (128 + 1) * (size_t)ws->sms,
+               counters = sizeof(unsigned) * 2 * 2 * (size_t)ws->sms;
   uint8_t* mem = nullptr;
   if (e == cudaSuccess) e = cudaMalloc(&mem, part + counters + 64 + sizeof(KvStatus));
   if (e == cudaSuccess) {
@@ -834,7 +882,7 @@ extern "C" int tk_kv_status(tk_kv_workspace* ws, int64_t* h_request, void* cuda_
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e == cudaSuccess && s.code) e = cudaMemsetAsync(ws->status, 0, sizeof(s), st);
   // a call that gave up may have left counts behind
-  if (e == cudaSuccess && s.code == TK_E_TIMEOUT) e = cudaMemsetAsync(ws->counters, 0, sizeof(unsigned) * ws->sms, st);
+  if (e == cudaSuccess && s.code == TK_E_TIMEOUT) e = cudaMemsetAsync(ws->counters, 0, sizeof(unsigned) * 4 * ws->sms, st);
   if (e != cudaSuccess) {
     tk_set_error("tk_kv_status: %s", cudaGetErrorString(e));
     return TK_E_CUDA;
@@ -867,16 +915,20 @@ extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const
   if (T == 0 || R == 0) return TK_OK;
   if (!d_q || !d_off || !d_len || !d_out || (table_width > 0 && !d_table)) return attend_arg(where, "null pointer");
   if ((((uintptr_t)d_q | (uintptr_t)d_out) & 15) != 0) return attend_arg(where, "a buffer is not 16-byte aligned");
-  // a request's rows for one key head fill one row tile, or two and more
   const int group = n_q_heads / cache->n_heads;
-  const bool two = std::min(max_new, T) * group > 128;
   AttendArgs a = {d_q, q_stride, n_q_heads, cache->n_heads, group, d_off, R, T, max_new, d_len, d_table, table_stride,
                   table_width, d_mask, scale * 1.4426950408889634f, d_out, d_lse, ws->status,
-                  static_cast<const uint8_t*>(cache->v), cache->n_blocks, cache->stride[0], cache->stride[1],
+                  cache->v, cache->n_blocks, cache->stride[0], cache->stride[1],
                   cache->stride[2], cache->log2_block, ws->part, ws->counters};
   cudaStream_t st = (cudaStream_t)cuda_stream;
-  const cudaError_t e = cache->type == TK_BF16 ? attend_pick<__nv_bfloat16>(a, cache, two, ws->sms, st)
-                                               : attend_pick<__half>(a, cache, two, ws->sms, st);
+  const int64_t rows = std::min(max_new, T) * group;  // of a request and key head
+  cudaError_t e;
+  if (cache->type == TK_BF16)
+    e = cache->head_dim == 64 ? attend_pick<__nv_bfloat16, 64>(a, cache, rows, ws->sms, st)
+                              : attend_pick<__nv_bfloat16, 128>(a, cache, rows, ws->sms, st);
+  else
+    e = cache->head_dim == 64 ? attend_pick<__half, 64>(a, cache, rows, ws->sms, st)
+                              : attend_pick<__half, 128>(a, cache, rows, ws->sms, st);
   if (e != cudaSuccess) {
     tk_set_error("%s: %s", where, cudaGetErrorString(e));
     return TK_E_CUDA;
