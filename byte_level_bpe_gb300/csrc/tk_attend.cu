@@ -4,10 +4,10 @@
 //
 // The query rows of one request and key head (tokens x query heads of that key
 // head) are the rows of the products S = Q K^T and O = P V on the 5th-generation
-// tensor cores; 128 rows are one tile whether they are all in use or not: a
-// tile's two products take about 1,000 cycles against the 2,850 that its
+// tensor cores; 128 rows are one tile whether they are all in use or not: for 128
+// keys the two products take about 1,300 cycles against the 2,850 that their
 // 64 KB of keys and values take from HBM (head_dim 128), so padding costs nothing while
-// memory is the bound.  Keys come in tiles of 128.  With a running maximum m and sum l,
+// memory is the bound.  Keys come in tiles of 64.  With a running maximum m and sum l,
 //   p_j = 2^(c (s_j - m)), c = scale log2(e),  l += sum p_j,  O += P V,
 // and O is rescaled in tensor memory only when m grows by more than 2^8 in p
 // (p and l are relative to the same m, so the quotient is exact either way).
@@ -21,11 +21,11 @@
 
 namespace tk {
 
-constexpr int AT_KEYS = 128;     // keys of a tile
+constexpr int AT_KEYS = 64;      // keys of a tile
 constexpr int AT_THREADS = 384;  // loads and products of two streams (4 warps), their softmax (2 x 4 warps)
-constexpr int AT_UNIT_COST = 1;  // what starting a unit costs, in tiles
-constexpr int AT_MIN_SHARE = 4;  // least share of a worker, in tiles
-constexpr int AT_SNAP = 2;       // a unit is not cut nearer to its ends than this, in tiles
+constexpr int AT_UNIT_COST = 2;  // what starting a unit costs, in tiles
+constexpr int AT_MIN_SHARE = 8;  // least share of a worker, in tiles
+constexpr int AT_SNAP = 4;       // a unit is not cut nearer to its ends than this, in tiles
 
 struct AttendArgs {
   const void* q;
@@ -217,11 +217,11 @@ struct AttendShape {
   static constexpr int RINGS = MODE == 2 ? 1 : 2, ROWS = MODE == 0 ? 32 : MODE == 1 ? 128 : 256;
   static constexpr int Q_ROWS = MODE == 0 ? 32 : 128;  // of a stream
   static constexpr int Q = Q_ROWS * D * 2, STAGE = AT_KEYS * D * 2;
-  static constexpr int STAGES = D == 64 ? (MODE == 2 ? 12 : 6) : MODE == 0 ? 3 : MODE == 1 ? 2 : 5;  // of a ring
+  static constexpr int STAGES = (RINGS == 1 ? 160 : MODE == 0 ? 96 : 80) * 1024 / STAGE;  // of a ring
   static constexpr int RING = 2 * Q;
-  // barriers: full and empty of the stages; pieces handed over and taken; per stream q, s, p (2), o ready, o free; drain (2)
+  // barriers: full and empty of the stages; pieces handed over and taken; per stream q, s (2), p (2), v, o ready, o free, drain
   static constexpr int BARS = RING + RINGS * STAGES * STAGE;
-  static constexpr int N_BARS = RINGS * (2 * STAGES + 2 * AT_PIECES) + 2 * 6 + 2;
+  static constexpr int N_BARS = RINGS * (2 * STAGES + 2 * AT_PIECES) + 2 * 9;
   static constexpr int PIECES = BARS + 8 * N_BARS;
   static constexpr int SMALL = PIECES + RINGS * AT_PIECES * (int)sizeof(Piece);
   // start of the walk (2 x 2 x 8), sums of the warps, tensor memory, abort, non-finite values (2 x 8)
@@ -238,9 +238,12 @@ __device__ __forceinline__ float* part_at(float* part, int stream, int slot) {
 }
 
 // Warps 0 and 3 load (one per ring), warps 1 and 2 issue the products of streams
-// 0 and 1, warps 4-7 and 8-11 are their softmax, a thread per row.  Tensor memory:
-// S at 0 and 128 (P over the first half of it), O at 256 and 384.  While one stream
-// is in its softmax the other's products run.
+// 0 and 1, warps 4-7 and 8-11 are their softmax, a thread per row.  Tensor memory of a
+// stream: two tiles' scores (64 columns each, the weights over the first half of
+// them) and O (128), 256 columns from 256 * stream.  With two of them the products of
+// the next tile run under the softmax of this one: 128-key tiles, for which there is
+// only one, took 1.7 times as long.  (64-key scores read Q twice as often from
+// shared memory, 96 instead of 64 cycles for 128 keys and k = 16.)
 template <class T, int D, int MODE>
 __global__ void __launch_bounds__(AT_THREADS, 1)
 k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
@@ -255,8 +258,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
   const uint32_t s_ring = base + L::RING + ring * (NST * L::STAGE), s_q = base + stream * L::Q;
   const uint32_t b_full = base + L::BARS + ring * 8 * (2 * NST + 2 * AT_PIECES), b_empty = b_full + 8 * NST,
                  b_piece = b_empty + 8 * NST, b_taken = b_piece + 8 * AT_PIECES;
-  const uint32_t b_q = base + L::BARS + L::RINGS * 8 * (2 * NST + 2 * AT_PIECES) + stream * 56, b_s = b_q + 8, b_p = b_s + 8,
-                 b_o = b_p + 16, b_free = b_o + 8, b_drain = b_free + 8;
+  const uint32_t b_q = base + L::BARS + L::RINGS * 8 * (2 * NST + 2 * AT_PIECES) + stream * 72, b_s = b_q + 8, b_p = b_s + 16,
+                 b_v = b_p + 16, b_o = b_v + 8, b_free = b_o + 8, b_drain = b_free + 8;
   Piece* s_piece = reinterpret_cast<Piece*>(smem + L::PIECES) + ring * AT_PIECES;
   int64_t* s_walk = reinterpret_cast<int64_t*>(smem + L::SMALL);  // of each worker: first request, where it starts
   int64_t* s_sum = s_walk + 4;
@@ -276,14 +279,18 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         if (in >= NST && in < 2 * NST) count = MODE == 2 ? 2 : 1;                // empty: the streams that read the stage
         else if (in >= 2 * NST + AT_PIECES) count = MODE == 2 ? 10 : 5;          // taken: products and softmax warps
       } else {
-        const int k = st % 7;
-        count = k == 0 ? 128 : k == 2 || k == 3 || k == 5 ? 4 : 1;               // q, p, p, o free
+        const int k = st % 9;
+        count = k == 0 ? 128 : k == 3 || k == 4 || k == 7 ? 4 : 1;               // q, p, p, o free
       }
       bar_init(base + L::BARS + 8 * i, count);
     }
     fence_bar_init();
   }
   if (tid < 17) s_int[1 + tid] = 0;
+  if (tid == 0 || tid == 96) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k));
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v));
+  }
   if (warp == 1) tmem_alloc(smem_addr(const_cast<int*>(s_int)));
 
   // where the workers start: the requests' costs added up, each thread a run of them
@@ -337,9 +344,9 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
 
   // the pieces, for the roles that follow the loads
   uint32_t taken = 0;
-  auto coming = [&]() {  // waits for the next one; false when there is none
-    if (!__all_sync(0xffffffffu, bar_wait(b_piece + 8 * (taken % AT_PIECES), (taken / AT_PIECES) & 1, abort))) return false;
-    return s_piece[taken % AT_PIECES].valid != 0;
+  auto coming = [&](uint32_t i) {  // waits for piece i; false when there is none
+    if (!__all_sync(0xffffffffu, bar_wait(b_piece + 8 * (i % AT_PIECES), (i / AT_PIECES) & 1, abort))) return false;
+    return s_piece[i % AT_PIECES].valid != 0;
   };
   auto release = [&]() {
     __syncwarp();
@@ -347,11 +354,9 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     taken++;
   };
 
-  // registers: 384 x 168 at launch = 128 x 72 + 256 x 216
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0 || (warp == 3 && MODE != 2)) {
-      // ---- loads, in the order of their use: K0 V0 K1 V1 ...
+      // ---- loads, in the order of their use: K0 K1 V0 K2 V1 K3 ...
       Walk<ROWS> walk;
       walk.share = share;
       walk.from = (blockIdx.x * WORKERS + ring) * share;
@@ -371,41 +376,51 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         __syncwarp();
         at++;
       };
-      const int ppt = AT_KEYS >> a.log2_bs;  // pages of a tile
+      // a box is 64 elements of one page, or of half of one of 128
+      const int log2_box = min(a.log2_bs, 6), ppt = AT_KEYS >> log2_box;
       Piece nx;
       walk.next(a, nx);
       hand(nx);
       while (ok && nx.valid) {
-        const int r = nx.r, h = nx.h, lo = nx.lo, n = nx.hi - nx.lo, pages = (nx.keys + (1 << a.log2_bs) - 1) >> a.log2_bs;
-        // the next piece is known to the softmax before this one's loads wait for it
-        walk.next(a, nx);
-        hand(nx);
-        // lanes hold the ids of 32 pages, and of the next 32
+        const int r = nx.r, h = nx.h, lo = nx.lo, n = nx.hi - nx.lo;
+        const int boxes = (nx.keys + (1 << log2_box) - 1) >> log2_box, per_page = a.log2_bs - log2_box;
+        // lanes hold the block ids of 32 boxes, and of the next 32
         const int32_t* row = a.table + (int64_t)r * a.table_stride;
-        int window = (lo * ppt) & ~31;
-        int ids = window + lane < pages ? row[window + lane] : 0, ids2 = window + 32 + lane < pages ? row[window + 32 + lane] : 0;
-        for (int t = lo; ok && t < lo + n; t++) {
-          const int page0 = t * ppt;
-          if (page0 >= window + 32) {
-            window += 32;
-            ids = ids2;
-            ids2 = window + 32 + lane < pages ? row[window + 32 + lane] : 0;
+        auto id_of = [&](int b) { return b < boxes ? row[b >> per_page] : 0; };
+        int win_k = (lo * ppt) & ~31, win_v = win_k;
+        int ids_k = id_of(win_k + lane), nxt_k = id_of(win_k + 32 + lane), ids_v = ids_k, nxt_v = nxt_k;
+        for (int i = 0; ok && i < 2 * n; i++, pos++) {
+          const int lead = min(n, 2);
+          const bool value = i >= lead && (i == 2 * n - 1 || ((i - lead) & 1) == 0);
+          const int t = i < lead ? i : i == 2 * n - 1 ? n - 1 : value ? (i - lead) >> 1 : ((i - lead) >> 1) + 2;
+          const int box0 = (lo + t) * ppt;
+          if (value && box0 >= win_v + 32) {
+            win_v += 32;
+            ids_v = nxt_v;
+            nxt_v = id_of(win_v + 32 + lane);
+          } else if (!value && box0 >= win_k + 32) {
+            win_k += 32;
+            ids_k = nxt_k;
+            nxt_k = id_of(win_k + 32 + lane);
           }
-          const int np = max(0, min(ppt, pages - page0));
-          const int id = __shfl_sync(0xffffffffu, ids, (page0 + lane) & 31);
+          const int nb = max(0, min(ppt, boxes - box0));
+          const int id = __shfl_sync(0xffffffffu, value ? ids_v : ids_k, (box0 + lane) & 31);
+          const uint32_t st = pos % NST, dst = s_ring + st * L::STAGE;
+          ok = pos < NST || bar_wait(b_empty + 8 * st, (pos / NST + 1) & 1, abort);
+          if (!(ok = __all_sync(0xffffffffu, ok) != 0)) break;
+          if (lane == 0) bar_expect(b_full + 8 * st, (uint32_t)nb * (HALVES * 128u << log2_box));
+          __syncwarp();
+          if (lane < nb) {
 #pragma unroll
-          for (int kv = 0; kv < 2; kv++, pos++) {
-            const uint32_t st = pos % NST, dst = s_ring + st * L::STAGE;
-            ok = pos < NST || bar_wait(b_empty + 8 * st, (pos / NST + 1) & 1, abort);
-            if (!(ok = __all_sync(0xffffffffu, ok) != 0)) break;
-            if (lane == 0) bar_expect(b_full + 8 * st, (uint32_t)np * (HALVES * 128u << a.log2_bs));
-            __syncwarp();
-            if (lane < np) {
-#pragma unroll
-              for (int s = 0; s < HALVES; s++)  // a box: one page, 64 elements
-                tma_load_4d(dst + s * (AT_KEYS * 128) + (lane * 128 << a.log2_bs), kv ? &map_v : &map_k, b_full + 8 * st, s * 64,
-                            0, h, id);
-            }
+            for (int s = 0; s < HALVES; s++)
+              tma_load_4d(dst + s * (AT_KEYS * 128) + (lane * 128 << log2_box), value ? &map_v : &map_k, b_full + 8 * st, s * 64,
+                          per_page ? (box0 & 1) * AT_KEYS : 0, h, id);
+          }
+          // the next piece is known to the softmax, which asks for it in its last tile, before
+          // more loads wait for it
+          if (i == 1) {
+            walk.next(a, nx);
+            hand(nx);
           }
         }
       }
@@ -425,20 +440,20 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         return r;
       };
       auto full = [&]() { return wait(b_full + 8 * (pos % NST), (pos / NST) & 1); };
-      auto scores = [&]() {  // S = Q K^T
+      auto scores = [&](uint32_t buf) {  // S = Q K^T
         const uint32_t k = mma_desc(s_ring + (pos % NST) * L::STAGE, 16), q = mma_desc(s_q, 16);
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < D / 16; i++)
-            mma_ss(stream * 128, q + (((i >> 2) * (L::Q_ROWS * 128) + (i & 3) * 32) >> 4),
+            mma_ss(stream * 256 + buf * 64, q + (((i >> 2) * (L::Q_ROWS * 128) + (i & 3) * 32) >> 4),
                    k + (((i >> 2) * (AT_KEYS * 128) + (i & 3) * 32) >> 4), KIND_S, i > 0);
-          mma_commit(b_s);
+          mma_commit(b_s + 8 * buf);
           mma_commit(b_empty + 8 * (pos % NST));
         }
         __syncwarp();
         pos++;
       };
-      while (ok && coming()) {
+      while (ok && coming(taken)) {
         const Piece& p = s_piece[taken % AT_PIECES];
         const int n = __shfl_sync(0xffffffffu, p.hi - p.lo, 0), rows = __shfl_sync(0xffffffffu, p.rows, 0);
         release();
@@ -450,29 +465,29 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           continue;
         }
         if (!(ok = wait(b_q, units & 1) && full())) break;
-        scores();
-        for (int t = 0; t < n; t++) {
+        scores(nt & 1);
+        if (n > 1) {
+          if (!(ok = full())) break;
+          scores((nt + 1) & 1);
+        }
+        for (int t = 0; t < n; t++, nt++) {
+          // O += P V; the first of a unit when the last one's output has been read
           if (!(ok = full() && (t > 0 || units == 0 || wait(b_free, (units + 1) & 1)))) break;
-          // O += P V, the first keys as soon as their weights are there
-          const uint32_t v = mma_desc(s_ring + (pos % NST) * L::STAGE, AT_KEYS * 128);
+          if (!(ok = wait(b_p + 8 * (nt & 1), (nt >> 1) & 1))) break;
+          const uint32_t v = mma_desc(s_ring + (pos % NST) * L::STAGE, AT_KEYS * 128), buf = nt & 1;
+          if (elect_one()) {
 #pragma unroll
-          for (int half = 0; half < 2; half++) {
-            if (!(ok = wait(b_p + 8 * half, nt & 1))) break;
-            if (elect_one()) {
-#pragma unroll
-              for (int i = half * (AT_KEYS / 32); i < (half + 1) * (AT_KEYS / 32); i++)
-                mma_ts(256 + stream * 128, stream * 128 + i * 8, v + i * (2048 >> 4), KIND_O, t > 0 || i > 0);
-              if (half) mma_commit(b_empty + 8 * (pos % NST));
-              if (half && t == n - 1) mma_commit(b_o);
-            }
-            __syncwarp();
+            for (int i = 0; i < AT_KEYS / 16; i++)
+              mma_ts(stream * 256 + 128, stream * 256 + buf * 64 + i * 8, v + i * (2048 >> 4), KIND_O, t > 0 || i > 0);
+            mma_commit(b_v);
+            mma_commit(b_empty + 8 * (pos % NST));
+            if (t == n - 1) mma_commit(b_o);
           }
-          if (!ok) break;
-          nt++;
+          __syncwarp();
           pos++;
-          if (t + 1 < n) {
+          if (t + 2 < n) {
             if (!(ok = full())) break;
-            scores();
+            scores(buf);
           }
         }
         units++;
@@ -486,24 +501,24 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    // ---- softmax: a thread has one row
+    // ---- softmax
     const int wq = warp & 3, row = wq * 32 + lane;  // row = also its lane of tensor memory
-    const uint32_t t_s = ((uint32_t)(wq * 32) << 16) + stream * 128, t_o = t_s + 256;
+    const uint32_t t_s = ((uint32_t)(wq * 32) << 16) + stream * 256, t_o = t_s + 128;
     const float c = a.scale_log2;
     const int me = blockIdx.x * 2 + stream;
     uint32_t nt = 0, units = 0, stages = 0;
     bool ok = true;
-    int joins = 0, join_first[2], join_pieces[2], join_rows[2];
-    int64_t join_out[2];
-    int join_g[2];
+    int joins = 0, join_first[2], join_pieces[2], join_rows[2], join_g[2], join_out[2];
     auto wait = [&](uint32_t bar, uint32_t parity) {  // one answer for the warp
       return __all_sync(0xffffffffu, bar_wait(bar, parity, abort)) != 0;
     };
+    auto stream_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + stream) : "memory"); };
+    constexpr int SKIP = MODE == 2 ? 128 : 0;  // rows of a unit before those of the second stream
+    const int skip = stream * SKIP;
     // queries of the next piece, 16 bytes a copy, into 128-byte swizzled rows
-    auto fetch = [&]() {
-      const Piece& x = s_piece[taken % AT_PIECES];
-      const int row0 = x.row0 + (MODE == 2 ? stream * 128 : 0), rows = min(128, x.rows - (MODE == 2 ? stream * 128 : 0));
+    auto fetch = [&](uint32_t pc) {
+      const Piece& x = s_piece[pc % AT_PIECES];
+      const int row0 = x.row0 + skip, rows = min(128, x.rows - skip);
       const T* q = static_cast<const T*>(a.q) + x.t0 * a.q_stride + x.h * a.group * D;
 #pragma unroll 4
       for (int i = row; i < rows * (D / 8); i += 128) {
@@ -518,24 +533,23 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       fence_async_smem();
       bar_arrive(b_q);
     };
-    bool more = coming();
-    if (more && !(MODE == 2 && stream * 128 >= s_piece[taken % AT_PIECES].rows)) {
-      fetch();
+    auto has_rows = [&](uint32_t pc) { return MODE != 2 || s_piece[pc % AT_PIECES].rows > skip; };
+    bool more = coming(0);
+    if (more && has_rows(0)) {
+      fetch(0);
       fetched();
     }
     while (more) {
-      const Piece p = s_piece[taken % AT_PIECES];
-      release();
-      const uint32_t no = taken - 1;
-      const int n = p.hi - p.lo, skip = MODE == 2 ? stream * 128 : 0, rows = min(128, p.rows - skip), open = p.open;
-      const uint32_t v0 = stages + 1;  // stage of the first values
+      const Piece& p = s_piece[taken % AT_PIECES];  // released at the unit's end: registers are short
+      const int n = p.hi - p.lo, rows = min(128, p.rows - skip), open = p.open;
+      const uint32_t ring0 = stages;  // its first stage
       stages += 2 * n;
-      if (MODE == 2 && rows <= 0) {  // nothing for this stream
-        if (!(more = coming())) break;
-        if (s_piece[taken % AT_PIECES].rows > skip) {
-          fetch();
+      if (rows <= 0) {  // nothing for this stream
+        if ((more = coming(taken + 1)) && has_rows(taken + 1)) {
+          fetch(taken + 1);
           fetched();
         }
+        release();
         continue;
       }
       const bool live = row < rows, active = wq * 32 < rows;  // the row's, the warp's
@@ -554,20 +568,17 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       for (int t = 0; t < n; t++, nt++) {
         const int k0 = (p.lo + t) * AT_KEYS;
         const bool masked = k0 + AT_KEYS > open;
-        if (!(ok = wait(b_s, nt & 1))) break;
+        const uint32_t buf = nt & 1;
+        if (!(ok = wait(b_s + 8 * buf, (nt >> 1) & 1))) break;
         tmem_fence_after();
-        if (t == n - 1) {  // the queries have been read for the last time: the next ones come in meanwhile
-          more = coming();
-          if (more && !(MODE == 2 && s_piece[taken % AT_PIECES].rows <= skip)) fetch();
-        }
-        uint32_t s[128];
+        uint32_t s[64];
         if (active) {
-#pragma unroll
-          for (int i = 0; i < 4; i++) tmem_ld32(s + 32 * i, t_s + 32 * i);
+          tmem_ld32(s, t_s + buf * 64);
+          tmem_ld32(s + 32, t_s + buf * 64 + 32);
           tmem_wait_ld();
           if (masked) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < 2; i++) {
               const uint32_t w = seen.bits(k0 + 32 * i);
 #pragma unroll
               for (int e = 0; e < 32; e++)
@@ -578,14 +589,16 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
 #pragma unroll
           for (int i = 0; i < 4; i++) top[i] = fmaxf(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
 #pragma unroll
-          for (int i = 8; i < 128; i += 2)
+          for (int i = 8; i < 64; i += 2)
             top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
           const bool grow = live && mx > m && !((mx - m) * c <= 8.f);
           if (t > 0 && __any_sync(0xffffffffu, grow)) {
-            // the products before S are done: O is ours
+            // the products of the tile before may still run
+            if (!(ok = wait(b_v, (nt + 1) & 1))) break;
+            tmem_fence_after();
             const float f = grow ? exp2_fast((m - mx) * c) : 1.f;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < D / 32; i++) {
               uint32_t o[32];
               tmem_ld32(o, t_o + 32 * i);
@@ -603,22 +616,21 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           // keys that only some rows see: 0 * inf in a product would reach the others.
           // (Rows that do see them get them back below.)  Streams that share a tile leave it to the first.
           if (MODE != 2 || stream == 0) {
-            const uint32_t at = v0 + 2 * t;
+            const uint32_t at = ring0 + (n == 1 ? 1 : t == n - 1 ? 2 * n - 1 : 2 * t + 2);
             if (!(ok = wait(b_full + 8 * (at % NST), (at / NST) & 1))) break;
-            const int key = k0 + row;
+            const int kr = row & 63, half = row >> 6, key = k0 + kr;  // a thread has half a row
             if (key >= open) {
-              uint8_t* v = smem + (s_ring - base) + (at % NST) * L::STAGE + row * 128;
+              uint8_t* v = smem + (s_ring - base) + (at % NST) * L::STAGE + kr * 128;
               bool bad = false;
-#pragma unroll
-              for (int i = 0; i < D / 8; i++) {
-                uint4* x = reinterpret_cast<uint4*>(v + (i >> 3) * (AT_KEYS * 128) + (((i & 7) ^ (row & 7)) << 4));
+#pragma unroll 4
+              for (int i = half * (D / 16); i < (half + 1) * (D / 16); i++) {
+                uint4* x = reinterpret_cast<uint4*>(v + (i >> 3) * (AT_KEYS * 128) + (((i & 7) ^ (kr & 7)) << 4));
                 if (key >= p.len) {
                   *x = make_uint4(0, 0, 0, 0);
                 } else {
                   uint4 y = *x;
                   uint32_t* z = reinterpret_cast<uint32_t*>(&y);
-                  const uint32_t any = nonfinite2<T>(z[0]) | nonfinite2<T>(z[1]) | nonfinite2<T>(z[2]) | nonfinite2<T>(z[3]);
-                  if (any) {
+                  if (nonfinite2<T>(z[0]) | nonfinite2<T>(z[1]) | nonfinite2<T>(z[2]) | nonfinite2<T>(z[3])) {
                     bad = true;
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
@@ -630,47 +642,49 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
                   }
                 }
               }
-              if (bad) s_bad[no & 7] = 1;
+              if (bad) s_bad[taken & 7] = 1;
             }
             fence_async_smem();
           }
           if (MODE == 2 && p.rows > 128) asm volatile("bar.sync 3, 256;" ::: "memory");
         }
-        const float mc = m == -INFINITY ? 0.f : m * c;
-        const uint64_t c2 = pair64(c, c), mc2 = pair64(-mc, -mc);
-        uint64_t sum[2] = {0, 0};
+        if (active) {
+          const float mc = m == -INFINITY ? 0.f : m * c;
+          const uint64_t c2 = pair64(c, c), mc2 = pair64(-mc, -mc);
+          uint64_t sum[2] = {0, 0};
+          uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-          if (active) {
-            uint32_t w[32];
-#pragma unroll
-            for (int e = 0; e < 32; e++) {
-              const float2 x = unpair64(fma2(pair64(s[64 * i + 2 * e], s[64 * i + 2 * e + 1]), c2, mc2));
-              const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
-              sum[e & 1] = add2(sum[e & 1], pair64(p0, p1));
-              w[e] = pack2<T>(p0, p1);
-            }
-            tmem_st32(t_s + 32 * i, w);
-            tmem_wait_st();
+          for (int e = 0; e < 32; e++) {
+            const float2 x = unpair64(fma2(pair64(s[2 * e], s[2 * e + 1]), c2, mc2));
+            const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
+            sum[e & 1] = add2(sum[e & 1], pair64(p0, p1));
+            w[e] = pack2<T>(p0, p1);
           }
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(b_p + 8 * i);
+          tmem_st32(t_s + buf * 64, w);
+          const float2 l2 = unpair64(add2(sum[0], sum[1]));
+          l += l2.x + l2.y;
+          tmem_wait_st();
         }
-        const float2 l2 = unpair64(add2(sum[0], sum[1]));
-        l += l2.x + l2.y;
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(b_p + 8 * buf);
+        if (t == n - 1) {  // the queries have been read for the last time
+          more = coming(taken + 1);
+          if (more && has_rows(taken + 1)) {
+            fetch(taken + 1);
+            fetched();
+          }
+        }
       }
-      if (!ok) break;
-      if (more && !(MODE == 2 && s_piece[taken % AT_PIECES].rows <= skip)) fetched();
-      if (!(ok = wait(b_o, units & 1))) break;
+      if (!ok || !(ok = wait(b_o, units & 1))) break;
       tmem_fence_after();
 
       const bool whole = p.pieces == 1;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const bool bad = s_bad[no & 7] != 0;
+      const bool bad = s_bad[taken & 7] != 0;
       float* part = part_at<D>(a.part, me, p.lo == 0);
       const int64_t o_at = (int64_t)(p.t0 + tok) * a.hq + p.h * a.group + (gr - tok * a.group);
       if (active) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t x[32];
@@ -680,22 +694,6 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
             float o[32];
 #pragma unroll
             for (int e = 0; e < 32; e++) o[e] = l == 0.f ? 0.f : __uint_as_float(x[e]) * inv;
-            if (bad) {
-              // the values taken out above, for the rows that see them: any weight makes them infinite or NaN
-              const int from = max(open, p.lo * AT_KEYS), to = min(p.len, p.hi * AT_KEYS);
-              for (int j = from; j < to; j++) {
-                if (!seen.has(j)) continue;
-                const int64_t id = a.table[(int64_t)p.r * a.table_stride + (j >> a.log2_bs)];
-                if (id < 0 || id >= a.n_blocks) continue;
-                const T* v = static_cast<const T*>(a.v) + id * a.s_block + p.h * a.s_head +
-                             (j & ((1 << a.log2_bs) - 1)) * a.s_token + d;
-#pragma unroll
-                for (int e = 0; e < 32; e++) {
-                  const float y = (float)v[e];
-                  if (!(fabsf(y) < INFINITY)) o[e] += y;
-                }
-              }
-            }
             if (whole) {
               T* dst = static_cast<T*>(a.out) + o_at * D + d;
 #pragma unroll
@@ -721,10 +719,30 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       __syncwarp();
       if (lane == 0) bar_arrive(b_free);
       // two pieces ahead; streams that share it are at most AT_PIECES apart
-      if (row == 0 && (MODE != 2 || stream == 0)) s_bad[(no + 2) & 7] = 0;
+      if (row == 0 && (MODE != 2 || stream == 0)) s_bad[(taken + 2) & 7] = 0;
+      if (bad && live) {
+        // the values taken out above, for the rows that see them: any weight makes them infinite or NaN
+        const int to = min(p.len, p.hi * AT_KEYS);
+        for (int j = max(open, p.lo * AT_KEYS); j < to; j++) {
+          const int64_t id = a.table[(int64_t)p.r * a.table_stride + (j >> a.log2_bs)];
+          if (!seen.has(j) || id < 0 || id >= a.n_blocks) continue;
+          const T* v = static_cast<const T*>(a.v) + id * a.s_block + p.h * a.s_head + (j & ((1 << a.log2_bs) - 1)) * a.s_token;
+          for (int d = 0; d < D; d++) {
+            const float y = (float)v[d];
+            if (fabsf(y) < INFINITY) continue;
+            if (whole) {
+              T* dst = static_cast<T*>(a.out) + o_at * D + d;
+              *dst = (T)((float)*dst + y);
+            } else {
+              float* dst = part + (d / 4) * 512 + row * 4 + (d & 3);
+              __stcg(dst, __ldcg(dst) + y);
+            }
+          }
+        }
+      }
       if (!whole) {
         __threadfence();
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + stream) : "memory");
+        stream_sync();
         const int key = MODE == 2 ? p.first * 2 + stream : p.first;
         if (row == 0) atomicAdd(a.counters + 2 * key, 1u);
         if (joins < 2) {
@@ -732,18 +750,19 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           join_pieces[joins] = p.pieces;
           join_rows[joins] = rows;
           join_g[joins] = p.row0 + skip;
-          join_out[joins] = (int64_t)p.t0 * a.hq + p.h * a.group;
+          join_out[joins] = p.t0 * a.hq + p.h * a.group;
           joins++;
         }
       }
+      release();
       units++;
     }
     // The streams that a unit is divided over join it together, each some of its
-    // rows, the pieces always in their order on the line.  They wait for one another:
+    // outputs, the pieces always in the same order.  They wait for one another:
     // the launch is cooperative, so all are resident, and each ends its pieces first.
     for (int k = 0; k < joins && ok; k++) {
       constexpr int STEP = MODE == 2 ? 2 : 1;  // from one piece's stream to the next one's
-      const int key = join_first[k], np = join_pieces[k], mine = (me - key) / STEP;
+      const int key = join_first[k], np = join_pieces[k], mine = (me - key) / STEP, rows = join_rows[k];
       if (row == 0) {
         const volatile unsigned* done = a.counters + 2 * key;
         for (uint32_t i = 0; *done < (unsigned)np && !*abort; i++) {
@@ -752,37 +771,67 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         }
         __threadfence();
       }
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + stream) : "memory");
+      stream_sync();
       if (*abort) break;
-      const int each = (join_rows[k] + np - 1) / np, from = mine * each, n = max(0, min(join_rows[k] - from, each));
-      for (int i = row; i < n * (D / 4); i += 128) {
-        const int rr = from + i % n, ch = i / n;
+      // an item is four columns of a row; G lanes share its pieces, at most 8 at a time each
+      int G = 1;
+      while (G < 32 && G * 8 < np) G *= 2;
+      const int items = rows * (D / 4), each = (items + np - 1) / np, to = min(items, (mine + 1) * each), g = lane & (G - 1);
+      for (int i = mine * each + row / G; i - row / G < to; i += 128 / G) {
+        const bool in = i < to;
+        const int rr = in ? i % rows : 0, ch = in ? i / rows : 0;
         float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-        for (int j = 0; j < np; j++) top = fmaxf(top, __ldcg(part_at<D>(a.part, key + j * STEP, j == 0) + 128 * D + rr));
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int j = 0; j < np; j++) {
-          const float* src = part_at<D>(a.part, key + j * STEP, j == 0);
-          const float e = __ldcg(src + 128 * D + rr);
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(src) + ch * 128 + rr);
-          if (e != -INFINITY) {  // a piece without weight may hold anything
-            const float w = exp2_fast(e - top);
+        for (int j0 = g; j0 < np; j0 += 8 * G) {
+          float e[8];
+          float4 x[8];
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            const int pc = j0 + j * G;
+            const float* src = part_at<D>(a.part, key + pc * STEP, pc == 0);
+            e[j] = pc < np ? __ldcg(src + 128 * D + rr) : -INFINITY;
+            x[j] = pc < np ? __ldcg(reinterpret_cast<const float4*>(src) + ch * 128 + rr) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          float up = top;
+#pragma unroll
+          for (int j = 0; j < 8; j++) up = fmaxf(up, e[j]);
+          const float f = top == -INFINITY ? 0.f : exp2_fast(top - up);
+          sum *= f;
+          o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+          top = up;
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            if (e[j] == -INFINITY) continue;  // a piece without weight
+            const float w = exp2_fast(e[j] - top);
             sum += w;
-            o.x = fmaf(w, x.x, o.x);
-            o.y = fmaf(w, x.y, o.y);
-            o.z = fmaf(w, x.z, o.z);
-            o.w = fmaf(w, x.w, o.w);
+            o.x = fmaf(w, x[j].x, o.x);
+            o.y = fmaf(w, x[j].y, o.y);
+            o.z = fmaf(w, x[j].z, o.z);
+            o.w = fmaf(w, x[j].w, o.w);
           }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int g = join_g[k] + rr, tk = g / a.group;
-        const int64_t to = join_out[k] + (int64_t)tk * a.hq + (g - tk * a.group);
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + to * D + ch * 4) =
-            make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
-        if (a.lse && ch == 0) a.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+        for (int d = 1; d < G; d *= 2) {
+          const float t2 = __shfl_xor_sync(0xffffffffu, top, d), up = fmaxf(top, t2);
+          const float f = top == -INFINITY && sum == 0.f ? 0.f : top == up ? 1.f : exp2_fast(top - up);
+          sum *= f;
+          o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+          top = up;
+          sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          o.x += __shfl_xor_sync(0xffffffffu, o.x, d);
+          o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
+          o.z += __shfl_xor_sync(0xffffffffu, o.z, d);
+          o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
+        }
+        if (in && g == 0) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const int gr = join_g[k] + rr, tk = gr / a.group;
+          const int64_t at = (int64_t)join_out[k] + (int64_t)tk * a.hq + (gr - tk * a.group);
+          *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * D + ch * 4) =
+              make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+          if (a.lse && ch == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+        }
       }
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + stream) : "memory");
+      stream_sync();
       if (row == 0 && atomicAdd(a.counters + 2 * key + 1, 1u) == (unsigned)np - 1) {
         a.counters[2 * key] = 0;  // all have seen it
         a.counters[2 * key + 1] = 0;
@@ -911,7 +960,7 @@ extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const
   if (q_stride < (int64_t)n_q_heads * cache->head_dim || q_stride % 8)
     return attend_arg(where, "q_stride is below a token's elements or no multiple of 8");
   if (!(scale > 0.f) || scale > 3e38f) return attend_arg(where, "scale is not a positive number");
-  if (T * (n_q_heads / cache->n_heads) > INT32_MAX) return attend_arg(where, "T times the heads of a group is above 2^31");
+  if (T * n_q_heads > INT32_MAX) return attend_arg(where, "T times n_q_heads is above 2^31");
   if (T == 0 || R == 0) return TK_OK;
   if (!d_q || !d_off || !d_len || !d_out || (table_width > 0 && !d_table)) return attend_arg(where, "null pointer");
   if ((((uintptr_t)d_q | (uintptr_t)d_out) & 15) != 0) return attend_arg(where, "a buffer is not 16-byte aligned");

@@ -427,8 +427,8 @@ extern "C" int tk_kv_plan(const int64_t* d_off, const int32_t* d_ctx, int64_t R,
   return TK_OK;
 }
 
-// The cache as a tensor (element, token, head, block) whose box is one block of
-// one head and 64 elements: 128-byte rows, swizzled as the tensor cores read them.
+// The cache as a tensor (element, token, head, block) whose box is 64
+// elements of one head's block, or of half of one of 128 tokens: 128-byte rows, swizzled as the tensor cores read them.
 static bool kv_map(const tk_kv_cache* c, void* mem, CUtensorMap* map) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -440,7 +440,7 @@ static bool kv_map(const tk_kv_cache* c, void* mem, CUtensorMap* map) {
     return false;
   const cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->block_size, (cuuint64_t)c->n_heads, (cuuint64_t)c->n_blocks};
   const cuuint64_t strides[3] = {(cuuint64_t)c->stride[2] * 2, (cuuint64_t)c->stride[1] * 2, (cuuint64_t)c->stride[0] * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)c->block_size, 1, 1}, step[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)std::min(c->block_size, 64), 1, 1}, step[4] = {1, 1, 1, 1};
   return reinterpret_cast<Encode>(fn)(map, c->type == TK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                                       4, mem, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
