@@ -26,6 +26,7 @@ constexpr int AT_THREADS = 384;  // loads and products of two streams (4 warps),
 constexpr int AT_UNIT_COST = 2;  // what starting a unit costs, in tiles
 constexpr int AT_MIN_SHARE = 8;  // least share of a worker, in tiles
 constexpr int AT_SNAP = 4;       // a unit is not cut nearer to its ends than this, in tiles
+constexpr int AT_PAD = 8;        // what a worker may do more, in tiles, if it has a single piece for that
 
 struct AttendArgs {
   const void* q;
@@ -79,20 +80,39 @@ __device__ __forceinline__ int unit_keys(const AttendArgs& a, const Request& q, 
 }
 __device__ __forceinline__ int key_tiles(int keys) { return max(1, (keys + AT_KEYS - 1) / AT_KEYS); }
 
+// How the work is divided.  It is one line of units (request, row tile, key
+// head), each AT_UNIT_COST + its key tiles long; worker w has it from w * share to
+// (w + 1) * share.  Long caches are so divided over workers and short ones
+// gathered in one; a cut within AT_SNAP of a unit's start or end moves there.
+// Padded: there are fewer units than workers; a unit's length is rounded up to
+// whole shares and divided evenly over its workers, each of which has that one piece.
+// (The host keeps the line under 2^31.)
+struct Plan {
+  int share;
+  bool padded;
+};
+
+struct UnitSum {
+  int length, units, longest;
+};
 template <int ROWS>
-__device__ __forceinline__ int64_t request_cost(const AttendArgs& a, const Request& q) {
-  int64_t c = 0;
+__device__ __forceinline__ UnitSum request_work(const AttendArgs& a, const Request& q, const Plan& plan) {
+  UnitSum w = {0, 0, 0};
   const int rows = q.n * a.group;
-  if (a.mask || !q.good || rows <= ROWS) c = (int64_t)((rows + ROWS - 1) / ROWS) * (key_tiles(q.len) + AT_UNIT_COST);
-  else
-    for (int row0 = 0; row0 < rows; row0 += ROWS) c += key_tiles(unit_keys<ROWS>(a, q, row0)) + AT_UNIT_COST;
-  return c * a.hk;
+  const bool same = a.mask || !q.good || rows <= ROWS;  // every row tile has the request's keys
+  for (int row0 = 0; row0 < rows; row0 += ROWS) {
+    const int cost = key_tiles(unit_keys<ROWS>(a, q, row0)) + AT_UNIT_COST;
+    const int tiles = same ? (rows + ROWS - 1) / ROWS : 1;
+    w.length += (plan.padded ? ((unsigned)(cost + plan.share - 1) / (unsigned)plan.share) * plan.share : cost) * tiles;
+    w.units += tiles;
+    w.longest = max(w.longest, cost);
+    if (same) break;
+  }
+  w.length *= a.hk;
+  w.units *= a.hk;
+  return w;
 }
 
-// The work is one line of units (request, row tile, key head), each AT_UNIT_COST
-// + its key tiles long.  Worker w takes it from w * share to (w + 1) * share, so
-// that a long cache is divided over workers and short ones are gathered in one; a cut
-// within AT_SNAP of a unit's start or end moves there.
 struct Piece {
   int t0, r, h;       // first row of q, request, key head
   int row0, rows;     // rows of the unit among the request's tokens x group
@@ -106,68 +126,83 @@ constexpr int AT_PIECES = 4;  // handed over ahead
 
 template <int ROWS>
 struct Walk {
-  int64_t from, to, share;  // the worker's part of the line
-  int64_t u, r;             // where the next unit starts, and its request
+  Plan plan;
+  int from, to;  // the worker's part of the line
+  int u, r;      // where the next unit starts, and its request
   Request q;
-  int row0, h;
+  int row0, h;                         // the unit's row tile and head
+  int keys, cost, pieces, size, length;  // of the row tile's units; padded: what they are divided into
   bool loaded;
 
+  __device__ __forceinline__ void row_tile(const AttendArgs& a) {
+    keys = unit_keys<ROWS>(a, q, row0);
+    cost = length = key_tiles(keys) + AT_UNIT_COST;
+    if (plan.padded) {
+      pieces = (unsigned)(cost + plan.share - 1) / (unsigned)plan.share;
+      size = (unsigned)(cost + pieces - 1) / (unsigned)pieces;
+      length = pieces * plan.share;
+    }
+  }
   __device__ __forceinline__ bool next(const AttendArgs& a, Piece& x) {
-    while (u < to && r < a.R) {
+    for (;;) {
+      if (u >= to || r >= a.R) break;
       if (!loaded) {
         q = load_request(a, r);
+        if (q.n <= 0) {
+          r++;
+          continue;
+        }
         row0 = h = 0;
         loaded = true;
+        row_tile(a);
       }
-      if (row0 >= q.n * a.group) {
-        r++;
-        loaded = false;
-        continue;
+      if (u + length <= from) {  // heads before this worker
+        const int skip = min(a.hk - h, (int)((unsigned)(from - u) / (unsigned)length));
+        u += skip * length;
+        h += skip;
       }
-      const int keys = unit_keys<ROWS>(a, q, row0), tiles = key_tiles(keys), cost = tiles + AT_UNIT_COST;
-      if (h == 0 && u + (int64_t)cost * a.hk <= from) {  // all heads are before this worker
-        u += (int64_t)cost * a.hk;
-        row0 += ROWS;
-        continue;
-      }
-      const int lo = cut(from, cost), hi = cut(to, cost);
-      const bool mine = hi > lo && u + cost > from;
-      if (mine) {
-        x.t0 = q.t0;
-        x.r = (int)r;
-        x.h = h;
-        x.row0 = row0;
-        x.rows = min(ROWS, q.n * a.group - row0);
-        x.n = q.n;
-        x.ctx = q.ctx;
-        x.len = q.len;
-        x.open = !q.good ? 0 : a.mask ? q.ctx : q.ctx + row0 / a.group + 1;
-        x.keys = keys;
-        x.lo = max(0, lo - AT_UNIT_COST);
-        x.hi = hi - AT_UNIT_COST;
-        x.first = 0;
-        x.pieces = 1;
-        if (lo > 0 || hi < cost) {
-          x.first = (int)((u + AT_SNAP) / share);
-          x.pieces = (int)((u + cost - AT_SNAP - 1) / share) - x.first + 1;
-        }
-        x.valid = 1 + q.good;
-      }
-      u += cost;
-      if (++h == a.hk) {
+      if (h == a.hk) {
         h = 0;
         row0 += ROWS;
+        loaded = row0 < q.n * a.group;
+        if (loaded) row_tile(a);
+        else r++;
+        continue;
       }
-      if (mine) return true;
+      const int lo = cut(from - u), hi = cut(to - u), at = u;
+      u += length;
+      h++;
+      if (hi <= lo) continue;
+      x.t0 = q.t0;
+      x.r = r;
+      x.h = h - 1;
+      x.row0 = row0;
+      x.rows = min(ROWS, q.n * a.group - row0);
+      x.n = q.n;
+      x.ctx = q.ctx;
+      x.len = q.len;
+      x.open = !q.good ? 0 : a.mask ? q.ctx : q.ctx + row0 / a.group + 1;
+      x.keys = keys;
+      x.lo = max(0, lo - AT_UNIT_COST);
+      x.hi = hi - AT_UNIT_COST;
+      x.first = 0;
+      x.pieces = 1;
+      if (lo > 0 || hi < cost) {
+        x.first = (unsigned)(at + (plan.padded ? 0 : AT_SNAP)) / (unsigned)plan.share;
+        x.pieces = plan.padded ? pieces : (int)((unsigned)(at + cost - AT_SNAP - 1) / (unsigned)plan.share) - x.first + 1;
+      }
+      x.valid = 1 + q.good;
+      return true;
     }
     x.valid = 0;
     return false;
   }
-  // a cut at `at` of the line, inside the unit at u
-  __device__ __forceinline__ int cut(int64_t at, int cost) const {
-    const int64_t in = at - u;
-    if (in <= AT_SNAP && in < cost) return 0;
-    return in >= cost - AT_SNAP ? cost : (int)in;
+  // a worker's end `in` after the unit's start, as a cut of the unit
+  __device__ __forceinline__ int cut(int in) const {
+    if (in <= 0) return 0;
+    if (in >= length) return cost;
+    if (plan.padded) return min(cost, (int)((unsigned)in / (unsigned)plan.share) * size);
+    return in <= AT_SNAP ? 0 : in >= cost - AT_SNAP ? cost : in;
   }
 };
 
@@ -224,8 +259,8 @@ struct AttendShape {
   static constexpr int N_BARS = RINGS * (2 * STAGES + 2 * AT_PIECES) + 2 * 9;
   static constexpr int PIECES = BARS + 8 * N_BARS;
   static constexpr int SMALL = PIECES + RINGS * AT_PIECES * (int)sizeof(Piece);
-  // start of the walk (2 x 2 x 8), sums of the warps, tensor memory, abort, non-finite values (2 x 8)
-  static constexpr int TOTAL = SMALL + 32 + 8 * (AT_THREADS / 32) + 72;
+  // start of the walk (2 x 2), sums, units and longest of the warps, tensor memory, abort, non-finite values (2 x 8)
+  static constexpr int TOTAL = SMALL + 16 + 12 * (AT_THREADS / 32) + 72;
   static_assert(SMALL % 8 == 0 && TOTAL <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -261,9 +296,11 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
   const uint32_t b_q = base + L::BARS + L::RINGS * 8 * (2 * NST + 2 * AT_PIECES) + stream * 72, b_s = b_q + 8, b_p = b_s + 16,
                  b_v = b_p + 16, b_o = b_v + 8, b_free = b_o + 8, b_drain = b_free + 8;
   Piece* s_piece = reinterpret_cast<Piece*>(smem + L::PIECES) + ring * AT_PIECES;
-  int64_t* s_walk = reinterpret_cast<int64_t*>(smem + L::SMALL);  // of each worker: first request, where it starts
-  int64_t* s_sum = s_walk + 4;
-  volatile int* s_int = reinterpret_cast<volatile int*>(s_sum + AT_THREADS / 32);
+  int* s_walk = reinterpret_cast<int*>(smem + L::SMALL);  // of each worker: first request, where it starts
+  int* s_sum = s_walk + 4;
+  int* s_units = s_sum + AT_THREADS / 32;
+  int* s_longest = s_units + AT_THREADS / 32;
+  volatile int* s_int = reinterpret_cast<volatile int*>(s_longest + AT_THREADS / 32);
   volatile int* abort = s_int + 1;
   volatile int* s_bad = s_int + 2 + 8 * ring;  // by piece
 
@@ -293,42 +330,82 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
   }
   if (warp == 1) tmem_alloc(smem_addr(const_cast<int*>(s_int)));
 
-  // where the workers start: the requests' costs added up, each thread a run of them
-  constexpr int WORKERS = MODE == 2 ? 1 : 2;  // of a CTA
-  int64_t share, total = 0;
+  // the block table on its way to L2, for the loads that follow the plan
   {
-    const int64_t per = (a.R + AT_THREADS - 1) / AT_THREADS;
-    const int64_t r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
-    int64_t sum = 0;
-    for (int64_t r = r0; r < r1; r++) {
+    const int64_t at = ((int64_t)blockIdx.x * AT_THREADS + tid) * 32;
+    if (at < (a.R - 1) * a.table_stride + a.table_width) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.table + at));
+  }
+  // the plan, and where the workers start on its line: the requests' lengths added up, each
+  // thread a run of them
+  constexpr int WORKERS = MODE == 2 ? 1 : 2;  // of a CTA
+  Plan plan = {1, false};
+  int total;
+  {
+    const int R = (int)a.R, per = (R + AT_THREADS - 1) / AT_THREADS;
+    const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
+    int mine = 0, units = 0, longest = 0, before;
+    for (int r = r0; r < r1; r++) {
       const Request q = load_request(a, r);
       if (!q.good && blockIdx.x == 0 && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = r;
-      sum += request_cost<ROWS>(a, q);
+      const UnitSum w = request_work<ROWS>(a, q, plan);
+      mine += w.length;
+      units += w.units;
+      longest = max(longest, w.longest);
     }
-    int64_t incl = sum;
+    // the sum over the threads before this one, and over all
+    auto scan = [&](int x, int& all) {
+      int incl = x;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) s_sum[warp] = incl;
+      __syncthreads();
+      int b = incl - x;
+      all = 0;
+#pragma unroll
+      for (int w = 0; w < AT_THREADS / 32; w++) {
+        const int y = s_sum[w];
+        if (w < warp) b += y;
+        all += y;
+      }
+      return b;
+    };
+    units = __reduce_add_sync(0xffffffffu, units);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+      s_units[warp] = units;
+      s_longest[warp] = longest;
     }
-    if (lane == 31) s_sum[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - sum;
+    before = scan(mine, total);
+    units = 0;
 #pragma unroll
     for (int w = 0; w < AT_THREADS / 32; w++) {
-      const int64_t y = s_sum[w];
-      if (w < warp) before += y;
-      total += y;
+      units += s_units[w];
+      longest = max(longest, s_longest[w]);
     }
-    const unsigned workers = gridDim.x * WORKERS;
-    share = total >> 31 ? (total + workers - 1) / workers : ((unsigned)total + workers - 1) / workers;
-    share = max((int64_t)AT_MIN_SHARE, share);
+    const int workers = gridDim.x * WORKERS;
+    auto over = [](int x, int y) { return (int)((unsigned)(x + y - 1) / (unsigned)y); };
+    plan.share = max(AT_MIN_SHARE, over(total, workers));
+    if (units > 0 && units < workers) {
+      // shares that give the units no more workers than there are
+      const int share = max(AT_MIN_SHARE, min(over(longest, workers / units), over(total, workers - units)));
+      if (share <= plan.share + AT_PAD) {
+        plan.share = share;
+        plan.padded = true;
+        mine = 0;
+        for (int r = r0; r < r1; r++) mine += request_work<ROWS>(a, load_request(a, r), plan).length;
+        __syncthreads();  // s_sum has been read
+        before = scan(mine, total);
+      }
+    }
     for (int w = 0; w < WORKERS; w++) {
-      const int64_t x = (blockIdx.x * WORKERS + w) * share;
-      if (x < before || x >= before + sum) continue;
-      int64_t r = r0, at = before;
+      const int x = (blockIdx.x * WORKERS + w) * plan.share;
+      if (x < before || x >= before + mine) continue;
+      int r = r0, at = before;
       for (; r < r1 - 1; r++) {
-        const int64_t c = request_cost<ROWS>(a, load_request(a, r));
+        const int c = request_work<ROWS>(a, load_request(a, r), plan).length;
         if (x < at + c) break;
         at += c;
       }
@@ -358,10 +435,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     if (warp == 0 || (warp == 3 && MODE != 2)) {
       // ---- loads, in the order of their use: K0 K1 V0 K2 V1 K3 ...
       Walk<ROWS> walk;
-      walk.share = share;
-      walk.from = (blockIdx.x * WORKERS + ring) * share;
-      walk.to = min(total, walk.from + share);
-      walk.r = walk.from < total ? s_walk[2 * ring] : a.R;
+      walk.plan = plan;
+      walk.from = (blockIdx.x * WORKERS + ring) * plan.share;
+      walk.to = min(total, walk.from + plan.share);
+      walk.r = walk.from < total ? s_walk[2 * ring] : (int)a.R;
       walk.u = walk.from < total ? s_walk[2 * ring + 1] : total;
       walk.loaded = false;
       uint32_t at = 0, pos = 0;
@@ -439,7 +516,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         tmem_fence_after();
         return r;
       };
-      auto full = [&]() { return wait(b_full + 8 * (pos % NST), (pos / NST) & 1); };
+      auto full = [&](uint32_t at) { return wait(b_full + 8 * (at % NST), (at / NST) & 1); };
       auto scores = [&](uint32_t buf) {  // S = Q K^T
         const uint32_t k = mma_desc(s_ring + (pos % NST) * L::STAGE, 16), q = mma_desc(s_q, 16);
         if (elect_one()) {
@@ -459,23 +536,25 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         release();
         if (MODE == 2 && stream * 128 >= rows) {  // no rows for this stream
           for (int i = 0; ok && i < 2 * n; i++, pos++) {
-            ok = full();
+            ok = full(pos);
             if (ok && lane == 0) bar_arrive(b_empty + 8 * (pos % NST));
           }
           continue;
         }
-        if (!(ok = wait(b_q, units & 1) && full())) break;
+        if (!(ok = wait(b_q, units & 1) && full(pos))) break;
         scores(nt & 1);
         if (n > 1) {
-          if (!(ok = full())) break;
+          if (!(ok = full(pos))) break;
           scores((nt + 1) & 1);
         }
         for (int t = 0; t < n; t++, nt++) {
-          // O += P V; the first of a unit when the last one's output has been read
-          if (!(ok = full() && (t > 0 || units == 0 || wait(b_free, (units + 1) & 1)))) break;
+          // the weights come last: what follows them is on the way to the next scores
+          if (!(ok = full(pos) && (t + 2 >= n || full(pos + 1)))) break;
+          // the first of a unit when the last one's output has been read
+          if (t == 0 && units > 0 && !(ok = wait(b_free, (units + 1) & 1))) break;
           if (!(ok = wait(b_p + 8 * (nt & 1), (nt >> 1) & 1))) break;
           const uint32_t v = mma_desc(s_ring + (pos % NST) * L::STAGE, AT_KEYS * 128), buf = nt & 1;
-          if (elect_one()) {
+          if (elect_one()) {  // O += P V
 #pragma unroll
             for (int i = 0; i < AT_KEYS / 16; i++)
               mma_ts(stream * 256 + 128, stream * 256 + buf * 64 + i * 8, v + i * (2048 >> 4), KIND_O, t > 0 || i > 0);
@@ -485,10 +564,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           }
           __syncwarp();
           pos++;
-          if (t + 2 < n) {
-            if (!(ok = full())) break;
-            scores(buf);
-          }
+          if (t + 2 < n) scores(buf);
         }
         units++;
       }
@@ -970,6 +1046,13 @@ extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const
                   cache->v, cache->n_blocks, cache->stride[0], cache->stride[1],
                   cache->stride[2], cache->log2_block, ws->part, ws->counters};
   cudaStream_t st = (cudaStream_t)cuda_stream;
+  // an upper bound of the line that the kernel divides
+  const double tiles = ((double)(table_width << cache->log2_block) / AT_KEYS + 1 + AT_UNIT_COST + AT_MIN_SHARE) * cache->n_heads;
+  if (tiles * ((double)T * group / 32 + (double)R) >= 2e9) {
+    tk_set_error("%s: %lld tokens over tables of %lld blocks are too much work for one call", where, (long long)T,
+                 (long long)table_width);
+    return TK_E_LIMIT;
+  }
   const int64_t rows = std::min(max_new, T) * group;  // of a request and key head
   cudaError_t e;
   if (cache->type == TK_BF16)
