@@ -509,62 +509,72 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       // ---- products: the warp waits as one, one lane issues (with a branch of its own for
       // the lane every operand would be a divergent one: 120 cycles a product instead of 64)
       constexpr uint32_t KIND_S = mma_kind(BF, 128, AT_KEYS, false), KIND_O = mma_kind(BF, 128, D, true);
-      uint32_t pos = 0, units = 0, nt = 0;
+      uint32_t st = 0, ph = 0, units = 0, nt = 0;  // stage, its parity; units, tiles so far
       bool ok = true;
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        const bool r = __all_sync(0xffffffffu, bar_wait(bar, parity, abort)) != 0;
-        tmem_fence_after();
-        return r;
+      const uint32_t q = mma_desc(s_q, 16);
+      auto after = [&](uint32_t x) { return x + 1 == NST ? 0 : x + 1; };
+      auto advance = [&]() {
+        st = after(st);
+        if (st == 0) ph ^= 1;
       };
-      auto full = [&](uint32_t at) { return wait(b_full + 8 * (at % NST), (at / NST) & 1); };
-      auto scores = [&](uint32_t buf) {  // S = Q K^T
-        const uint32_t k = mma_desc(s_ring + (pos % NST) * L::STAGE, 16), q = mma_desc(s_q, 16);
-        if (elect_one()) {
-#pragma unroll
-          for (int i = 0; i < D / 16; i++)
-            mma_ss(stream * 256 + buf * 64, q + (((i >> 2) * (L::Q_ROWS * 128) + (i & 3) * 32) >> 4),
-                   k + (((i >> 2) * (AT_KEYS * 128) + (i & 3) * 32) >> 4), KIND_S, i > 0);
-          mma_commit(b_s + 8 * buf);
-          mma_commit(b_empty + 8 * (pos % NST));
+      // up to four barriers at once, one a lane: what a tile waits for costs one wait
+      auto wait4 = [&](uint32_t bar, uint32_t parity, bool mine) {
+        for (uint32_t i = 0; i < 1u << 20; i++) {
+          if (__all_sync(0xffffffffu, !mine || bar_try(bar, parity))) {
+            tmem_fence_after();
+            return true;
+          }
+          if ((i & 63) == 63 && __any_sync(0xffffffffu, *abort)) return false;
         }
-        __syncwarp();
-        pos++;
+        *abort = 1;
+        return false;
+      };
+      auto scores = [&](uint32_t buf, uint32_t at) {  // S = Q K^T
+        const uint32_t k = mma_desc(s_ring + at * L::STAGE, 16);
+#pragma unroll
+        for (int i = 0; i < D / 16; i++)
+          mma_ss(stream * 256 + buf * 64, q + (((i >> 2) * (L::Q_ROWS * 128) + (i & 3) * 32) >> 4),
+                 k + (((i >> 2) * (AT_KEYS * 128) + (i & 3) * 32) >> 4), KIND_S, i > 0);
+        mma_commit(b_s + 8 * buf);
+        mma_commit(b_empty + 8 * at);
       };
       while (ok && coming(taken)) {
         const Piece& p = s_piece[taken % AT_PIECES];
         const int n = __shfl_sync(0xffffffffu, p.hi - p.lo, 0), rows = __shfl_sync(0xffffffffu, p.rows, 0);
         release();
         if (MODE == 2 && stream * 128 >= rows) {  // no rows for this stream
-          for (int i = 0; ok && i < 2 * n; i++, pos++) {
-            ok = full(pos);
-            if (ok && lane == 0) bar_arrive(b_empty + 8 * (pos % NST));
+          for (int i = 0; ok && i < 2 * n; i++, advance()) {
+            ok = wait4(b_full + 8 * st, ph, lane == 0);
+            if (ok && lane == 0) bar_arrive(b_empty + 8 * st);
           }
           continue;
         }
-        if (!(ok = wait(b_q, units & 1) && full(pos))) break;
-        scores(nt & 1);
-        if (n > 1) {
-          if (!(ok = full(pos))) break;
-          scores((nt + 1) & 1);
+        for (int t = 0; t < min(n, 2); t++, advance()) {
+          if (!(ok = wait4(lane == 0 ? b_full + 8 * st : b_q, lane == 0 ? ph : units & 1, lane < 2))) break;
+          if (elect_one()) scores((nt + t) & 1, st);
+          __syncwarp();
         }
+        if (!ok) break;
         for (int t = 0; t < n; t++, nt++) {
-          // the weights come last: what follows them is on the way to the next scores
-          if (!(ok = full(pos) && (t + 2 >= n || full(pos + 1)))) break;
-          // the first of a unit when the last one's output has been read
-          if (t == 0 && units > 0 && !(ok = wait(b_free, (units + 1) & 1))) break;
-          if (!(ok = wait(b_p + 8 * (nt & 1), (nt >> 1) & 1))) break;
-          const uint32_t v = mma_desc(s_ring + (pos % NST) * L::STAGE, AT_KEYS * 128), buf = nt & 1;
-          if (elect_one()) {  // O += P V
+          // lanes: the values, the keys two tiles on, the weights, and at first the last unit's output to be read
+          const uint32_t buf = nt & 1, nx = after(st);
+          const bool more = t + 2 < n;
+          const uint32_t bar = lane == 0 ? b_full + 8 * st : lane == 1 ? b_full + 8 * nx : lane == 2 ? b_p + 8 * buf : b_free;
+          const uint32_t par = lane == 0 ? ph : lane == 1 ? (nx == 0 ? ph ^ 1 : ph) : lane == 2 ? (nt >> 1) & 1 : (units + 1) & 1;
+          if (!(ok = wait4(bar, par, lane == 0 || (lane == 1 && more) || lane == 2 || (lane == 3 && t == 0 && units > 0)))) break;
+          if (elect_one()) {
+            const uint32_t v = mma_desc(s_ring + st * L::STAGE, AT_KEYS * 128);
 #pragma unroll
-            for (int i = 0; i < AT_KEYS / 16; i++)
+            for (int i = 0; i < AT_KEYS / 16; i++)  // O += P V
               mma_ts(stream * 256 + 128, stream * 256 + buf * 64 + i * 8, v + i * (2048 >> 4), KIND_O, t > 0 || i > 0);
             mma_commit(b_v);
-            mma_commit(b_empty + 8 * (pos % NST));
+            mma_commit(b_empty + 8 * st);
             if (t == n - 1) mma_commit(b_o);
+            if (more) scores(buf, nx);
           }
           __syncwarp();
-          pos++;
-          if (t + 2 < n) scores(buf);
+          advance();
+          if (more) advance();
         }
         units++;
       }
