@@ -441,7 +441,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       walk.r = walk.from < total ? s_walk[2 * ring] : (int)a.R;
       walk.u = walk.from < total ? s_walk[2 * ring + 1] : total;
       walk.loaded = false;
-      uint32_t at = 0, pos = 0;
+      uint32_t at = 0, st = 0, ph = 0, filled = 0;  // pieces handed over; stage, its parity, stages filled (up to all)
       bool ok = true;
       auto hand = [&](const Piece& x) {
         ok = at < AT_PIECES || bar_wait(b_taken + 8 * (at % AT_PIECES), (at / AT_PIECES + 1) & 1, abort);
@@ -453,58 +453,71 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         __syncwarp();
         at++;
       };
-      // a box is 64 elements of one page, or of half of one of 128
-      const int log2_box = min(a.log2_bs, 6), ppt = AT_KEYS >> log2_box;
+      // a box is 64 elements of one page, or of half of one of 128; a lane loads one box
+      const int log2_box = min(a.log2_bs, 6), per_page = a.log2_bs - log2_box, ppt = AT_KEYS >> log2_box;
+      const int my_box = lane / HALVES, my_half = lane % HALVES;
+      const uint32_t my_dst = s_ring + my_half * (AT_KEYS * 128) + (my_box * 128 << log2_box);
+      const uint32_t box_bytes = HALVES * 128u << log2_box;
+      // block ids: a lane has box `window + lane`, and the one 32 further on
+      struct Ids {
+        int window, now, then;
+      };
+      int boxes = 0, h = 0;
+      const int32_t* row = nullptr;
+      auto id_of = [&](int b) { return b < boxes ? __ldg(row + (b >> per_page)) : 0; };
+      auto load = [&](const CUtensorMap* map, Ids& ids, int tile) {
+        const int box0 = tile * ppt;
+        if (box0 >= ids.window + 32) {
+          ids.window += 32;
+          ids.now = ids.then;
+          ids.then = id_of(ids.window + 32 + lane);
+        }
+        const int nb = max(0, min(ppt, boxes - box0));
+        const int id = __shfl_sync(0xffffffffu, ids.now, (box0 + my_box) & 31);
+        if (filled == NST) {
+          ok = __all_sync(0xffffffffu, bar_wait(b_empty + 8 * st, ph ^ 1, abort)) != 0;
+          if (!ok) return;
+        } else {
+          filled++;
+        }
+        if (elect_one()) bar_expect(b_full + 8 * st, nb * box_bytes);
+        __syncwarp();
+        if (my_box < nb)
+          tma_load_4d(my_dst + st * L::STAGE, map, b_full + 8 * st, my_half * 64, per_page ? (box0 & 1) * AT_KEYS : 0, h, id);
+        if (++st == NST) st = 0, ph ^= 1;
+      };
       Piece nx;
       walk.next(a, nx);
       hand(nx);
       while (ok && nx.valid) {
-        const int r = nx.r, h = nx.h, lo = nx.lo, n = nx.hi - nx.lo;
-        const int boxes = (nx.keys + (1 << log2_box) - 1) >> log2_box, per_page = a.log2_bs - log2_box;
-        // lanes hold the block ids of 32 boxes, and of the next 32
-        const int32_t* row = a.table + (int64_t)r * a.table_stride;
-        auto id_of = [&](int b) { return b < boxes ? row[b >> per_page] : 0; };
-        int win_k = (lo * ppt) & ~31, win_v = win_k;
-        int ids_k = id_of(win_k + lane), nxt_k = id_of(win_k + 32 + lane), ids_v = ids_k, nxt_v = nxt_k;
-        for (int i = 0; ok && i < 2 * n; i++, pos++) {
-          const int lead = min(n, 2);
-          const bool value = i >= lead && (i == 2 * n - 1 || ((i - lead) & 1) == 0);
-          const int t = i < lead ? i : i == 2 * n - 1 ? n - 1 : value ? (i - lead) >> 1 : ((i - lead) >> 1) + 2;
-          const int box0 = (lo + t) * ppt;
-          if (value && box0 >= win_v + 32) {
-            win_v += 32;
-            ids_v = nxt_v;
-            nxt_v = id_of(win_v + 32 + lane);
-          } else if (!value && box0 >= win_k + 32) {
-            win_k += 32;
-            ids_k = nxt_k;
-            nxt_k = id_of(win_k + 32 + lane);
-          }
-          const int nb = max(0, min(ppt, boxes - box0));
-          const int id = __shfl_sync(0xffffffffu, value ? ids_v : ids_k, (box0 + lane) & 31);
-          const uint32_t st = pos % NST, dst = s_ring + st * L::STAGE;
-          ok = pos < NST || bar_wait(b_empty + 8 * st, (pos / NST + 1) & 1, abort);
-          if (!(ok = __all_sync(0xffffffffu, ok) != 0)) break;
-          if (lane == 0) bar_expect(b_full + 8 * st, (uint32_t)nb * (HALVES * 128u << log2_box));
-          __syncwarp();
-          if (lane < nb) {
-#pragma unroll
-            for (int s = 0; s < HALVES; s++)
-              tma_load_4d(dst + s * (AT_KEYS * 128) + (lane * 128 << log2_box), value ? &map_v : &map_k, b_full + 8 * st, s * 64,
-                          per_page ? (box0 & 1) * AT_KEYS : 0, h, id);
-          }
+        const int lo = nx.lo, hi = nx.hi;
+        h = nx.h;
+        boxes = (nx.keys + (1 << log2_box) - 1) >> log2_box;
+        row = a.table + (int64_t)nx.r * a.table_stride;
+        Ids k, v;
+        k.window = (lo * ppt) & ~31;
+        k.now = id_of(k.window + lane);
+        k.then = id_of(k.window + 32 + lane);
+        v = k;
+        load(&map_k, k, lo);
+        if (ok && lo + 1 < hi) load(&map_k, k, lo + 1);
+        for (int t = lo; ok && t < hi; t++) {
+          load(&map_v, v, t);
           // the next piece is known to the softmax, which asks for it in its last tile, before
           // more loads wait for it
-          if (i == 1) {
+          if (ok && t == lo) {
             walk.next(a, nx);
             hand(nx);
           }
+          if (ok && t + 2 < hi) load(&map_k, k, t + 2);
         }
       }
       // given up: the copies in flight land before the CTA ends
       if (*abort)
-        for (uint32_t k = pos > NST ? pos - NST : 0; k < pos; k++)
-          for (uint32_t i = 0; i < 1u << 16 && !bar_try(b_full + 8 * (k % NST), (k / NST) & 1); i++) {}
+        for (uint32_t k = 0; k < filled; k++) {
+          const uint32_t x = st + NST - filled + k;  // the stages filled last, oldest first
+          for (uint32_t i = 0; i < 1u << 16 && !bar_try(b_full + 8 * (x % NST), x >= NST ? ph : ph ^ 1); i++) {}
+        }
     } else if (warp == 1 || warp == 2) {
       // ---- products: the warp waits as one, one lane issues (with a branch of its own for
       // the lane every operand would be a divergent one: 120 cycles a product instead of 64)
