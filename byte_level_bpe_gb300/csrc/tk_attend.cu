@@ -525,22 +525,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       uint32_t st = 0, ph = 0, units = 0, nt = 0;  // stage, its parity; units, tiles so far
       bool ok = true;
       const uint32_t q = mma_desc(s_q, 16);
-      auto after = [&](uint32_t x) { return x + 1 == NST ? 0 : x + 1; };
+      auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity, abort)) != 0; };
+      auto full = [&]() { return wait(b_full + 8 * st, ph); };
       auto advance = [&]() {
-        st = after(st);
-        if (st == 0) ph ^= 1;
-      };
-      // up to four barriers at once, one a lane: what a tile waits for costs one wait
-      auto wait4 = [&](uint32_t bar, uint32_t parity, bool mine) {
-        for (uint32_t i = 0; i < 1u << 20; i++) {
-          if (__all_sync(0xffffffffu, !mine || bar_try(bar, parity))) {
-            tmem_fence_after();
-            return true;
-          }
-          if ((i & 63) == 63 && __any_sync(0xffffffffu, *abort)) return false;
-        }
-        *abort = 1;
-        return false;
+        if (++st == NST) st = 0, ph ^= 1;
       };
       auto scores = [&](uint32_t buf, uint32_t at) {  // S = Q K^T
         const uint32_t k = mma_desc(s_ring + at * L::STAGE, 16);
@@ -557,37 +545,45 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         release();
         if (MODE == 2 && stream * 128 >= rows) {  // no rows for this stream
           for (int i = 0; ok && i < 2 * n; i++, advance()) {
-            ok = wait4(b_full + 8 * st, ph, lane == 0);
+            ok = full();
             if (ok && lane == 0) bar_arrive(b_empty + 8 * st);
           }
           continue;
         }
+        if (!(ok = wait(b_q, units & 1))) break;
         for (int t = 0; t < min(n, 2); t++, advance()) {
-          if (!(ok = wait4(lane == 0 ? b_full + 8 * st : b_q, lane == 0 ? ph : units & 1, lane < 2))) break;
+          if (!(ok = full())) break;
+          tmem_fence_after();
           if (elect_one()) scores((nt + t) & 1, st);
           __syncwarp();
         }
-        if (!ok) break;
+        // the first output of a unit when the last one's has been read
+        if (!ok || (units > 0 && !(ok = wait(b_free, (units + 1) & 1)))) break;
         for (int t = 0; t < n; t++, nt++) {
-          // lanes: the values, the keys two tiles on, the weights, and at first the last unit's output to be read
-          const uint32_t buf = nt & 1, nx = after(st);
+          // what is there early is waited for first: nothing but the weights is on the way from them to
+          // the next scores
+          const uint32_t sv = st, buf = nt & 1;
+          if (!(ok = full())) break;
+          advance();
+          const uint32_t sk = st;
           const bool more = t + 2 < n;
-          const uint32_t bar = lane == 0 ? b_full + 8 * st : lane == 1 ? b_full + 8 * nx : lane == 2 ? b_p + 8 * buf : b_free;
-          const uint32_t par = lane == 0 ? ph : lane == 1 ? (nx == 0 ? ph ^ 1 : ph) : lane == 2 ? (nt >> 1) & 1 : (units + 1) & 1;
-          if (!(ok = wait4(bar, par, lane == 0 || (lane == 1 && more) || lane == 2 || (lane == 3 && t == 0 && units > 0)))) break;
+          if (more) {
+            if (!(ok = full())) break;
+            advance();
+          }
+          const uint32_t v = mma_desc(s_ring + sv * L::STAGE, AT_KEYS * 128);
+          if (!(ok = wait(b_p + 8 * buf, (nt >> 1) & 1))) break;
+          tmem_fence_after();
           if (elect_one()) {
-            const uint32_t v = mma_desc(s_ring + st * L::STAGE, AT_KEYS * 128);
 #pragma unroll
             for (int i = 0; i < AT_KEYS / 16; i++)  // O += P V
               mma_ts(stream * 256 + 128, stream * 256 + buf * 64 + i * 8, v + i * (2048 >> 4), KIND_O, t > 0 || i > 0);
             mma_commit(b_v);
-            mma_commit(b_empty + 8 * st);
+            mma_commit(b_empty + 8 * sv);
             if (t == n - 1) mma_commit(b_o);
-            if (more) scores(buf, nx);
+            if (more) scores(buf, sk);
           }
           __syncwarp();
-          advance();
-          if (more) advance();
         }
         units++;
       }
@@ -606,10 +602,12 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     const float c = a.scale_log2;
     const int me = blockIdx.x * 2 + stream;
     uint32_t nt = 0, units = 0, stages = 0;
-    bool ok = true;
     int joins = 0, join_first[2], join_pieces[2], join_rows[2], join_g[2], join_out[2];
-    auto wait = [&](uint32_t bar, uint32_t parity) {  // one answer for the warp
-      return __all_sync(0xffffffffu, bar_wait(bar, parity, abort)) != 0;
+    // A wait that gave up does not end the loops here (the next piece that does not come does):
+    // what runs on is bounded, and its results are reported as an error.
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      bar_wait(bar, parity, abort);
+      __syncwarp();
     };
     auto stream_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + stream) : "memory"); };
     constexpr int SKIP = MODE == 2 ? 128 : 0;  // rows of a unit before those of the second stream
@@ -668,7 +666,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         const int k0 = (p.lo + t) * AT_KEYS;
         const bool masked = k0 + AT_KEYS > open;
         const uint32_t buf = nt & 1;
-        if (!(ok = wait(b_s + 8 * buf, (nt >> 1) & 1))) break;
+        wait(b_s + 8 * buf, (nt >> 1) & 1);
         tmem_fence_after();
         uint32_t s[64];
         if (active) {
@@ -694,7 +692,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           const bool grow = live && mx > m && !((mx - m) * c <= 8.f);
           if (t > 0 && __any_sync(0xffffffffu, grow)) {
             // the products of the tile before may still run
-            if (!(ok = wait(b_v, (nt + 1) & 1))) break;
+            wait(b_v, (nt + 1) & 1);
             tmem_fence_after();
             const float f = grow ? exp2_fast((m - mx) * c) : 1.f;
 #pragma unroll 1
@@ -716,7 +714,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           // (Rows that do see them get them back below.)  Streams that share a tile leave it to the first.
           if (MODE != 2 || stream == 0) {
             const uint32_t at = ring0 + (n == 1 ? 1 : t == n - 1 ? 2 * n - 1 : 2 * t + 2);
-            if (!(ok = wait(b_full + 8 * (at % NST), (at / NST) & 1))) break;
+            wait(b_full + 8 * (at % NST), (at / NST) & 1);
             const int kr = row & 63, half = row >> 6, key = k0 + kr;  // a thread has half a row
             if (key >= open) {
               uint8_t* v = smem + (s_ring - base) + (at % NST) * L::STAGE + kr * 128;
@@ -775,7 +773,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           }
         }
       }
-      if (!ok || !(ok = wait(b_o, units & 1))) break;
+      wait(b_o, units & 1);
       tmem_fence_after();
 
       const bool whole = p.pieces == 1;
@@ -859,7 +857,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     // The streams that a unit is divided over join it together, each some of its
     // outputs, the pieces always in the same order.  They wait for one another:
     // the launch is cooperative, so all are resident, and each ends its pieces first.
-    for (int k = 0; k < joins && ok; k++) {
+    for (int k = 0; k < joins && !*abort; k++) {
       constexpr int STEP = MODE == 2 ? 2 : 1;  // from one piece's stream to the next one's
       const int key = join_first[k], np = join_pieces[k], mine = (me - key) / STEP, rows = join_rows[k];
       if (row == 0) {

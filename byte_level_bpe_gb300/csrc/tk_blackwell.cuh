@@ -35,9 +35,10 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // False after about a second without the phase, or when another wait of the
 // CTA has given up (*abort): the caller unwinds.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (bar_try(bar, parity)) return true;
   for (uint32_t i = 0; i < 1u << 20; i++) {
     if (bar_try(bar, parity)) return true;
-    if ((i & 63) == 63 && *abort) return false;
+    if ((i & 15) == 0 && *abort) return false;
   }
   *abort = 1;
   return false;
