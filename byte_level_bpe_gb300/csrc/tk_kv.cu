@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <new>
 
+#include "tk_blackwell.cuh"
 #include "tk_kv.cuh"
 
 namespace tk {
@@ -225,8 +226,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs a) {
 
 // -------------------------------------------------------------- tk_kv_append
 
-constexpr int APPEND_THREADS = 256;
-constexpr int APPEND_PASSES = 4;  // 16-byte loads in flight per lane
+constexpr int APPEND_THREADS = 128;
+constexpr int APPEND_FLIGHT = 4;  // passes of a warp in flight, two 16-byte loads a lane each
 
 struct AppendArgs {
   const void* qkv;
@@ -245,13 +246,15 @@ struct AppendArgs {
   void* v;
   int64_t s_block, s_head, s_token, n_slots;
   int log2_bs;
-  int chunks;  // warps per token
+  int chunks, passes;  // warps per token, passes of each
 };
 
-// One warp takes APPEND_PASSES * (32 / LANES) heads of one token; LANES lanes
-// hold a head, 8 elements each.  y = x * rsqrt(mean(x^2) + eps) * gain, then
-// (a, b) -> (a cos - b sin, b cos + a sin) on the first rot elements; values
-// are copied.  The (cos, sin) of a lane's elements are read once for all its heads.
+// y = x * rsqrt(mean(x^2) + eps) * gain for every head of queries and keys, then
+// (a, b) -> (a cos - b sin, b cos + a sin); values are copied.
+// Bound by the rows' bytes, so the arithmetic has to stay under them: LANES lanes
+// hold a head, 16 elements each, as 8 pairs that rotate together (so that no element crosses
+// lanes), and work on two of them per instruction; gain and rotation become
+// four factors per pair, computed once per token and side.  A pass is 32 / LANES heads of one token.
 template <class T, int LANES, bool NEIGHBOURS>
 __global__ void __launch_bounds__(APPEND_THREADS) k_kv_append(AppendArgs a) {
   using P = Pair<T>;
@@ -261,125 +264,165 @@ __global__ void __launch_bounds__(APPEND_THREADS) k_kv_append(AppendArgs a) {
   const int64_t w = ((int64_t)blockIdx.x * APPEND_THREADS + threadIdx.x) >> 5;
   const int64_t t = w / a.chunks;
   if (t >= a.T) return;
-  const int all = a.hq + 2 * a.hk, turned = a.hq + a.hk;
-  const int h0 = (int)(w - t * a.chunks) * (HEADS * APPEND_PASSES) + lane / LANES;
-  const int e0 = l * 8;
-  const bool in_dim = e0 < a.dim;
-  const T* row = static_cast<const T*>(a.qkv) + t * a.row_stride + e0;
+  // the lane's two runs of 8 elements: pairs are (e0 + i, e1 + i), or neighbours in each
+  const int half = a.rot >> 1;
+  const bool rotated = l * 16 < a.rot, in_dim = l * 16 < a.dim;
+  const bool apart = !NEIGHBOURS && rotated;
+  const int e0 = apart ? l * 8 : l * 16, e1 = apart ? e0 + half : e0 + 8;
 
   union Vec {
     uint4 u;
     T2 p[4];
   };
-  Vec x[APPEND_PASSES];
-#pragma unroll
-  for (int i = 0; i < APPEND_PASSES; i++) {
-    const int h = h0 + i * HEADS;
-    x[i].u = (in_dim && h < all) ? *reinterpret_cast<const uint4*>(row + (int64_t)h * a.dim) : make_uint4(0, 0, 0, 0);
-  }
-
-  const bool rotated = e0 < a.rot;
-  const int half = a.rot >> 1;
-  float cs[8], sn[8];
+  float cs[8], sn[8];  // of the 8 pairs
   if (rotated) {
     const int64_t p = a.pos[t];
-    if (p < 0 || p >= a.rope_len) {
+    const bool known = p >= 0 && p < a.rope_len;
+    const float4* src = reinterpret_cast<const float4*>(a.rope + ((known ? p : 0) * half + l * 8) * 2);
 #pragma unroll
-      for (int j = 0; j < 8; j++) cs[j] = sn[j] = __int_as_float(0x7fffffff);
-    } else {
-      const int f0 = NEIGHBOURS ? e0 >> 1 : (e0 < half ? e0 : e0 - half);
-      const float4* src = reinterpret_cast<const float4*>(a.rope + (p * half + f0) * 2);
-#pragma unroll
-      for (int j = 0; j < (NEIGHBOURS ? 2 : 4); j++) {
-        const float4 f = __ldg(src + j);
-        if (NEIGHBOURS) {
-          cs[4 * j] = cs[4 * j + 1] = f.x;
-          sn[4 * j] = sn[4 * j + 1] = f.y;
-          cs[4 * j + 2] = cs[4 * j + 3] = f.z;
-          sn[4 * j + 2] = sn[4 * j + 3] = f.w;
-        } else {
-          cs[2 * j] = f.x;
-          sn[2 * j] = f.y;
-          cs[2 * j + 1] = f.z;
-          sn[2 * j + 1] = f.w;
-        }
-      }
+    for (int j = 0; j < 4; j++) {
+      const float4 f = __ldg(src + j);
+      const float nan = __int_as_float(0x7fffffff);
+      cs[2 * j] = known ? f.x : nan;
+      sn[2 * j] = known ? f.y : nan;
+      cs[2 * j + 1] = known ? f.z : nan;
+      sn[2 * j + 1] = known ? f.w : nan;
     }
-    // the partner's sign: the first of a pair gets -b sin, the second +a sin
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-      if (NEIGHBOURS ? (j & 1) == 0 : e0 < half) sn[j] = -sn[j];
   }
   const int64_t slot = a.slot[t];
   const bool stored = slot >= 0 && slot < a.n_slots;
-  const int64_t place = (slot >> a.log2_bs) * a.s_block + (slot & ((1 << a.log2_bs) - 1)) * a.s_token + e0;
-  // the lane that holds the other halves of the pairs
-  const int partner = (lane - l) + (e0 < half ? l + half / 8 : l - half / 8);
+  const int64_t place = (slot >> a.log2_bs) * a.s_block + (slot & ((1 << a.log2_bs) - 1)) * a.s_token;
+  const int pq = (a.hq + HEADS - 1) / HEADS, pk = (a.hk + HEADS - 1) / HEADS;
+  const int first = (int)(w - t * a.chunks) * a.passes;
+  const T* row = static_cast<const T*>(a.qkv) + t * a.row_stride;
 
+#pragma unroll 1
+  for (int kind = 0; kind < 3; kind++) {  // queries, keys, values
+    const int base = kind == 0 ? 0 : kind == 1 ? pq : pq + pk, n = kind == 0 ? pq : pk, heads = kind == 0 ? a.hq : a.hk;
+    const int lo = max(0, first - base), hi = min(n, first + a.passes - base);
+    if (lo >= hi) continue;
+    const T* src = row + (int64_t)(kind == 0 ? 0 : kind == 1 ? a.hq : a.hq + a.hk) * a.dim;
+    T* dst = kind == 0 ? static_cast<T*>(a.q) + t * a.hq * a.dim : static_cast<T*>(kind == 1 ? a.k : a.v) + place;
+    const int64_t step = kind == 0 ? a.dim : a.s_head;
+    const bool write = in_dim && (kind == 0 || stored);
+    const float* gain = kind == 0 ? a.q_gain : a.k_gain;
+    // (x0, x1) -> (x0 f00 + x1 f01, x1 f11 + x0 f10), two pairs a register
+    uint64_t f00[4], f01[4], f10[4], f11[4];
+    if (kind < 2) {
+      float g0[8], g1[8];
 #pragma unroll
-  for (int i = 0; i < APPEND_PASSES; i++) {
-    const int h = h0 + i * HEADS;
-    float y[8];
-    float ss = 0.f;
+      for (int j = 0; j < 8; j++) g0[j] = g1[j] = 1.f;
+      if (gain && in_dim) {
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const float2 f = P::up(x[i].p[j]);
-      y[2 * j] = f.x;
-      y[2 * j + 1] = f.y;
-      ss += f.x * f.x + f.y * f.y;
-    }
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float* gain = h < a.hq ? a.q_gain : a.k_gain;
-    if (gain && in_dim && h < turned) {
-      const float inv = 1.f / sqrtf(ss / (float)a.dim + a.eps);
-      const float4 g0 = __ldg(reinterpret_cast<const float4*>(gain + e0)),
-                   g1 = __ldg(reinterpret_cast<const float4*>(gain + e0) + 1);
-      y[0] *= inv * g0.x; y[1] *= inv * g0.y; y[2] *= inv * g0.z; y[3] *= inv * g0.w;
-      y[4] *= inv * g1.x; y[5] *= inv * g1.y; y[6] *= inv * g1.z; y[7] *= inv * g1.w;
-    }
-    if (a.rot) {
-      float z[8];
-#pragma unroll
-      for (int j = 0; j < 8; j++) z[j] = NEIGHBOURS ? y[j ^ 1] : __shfl_sync(0xffffffffu, y[j], partner & 31);
-      if (rotated && h < turned)
-#pragma unroll
-        for (int j = 0; j < 8; j++) y[j] = y[j] * cs[j] + z[j] * sn[j];
-    }
-    if (in_dim && h < all) {
-      Vec o;
-      if (h < turned) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) o.p[j] = P::down(y[2 * j], y[2 * j + 1]);
-      } else {
-        o.u = x[i].u;
+        for (int j = 0; j < 2; j++) {
+          const float4 x = __ldg(reinterpret_cast<const float4*>(gain + e0) + j), y = __ldg(reinterpret_cast<const float4*>(gain + e1) + j);
+          g0[4 * j] = x.x; g0[4 * j + 1] = x.y; g0[4 * j + 2] = x.z; g0[4 * j + 3] = x.w;
+          g1[4 * j] = y.x; g1[4 * j + 1] = y.y; g1[4 * j + 2] = y.z; g1[4 * j + 3] = y.w;
+        }
       }
-      if (h < a.hq)
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.q) + (t * a.hq + h) * a.dim + e0) = o.u;
-      else if (stored && h < turned)
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.k) + place + (h - a.hq) * a.s_head) = o.u;
-      else if (stored)
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.v) + place + (h - turned) * a.s_head) = o.u;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        if (!rotated) {
+          f00[j] = pair64(g0[2 * j], g0[2 * j + 1]);
+          f11[j] = pair64(g1[2 * j], g1[2 * j + 1]);
+        } else if (NEIGHBOURS) {
+          // registers are the pairs themselves: run 0 has pairs 0-3, run 1 pairs 4-7; the second
+          // factors go to the neighbour, swapped
+          f00[j] = pair64(g0[2 * j] * cs[j], g0[2 * j + 1] * cs[j]);
+          f01[j] = pair64(-g0[2 * j + 1] * sn[j], g0[2 * j] * sn[j]);
+          f11[j] = pair64(g1[2 * j] * cs[4 + j], g1[2 * j + 1] * cs[4 + j]);
+          f10[j] = pair64(-g1[2 * j + 1] * sn[4 + j], g1[2 * j] * sn[4 + j]);
+        } else {
+          f00[j] = pair64(g0[2 * j] * cs[2 * j], g0[2 * j + 1] * cs[2 * j + 1]);
+          f01[j] = pair64(-g1[2 * j] * sn[2 * j], -g1[2 * j + 1] * sn[2 * j + 1]);
+          f11[j] = pair64(g1[2 * j] * cs[2 * j], g1[2 * j + 1] * cs[2 * j + 1]);
+          f10[j] = pair64(g0[2 * j] * sn[2 * j], g0[2 * j + 1] * sn[2 * j + 1]);
+        }
+      }
+    }
+#pragma unroll 1
+    for (int p = lo; p < hi; p += APPEND_FLIGHT) {
+      Vec x[APPEND_FLIGHT][2];
+#pragma unroll
+      for (int i = 0; i < APPEND_FLIGHT; i++) {
+        const int h = (p + i) * HEADS + lane / LANES;
+        const bool in = in_dim && p + i < hi && h < heads;
+        x[i][0].u = in ? *reinterpret_cast<const uint4*>(src + h * a.dim + e0) : make_uint4(0, 0, 0, 0);
+        x[i][1].u = in ? *reinterpret_cast<const uint4*>(src + h * a.dim + e1) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < APPEND_FLIGHT; i++) {
+        if (p + i >= hi) break;
+        const int h = (p + i) * HEADS + lane / LANES;
+        if (kind < 2) {
+          uint64_t y0[4], y1[4], ss = 0, ss2 = 0;
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const float2 u = P::up(x[i][0].p[j]), v = P::up(x[i][1].p[j]);
+            y0[j] = pair64(u.x, u.y);
+            y1[j] = pair64(v.x, v.y);
+            ss = fma2(y0[j], y0[j], ss);
+            ss2 = fma2(y1[j], y1[j], ss2);
+          }
+          if (gain) {
+            const float2 s2 = unpair64(add2(ss, ss2));
+            float s = s2.x + s2.y;
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            const float inv = rsqrtf(s / (float)a.dim + a.eps);
+            const uint64_t inv2 = pair64(inv, inv);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+              y0[j] = mul2(y0[j], inv2);
+              y1[j] = mul2(y1[j], inv2);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            uint64_t z0 = mul2(y0[j], f00[j]), z1 = mul2(y1[j], f11[j]);
+            if (rotated) {
+              if (NEIGHBOURS) {
+                const float2 u = unpair64(y0[j]), v = unpair64(y1[j]);
+                z0 = fma2(pair64(u.y, u.x), f01[j], z0);
+                z1 = fma2(pair64(v.y, v.x), f10[j], z1);
+              } else {
+                z0 = fma2(y1[j], f01[j], z0);
+                z1 = fma2(y0[j], f10[j], z1);
+              }
+            }
+            const float2 u = unpair64(z0), v = unpair64(z1);
+            x[i][0].p[j] = P::down(u.x, u.y);
+            x[i][1].p[j] = P::down(v.x, v.y);
+          }
+        }
+        if (write && h < heads) {
+          *reinterpret_cast<uint4*>(dst + h * step + e0) = x[i][0].u;
+          *reinterpret_cast<uint4*>(dst + h * step + e1) = x[i][1].u;
+        }
+      }
     }
   }
 }
 
 template <class T, int LANES>
-static void append_launch(const AppendArgs& a, bool neighbours, cudaStream_t st) {
-  const int64_t warps = a.T * a.chunks;
-  const unsigned grid = (unsigned)((warps * 32 + APPEND_THREADS - 1) / APPEND_THREADS);
+static void append_launch(AppendArgs& a, bool neighbours, int sms, cudaStream_t st) {
+  constexpr int HEADS = 32 / LANES;
+  const int all = (a.hq + HEADS - 1) / HEADS + 2 * ((a.hk + HEADS - 1) / HEADS);
+  // a warp takes a token, or less of it while that fills the GPU's SMs with 16 warps each
+  const int64_t enough = (int64_t)sms * 16;
+  a.chunks = (int)std::min<int64_t>(all, std::max<int64_t>(1, enough / std::max<int64_t>(a.T, 1)));
+  a.passes = (all + a.chunks - 1) / a.chunks;
+  a.chunks = (all + a.passes - 1) / a.passes;
+  const unsigned grid = (unsigned)((a.T * a.chunks * 32 + APPEND_THREADS - 1) / APPEND_THREADS);
   if (neighbours) k_kv_append<T, LANES, true><<<grid, APPEND_THREADS, 0, st>>>(a);
   else k_kv_append<T, LANES, false><<<grid, APPEND_THREADS, 0, st>>>(a);
 }
 
 template <class T>
-static void append_lanes(AppendArgs& a, bool neighbours, cudaStream_t st) {
-  const int lanes = a.dim <= 64 ? 8 : a.dim <= 128 ? 16 : 32;
-  const int heads = 32 / lanes * APPEND_PASSES;
-  a.chunks = (a.hq + 2 * a.hk + heads - 1) / heads;
-  if (lanes == 8) append_launch<T, 8>(a, neighbours, st);
-  else if (lanes == 16) append_launch<T, 16>(a, neighbours, st);
-  else append_launch<T, 32>(a, neighbours, st);
+static void append_lanes(AppendArgs& a, bool neighbours, int sms, cudaStream_t st) {
+  if (a.dim <= 64) append_launch<T, 4>(a, neighbours, sms, st);
+  else if (a.dim <= 128) append_launch<T, 8>(a, neighbours, sms, st);
+  else append_launch<T, 16>(a, neighbours, sms, st);
 }
 
 }  // namespace tk
@@ -464,8 +507,9 @@ extern "C" int tk_kv_cache_create(void* d_k, void* d_v, int type, int64_t n_bloc
       return kv_arg(where, "a stride is below head_dim, no multiple of 8 elements, or 2^38 and more");
   }
   if (!aligned16(d_k) || !aligned16(d_v)) return kv_arg(where, "keys or values are not 16-byte aligned");
-  int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
+  int dev = 0, sms = 1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) {
     tk_set_error("%s: %s", where, cudaGetErrorString(e));
     return TK_E_CUDA;
@@ -476,6 +520,7 @@ extern "C" int tk_kv_cache_create(void* d_k, void* d_v, int type, int64_t n_bloc
     return TK_E_NOMEM;
   }
   c->device = dev;
+  c->sms = sms;
   c->type = type;
   c->n_blocks = n_blocks;
   c->n_heads = n_heads;
@@ -517,9 +562,9 @@ extern "C" int tk_kv_append(const tk_kv_cache* cache, const void* d_qkv, int64_t
     return kv_arg(where, "a buffer is not 16-byte aligned");
   AppendArgs a = {d_qkv, row_stride, T, n_q_heads, cache->n_heads, cache->head_dim, d_q_gain, d_k_gain, eps, d_rope,
                   rope_len, rot_dim, d_pos, d_slot, d_q, cache->k, cache->v, cache->stride[0], cache->stride[1],
-                  cache->stride[2], cache->n_blocks << cache->log2_block, cache->log2_block, 0};
-  if (cache->type == TK_BF16) append_lanes<__nv_bfloat16>(a, neighbours != 0, (cudaStream_t)cuda_stream);
-  else append_lanes<__half>(a, neighbours != 0, (cudaStream_t)cuda_stream);
+                  cache->stride[2], cache->n_blocks << cache->log2_block, cache->log2_block, 0, 0};
+  if (cache->type == TK_BF16) append_lanes<__nv_bfloat16>(a, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);
+  else append_lanes<__half>(a, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     tk_set_error("%s: %s", where, cudaGetErrorString(e));

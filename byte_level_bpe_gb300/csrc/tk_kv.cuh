@@ -44,7 +44,7 @@ struct Pair<__half> {
 }  // namespace tk
 
 struct tk_kv_cache {
-  int device;
+  int device, sms;
   int type;
   int64_t n_blocks;
   int n_heads, block_size, log2_block, head_dim;

@@ -14,26 +14,50 @@ from typing import NamedTuple
 from . import native
 
 
-def _torch():
-    import torch
-    if not torch.cuda.is_available():
-        raise RuntimeError("byte_level_bpe_gb300 needs a CUDA device (no CPU fallback)")
-    return torch
+_T = None  # torch, once a CUDA device has been seen
+_raw_stream = None
 
+
+def _torch():
+    global _T, _raw_stream
+    if _T is None:
+        import torch
+        if not torch.cuda.is_available():
+            raise RuntimeError("byte_level_bpe_gb300 needs a CUDA device (no CPU fallback)")
+        # the current stream's handle without the object around it, where torch has that
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _T = torch
+    return _T
+
+
+# These calls take a few microseconds on the GPU for a decode step, so the checks
+# are written for few Python operations: devices are compared as indices.
 
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
-def _stream(torch, stream, device):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+def _stream(stream, index):
+    return stream.cuda_stream if stream is not None else _raw_stream(index)
 
 
-def _vector(x, name, dtype, n, device):
-    _need(x.dtype == dtype and x.dim() == 1 and x.numel() == n and x.is_contiguous() and x.device == device,
-          f"{name} must be a contiguous {dtype} vector of {n} on {device}")
+def _vector(x, name, dtype, n, index):
+    if x.dtype is not dtype or x.shape != (n,) or x.get_device() != index or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} on cuda:{index}")
     return x.data_ptr()
+
+
+def _table(table, R, dtype, index):
+    """(address, row stride, width) of a block table."""
+    if table.dim() != 2 or table.dtype is not dtype or table.get_device() != index or index < 0 or table.shape[0] != R:
+        raise ValueError("table must be int32[R, W] on the GPU, like the other tensors")
+    stride, unit = table.stride()
+    W = table.shape[1]
+    if unit != 1 and W > 1:
+        raise ValueError("the rows of table must be contiguous")
+    return table.data_ptr(), stride if R > 1 and stride > W else W, W
 
 
 class KVPlan(NamedTuple):
@@ -54,31 +78,30 @@ def kv_plan(offsets, context, table, free, block_size, n_tokens, parents=None, c
     the rest is padding), parents int32[T] for drafted trees, cursor: one
     int64 on the device, e.g. an earlier plan's info[:1]."""
     torch = _torch()
-    dev = table.device
-    R, T = context.numel(), int(n_tokens)
-    _need(table.dim() == 2 and table.shape[0] == R and table.dtype == torch.int32 and table.is_cuda
-          and (table.shape[1] < 2 or table.stride(1) == 1), "table must be int32[R, W] on the GPU, rows contiguous")
-    _need(free.dim() == 1, "free must be a vector")
+    index = table.get_device()
     i32, i64 = torch.int32, torch.int64
-    p_off = _vector(offsets, "offsets", i64, R + 1, dev)
-    p_ctx = _vector(context, "context", i32, R, dev)
-    p_free = _vector(free, "free", i32, free.numel(), dev)
-    p_par = _vector(parents, "parents", i32, T, dev) if parents is not None else None
-    p_cur = _vector(cursor, "cursor", i64, 1, dev) if cursor is not None else None
-    # one allocation, cut at multiples of 16 bytes: slots, masks, info, positions, requests, lengths
-    t4 = (T + 3) & ~3
-    words = torch.empty((3 if parents is not None else 2) * t4 + 4 + (R + 1) // 2, dtype=i64, device=dev)
-    slots, rest = words[:T], words[t4:]
-    masks = None
+    R, T = context.numel(), n_tokens
+    p_table, stride, W = _table(table, R, i32, index)
+    p_off = _vector(offsets, "offsets", i64, R + 1, index)
+    p_ctx = _vector(context, "context", i32, R, index)
+    n_free = free.numel()
+    p_free = _vector(free, "free", i32, n_free, index)
+    p_cur = _vector(cursor, "cursor", i64, 1, index) if cursor is not None else None
+    # an allocation each: on the host they are cheaper than views of a common one
+    empty, device = torch.empty, table.device
+    positions, slots = empty(T, dtype=i32, device=device), empty(T, dtype=i64, device=device)
+    requests, lengths = empty(T, dtype=i32, device=device), empty(R, dtype=i32, device=device)
+    info = empty(4, dtype=i64, device=device)
+    p_par, masks, p_mask = None, None, None
     if parents is not None:
-        masks, rest = rest[:T], rest[t4:]
-    info, small = rest[:4], rest[4:].view(i32)
-    positions, requests, lengths = small[:T], small[t4:t4 + T], small[2 * t4:2 * t4 + R]
-    stride = table.stride(0) if R > 1 else table.shape[1]
-    native.tk_kv_plan(p_off, p_ctx, R, T, block_size, table.data_ptr(), max(stride, table.shape[1]), table.shape[1],
-                      p_free, free.numel(), p_cur, p_par, positions.data_ptr(), slots.data_ptr(),
-                      requests.data_ptr(), lengths.data_ptr(), masks.data_ptr() if masks is not None else None,
-                      info.data_ptr(), _stream(torch, stream, dev))
+        p_par = _vector(parents, "parents", i32, T, index)
+        masks = empty(T, dtype=i64, device=device)
+        p_mask = masks.data_ptr()
+    rc = native.load().tk_kv_plan(p_off, p_ctx, R, T, block_size, p_table, stride, W, p_free, n_free, p_cur, p_par,
+                                  positions.data_ptr(), slots.data_ptr(), requests.data_ptr(), lengths.data_ptr(), p_mask,
+                                  info.data_ptr(), _stream(stream, index))
+    if rc:
+        native.check(rc, "tk_kv_plan")
     return KVPlan(positions, slots, requests, lengths, info, masks)
 
 
@@ -103,7 +126,7 @@ class KVWorkspace:
         """Waits for the stream; raises TkError for the first request that an
         attend on this workspace could not take (tk_kv_status)."""
         torch = _torch()
-        native.tk_kv_status(self._h, _stream(torch, stream, None))
+        native.tk_kv_status(self._h, _stream(stream, torch.cuda.current_device()))
 
     def close(self):
         if self._h is not None:
@@ -131,6 +154,7 @@ class KVCache:
         _need(k.stride(3) == 1, "the last dimension must be contiguous")
         self._h = None
         self.k, self.v, self.device, self.dtype = k, v, k.device, k.dtype
+        self._index = k.get_device()
         self.n_blocks, self.kv_heads, self.block_size, self.head_dim = k.shape
         # the stride of a dimension of one element is arbitrary in torch
         d = self.head_dim
@@ -146,29 +170,34 @@ class KVCache:
         stored at `slots` (tk_kv_append). gains float32[head_dim], rope
         float32[n, rot_dim / 2, 2] (`rope_table`)."""
         torch = _torch()
-        dev, d = self.device, self.head_dim
-        _need(qkv.dim() == 2 and qkv.dtype == self.dtype and qkv.device == dev
-              and qkv.shape[1] == (q_heads + 2 * self.kv_heads) * d and qkv.stride(1) == 1,
-              f"qkv must be {self.dtype}[T, (q_heads + 2 kv_heads) * head_dim] on {dev}, rows contiguous")
-        T = qkv.shape[0]
+        index, d = self._index, self.head_dim
+        T, width = qkv.shape  # a ValueError if there are not two dimensions
+        row, unit = qkv.stride()
+        if (qkv.dtype is not self.dtype or qkv.get_device() != index or width != (q_heads + 2 * self.kv_heads) * d
+                or unit != 1):
+            raise ValueError(f"qkv must be {self.dtype}[T, (q_heads + 2 kv_heads) * head_dim] on cuda:{index}, "
+                             "rows contiguous")
         f32 = torch.float32
-        p_qg = _vector(q_gain, "q_gain", f32, d, dev) if q_gain is not None else None
-        p_kg = _vector(k_gain, "k_gain", f32, d, dev) if k_gain is not None else None
+        p_qg = _vector(q_gain, "q_gain", f32, d, index) if q_gain is not None else None
+        p_kg = _vector(k_gain, "k_gain", f32, d, index) if k_gain is not None else None
         p_rope, n_rope, rot, p_pos = None, 0, 0, None
         if rope is not None:
-            _need(rope.dim() == 3 and rope.shape[2] == 2 and rope.dtype == f32 and rope.is_contiguous()
-                  and rope.device == dev, f"rope must be a contiguous float32[n, rot_dim / 2, 2] on {dev}")
-            p_rope, n_rope, rot = rope.data_ptr(), rope.shape[0], 2 * rope.shape[1]
-            p_pos = _vector(positions, "positions", torch.int32, T, dev)
-        p_slot = _vector(slots, "slots", torch.int64, T, dev)
+            n_rope, rot, two = rope.shape
+            if two != 2 or rope.dtype is not f32 or not rope.is_contiguous() or rope.get_device() != index:
+                raise ValueError(f"rope must be a contiguous float32[n, rot_dim / 2, 2] on cuda:{index}")
+            p_rope, rot = rope.data_ptr(), 2 * rot
+            p_pos = _vector(positions, "positions", torch.int32, T, index)
+        p_slot = _vector(slots, "slots", torch.int64, T, index)
         if out is None:
-            out = torch.empty((T, q_heads, d), dtype=self.dtype, device=dev)
-        else:
-            _need(out.shape == (T, q_heads, d) and out.dtype == self.dtype and out.is_contiguous() and out.device == dev,
-                  "out must be a contiguous tensor [T, q_heads, head_dim] of the cache's type")
-        native.tk_kv_append(self._h, qkv.data_ptr(), max(qkv.stride(0), qkv.shape[1]) if T > 1 else qkv.shape[1], T,
-                            q_heads, p_qg, p_kg, eps, p_rope, n_rope, rot, neighbours, p_pos, p_slot, out.data_ptr(),
-                            _stream(torch, stream, dev))
+            out = torch.empty((T, q_heads, d), dtype=self.dtype, device=self.device)
+        elif (out.shape != (T, q_heads, d) or out.dtype is not self.dtype or not out.is_contiguous()
+              or out.get_device() != index):
+            raise ValueError("out must be a contiguous tensor [T, q_heads, head_dim] of the cache's type")
+        rc = native.load().tk_kv_append(self._h, qkv.data_ptr(), row if T > 1 and row > width else width, T, q_heads, p_qg,
+                                        p_kg, eps, p_rope, n_rope, rot, 1 if neighbours else 0, p_pos, p_slot,
+                                        out.data_ptr(), _stream(stream, index))
+        if rc:
+            native.check(rc, "tk_kv_append")
         return out
 
     def attend(self, q, offsets, lengths, table, workspace, masks=None, scale=None, max_new=None, lse=False,
@@ -179,28 +208,28 @@ class KVCache:
         defaults to head_dim^-0.5; max_new: no request has more new tokens
         (T if not given). lse=True also returns float32[T, q_heads]."""
         torch = _torch()
-        dev, d = self.device, self.head_dim
-        _need(q.dim() == 3 and q.shape[2] == d and q.dtype == self.dtype and q.device == dev and q.stride(2) == 1
-              and (q.stride(1) == d or q.shape[1] == 1),
-              f"q must be {self.dtype}[T, q_heads, head_dim] on {dev}, the heads of a token contiguous")
-        T, hq = q.shape[0], q.shape[1]
+        index, d = self._index, self.head_dim
+        T, hq, width = q.shape  # a ValueError if there are not three dimensions
+        step, head, unit = q.stride()
+        if (width != d or q.dtype is not self.dtype or q.get_device() != index or unit != 1
+                or (head != d and hq > 1)):
+            raise ValueError(f"q must be {self.dtype}[T, q_heads, head_dim] on cuda:{index}, the heads of a token contiguous")
         R = lengths.numel()
-        _need(table.dim() == 2 and table.shape[0] == R and table.dtype == torch.int32 and table.device == dev
-              and (table.shape[1] < 2 or table.stride(1) == 1), f"table must be int32[R, W] on {dev}, rows contiguous")
-        p_off = _vector(offsets, "offsets", torch.int64, R + 1, dev)
-        p_len = _vector(lengths, "lengths", torch.int32, R, dev)
-        p_mask = _vector(masks, "masks", torch.int64, T, dev) if masks is not None else None
+        p_table, stride, W = _table(table, R, torch.int32, index)
+        p_off = _vector(offsets, "offsets", torch.int64, R + 1, index)
+        p_len = _vector(lengths, "lengths", torch.int32, R, index)
+        p_mask = _vector(masks, "masks", torch.int64, T, index) if masks is not None else None
         if out is None:
-            out = torch.empty((T, hq, d), dtype=self.dtype, device=dev)
-        else:
-            _need(out.shape == q.shape and out.dtype == self.dtype and out.is_contiguous() and out.device == dev,
-                  "out must be a contiguous tensor of q's shape and type")
-        sums = torch.empty((T, hq), dtype=torch.float32, device=dev) if lse else None
-        W = table.shape[1]
-        native.tk_kv_attend(self._h, workspace._h, q.data_ptr(), q.stride(0) if T > 1 else hq * d, hq, p_off, R, T,
-                            T if max_new is None else max_new, p_len, table.data_ptr(),
-                            max(table.stride(0), W) if R > 1 else W, W, p_mask, d ** -0.5 if scale is None else scale,
-                            out.data_ptr(), sums.data_ptr() if lse else None, _stream(torch, stream, dev))
+            out = torch.empty((T, hq, d), dtype=self.dtype, device=self.device)
+        elif out.shape != q.shape or out.dtype is not self.dtype or not out.is_contiguous() or out.get_device() != index:
+            raise ValueError("out must be a contiguous tensor of q's shape and type")
+        sums = torch.empty((T, hq), dtype=torch.float32, device=self.device) if lse else None
+        rc = native.load().tk_kv_attend(self._h, workspace._h, q.data_ptr(), step if T > 1 else hq * d, hq, p_off, R, T,
+                                        T if max_new is None else max_new, p_len, p_table, stride, W, p_mask,
+                                        d ** -0.5 if scale is None else scale, out.data_ptr(),
+                                        sums.data_ptr() if lse else None, _stream(stream, index))
+        if rc:
+            native.check(rc, "tk_kv_attend")
         return (out, sums) if lse else out
 
     def close(self):
