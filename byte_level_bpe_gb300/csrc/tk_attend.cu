@@ -15,13 +15,13 @@
 // cores ask for: an error of half an ulp in each weight.
 #include <algorithm>
 #include <new>
+#include <type_traits>
 
 #include "tk_blackwell.cuh"
 #include "tk_kv.cuh"
 
 namespace tk {
 
-constexpr int AT_KEYS = 64;      // keys of a tile
 constexpr int AT_THREADS = 384;  // loads and products of two streams (4 warps), their softmax (2 x 4 warps)
 constexpr int AT_UNIT_COST = 2;  // what starting a unit costs, in tiles
 constexpr int AT_MIN_SHARE = 8;  // least share of a worker, in tiles
@@ -78,7 +78,12 @@ __device__ __forceinline__ int unit_keys(const AttendArgs& a, const Request& q, 
   if (a.mask || !q.good) return q.len;
   return q.ctx + (min(q.n * a.group, row0 + ROWS) - 1) / a.group + 1;
 }
-__device__ __forceinline__ int key_tiles(int keys) { return max(1, (keys + AT_KEYS - 1) / AT_KEYS); }
+// Tiles of a 256-row unit have 128 keys, the others' 64 (see AttendShape).
+template <int ROWS>
+__device__ __forceinline__ int key_tiles(int keys) {
+  constexpr int KEYS = ROWS == 256 ? 128 : 64;
+  return max(1, (keys + KEYS - 1) / KEYS);
+}
 
 // How the work is divided.  It is one line of units (request, row tile, key
 // head), each AT_UNIT_COST + its key tiles long; worker w has it from w * share to
@@ -101,7 +106,7 @@ __device__ __forceinline__ UnitSum request_work(const AttendArgs& a, const Reque
   const int rows = q.n * a.group;
   const bool same = a.mask || !q.good || rows <= ROWS;  // every row tile has the request's keys
   for (int row0 = 0; row0 < rows; row0 += ROWS) {
-    const int cost = key_tiles(unit_keys<ROWS>(a, q, row0)) + AT_UNIT_COST;
+    const int cost = key_tiles<ROWS>(unit_keys<ROWS>(a, q, row0)) + AT_UNIT_COST;
     const int tiles = same ? (rows + ROWS - 1) / ROWS : 1;
     w.length += (plan.padded ? ((unsigned)(cost + plan.share - 1) / (unsigned)plan.share) * plan.share : cost) * tiles;
     w.units += tiles;
@@ -136,7 +141,7 @@ struct Walk {
 
   __device__ __forceinline__ void row_tile(const AttendArgs& a) {
     keys = unit_keys<ROWS>(a, q, row0);
-    cost = length = key_tiles(keys) + AT_UNIT_COST;
+    cost = length = key_tiles<ROWS>(keys) + AT_UNIT_COST;
     if (plan.padded) {
       pieces = (unsigned)(cost + plan.share - 1) / (unsigned)plan.share;
       size = (unsigned)(cost + pieces - 1) / (unsigned)pieces;
@@ -251,12 +256,14 @@ template <int D, int MODE>
 struct AttendShape {
   static constexpr int RINGS = MODE == 2 ? 1 : 2, ROWS = MODE == 0 ? 32 : MODE == 1 ? 128 : 256;
   static constexpr int Q_ROWS = MODE == 0 ? 32 : 128;  // of a stream
-  static constexpr int Q = Q_ROWS * D * 2, STAGE = AT_KEYS * D * 2;
+  static constexpr int KEYS = MODE == 2 ? 128 : 64, BUFS = 128 / KEYS;  // keys of a tile; tiles' scores in tensor memory
+  static constexpr int Q = Q_ROWS * D * 2, STAGE = KEYS * D * 2;
   static constexpr int STAGES = (RINGS == 1 ? 160 : MODE == 0 ? 96 : 80) * 1024 / STAGE;  // of a ring
   static constexpr int RING = 2 * Q;
-  // barriers: full and empty of the stages; pieces handed over and taken; per stream q, s (2), p (2), v, o ready, o free, drain
+  // barriers: full and empty of the stages; pieces handed over and taken; per stream q, s (2), p (2), v, o ready, o free, drain,
+  // turn
   static constexpr int BARS = RING + RINGS * STAGES * STAGE;
-  static constexpr int N_BARS = RINGS * (2 * STAGES + 2 * AT_PIECES) + 2 * 9;
+  static constexpr int N_BARS = RINGS * (2 * STAGES + 2 * AT_PIECES) + 2 * 10;
   static constexpr int PIECES = BARS + 8 * N_BARS;
   static constexpr int SMALL = PIECES + RINGS * AT_PIECES * (int)sizeof(Piece);
   // start of the walk (2 x 2), sums, units and longest of the warps, tensor memory, abort, non-finite values (2 x 8)
@@ -283,7 +290,7 @@ template <class T, int D, int MODE>
 __global__ void __launch_bounds__(AT_THREADS, 1)
 k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   using L = AttendShape<D, MODE>;
-  constexpr int ROWS = L::ROWS, HALVES = D / 64, NST = L::STAGES;
+  constexpr int ROWS = L::ROWS, KEYS = L::KEYS, BUFS = L::BUFS, HALVES = D / 64, NST = L::STAGES;
   constexpr bool BF = Pair<T>::BF;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle goes by address bits
   const uint32_t base = smem_addr(smem);
@@ -293,8 +300,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
   const uint32_t s_ring = base + L::RING + ring * (NST * L::STAGE), s_q = base + stream * L::Q;
   const uint32_t b_full = base + L::BARS + ring * 8 * (2 * NST + 2 * AT_PIECES), b_empty = b_full + 8 * NST,
                  b_piece = b_empty + 8 * NST, b_taken = b_piece + 8 * AT_PIECES;
-  const uint32_t b_q = base + L::BARS + L::RINGS * 8 * (2 * NST + 2 * AT_PIECES) + stream * 72, b_s = b_q + 8, b_p = b_s + 16,
-                 b_v = b_p + 16, b_o = b_v + 8, b_free = b_o + 8, b_drain = b_free + 8;
+  const uint32_t b_q = base + L::BARS + L::RINGS * 8 * (2 * NST + 2 * AT_PIECES) + stream * 80, b_s = b_q + 8, b_p = b_s + 16,
+                 b_v = b_p + 16, b_o = b_v + 8, b_free = b_o + 8, b_drain = b_free + 8, b_turn = b_drain + 8;
   Piece* s_piece = reinterpret_cast<Piece*>(smem + L::PIECES) + ring * AT_PIECES;
   int* s_walk = reinterpret_cast<int*>(smem + L::SMALL);  // of each worker: first request, where it starts
   int* s_sum = s_walk + 4;
@@ -316,7 +323,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         if (in >= NST && in < 2 * NST) count = MODE == 2 ? 2 : 1;                // empty: the streams that read the stage
         else if (in >= 2 * NST + AT_PIECES) count = MODE == 2 ? 10 : 5;          // taken: products and softmax warps
       } else {
-        const int k = st % 9;
+        const int k = st % 10;
         count = k == 0 ? 128 : k == 3 || k == 4 || k == 7 ? 4 : 1;               // q, p, p, o free
       }
       bar_init(base + L::BARS + 8 * i, count);
@@ -431,9 +438,11 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     taken++;
   };
 
+  // registers: 384 x 168 at launch = 128 x 104 + 256 x 200
   if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 0 || (warp == 3 && MODE != 2)) {
-      // ---- loads, in the order of their use: K0 K1 V0 K2 V1 K3 ...
+      // ---- loads, in the order of their use: K0 K1 V0 K2 V1 K3 ... with two tiles' scores, K0 V0 K1 V1 ... with one
       Walk<ROWS> walk;
       walk.plan = plan;
       walk.from = (blockIdx.x * WORKERS + ring) * plan.share;
@@ -453,10 +462,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         __syncwarp();
         at++;
       };
-      // a box is 64 elements of one page, or of half of one of 128; a lane loads one box
-      const int log2_box = min(a.log2_bs, 6), per_page = a.log2_bs - log2_box, ppt = AT_KEYS >> log2_box;
+      // a box is 64 elements of a page's keys, at most 64 of them; a lane loads one box
+      const int log2_box = min(a.log2_bs, 6), per_page = a.log2_bs - log2_box, ppt = KEYS >> log2_box;
       const int my_box = lane / HALVES, my_half = lane % HALVES;
-      const uint32_t my_dst = s_ring + my_half * (AT_KEYS * 128) + (my_box * 128 << log2_box);
+      const uint32_t my_dst = s_ring + my_half * (KEYS * 128) + (my_box * 128 << log2_box);
       const uint32_t box_bytes = HALVES * 128u << log2_box;
       // block ids: a lane has box `window + lane`, and the one 32 further on
       struct Ids {
@@ -483,7 +492,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         if (elect_one()) bar_expect(b_full + 8 * st, nb * box_bytes);
         __syncwarp();
         if (my_box < nb)
-          tma_load_4d(my_dst + st * L::STAGE, map, b_full + 8 * st, my_half * 64, per_page ? (box0 & 1) * AT_KEYS : 0, h, id);
+          tma_load_4d(my_dst + st * L::STAGE, map, b_full + 8 * st, my_half * 64, per_page ? ((box0 + my_box) & 1) * 64 : 0, h, id);
         if (++st == NST) st = 0, ph ^= 1;
       };
       Piece nx;
@@ -499,8 +508,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         k.now = id_of(k.window + lane);
         k.then = id_of(k.window + 32 + lane);
         v = k;
-        load(&map_k, k, lo);
-        if (ok && lo + 1 < hi) load(&map_k, k, lo + 1);
+        for (int t = lo; ok && t < min(hi, lo + BUFS); t++) load(&map_k, k, t);
         for (int t = lo; ok && t < hi; t++) {
           load(&map_v, v, t);
           // the next piece is known to the softmax, which asks for it in its last tile, before
@@ -509,7 +517,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
             walk.next(a, nx);
             hand(nx);
           }
-          if (ok && t + 2 < hi) load(&map_k, k, t + 2);
+          if (ok && t + BUFS < hi) load(&map_k, k, t + BUFS);
         }
       }
       // given up: the copies in flight land before the CTA ends
@@ -521,8 +529,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     } else if (warp == 1 || warp == 2) {
       // ---- products: the warp waits as one, one lane issues (with a branch of its own for
       // the lane every operand would be a divergent one: 120 cycles a product instead of 64)
-      constexpr uint32_t KIND_S = mma_kind(BF, 128, AT_KEYS, false), KIND_O = mma_kind(BF, 128, D, true);
-      uint32_t st = 0, ph = 0, units = 0, nt = 0;  // stage, its parity; units, tiles so far
+      constexpr uint32_t KIND_S = mma_kind(BF, 128, KEYS, false), KIND_O = mma_kind(BF, 128, D, true);
+      uint32_t st = 0, ph = 0, units = 0, nt = 0, turns = 0;  // stage, its parity; units, tiles, turns so far
       bool ok = true;
       const uint32_t q = mma_desc(s_q, 16);
       auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity, abort)) != 0; };
@@ -534,8 +542,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         const uint32_t k = mma_desc(s_ring + at * L::STAGE, 16);
 #pragma unroll
         for (int i = 0; i < D / 16; i++)
-          mma_ss(stream * 256 + buf * 64, q + (((i >> 2) * (L::Q_ROWS * 128) + (i & 3) * 32) >> 4),
-                 k + (((i >> 2) * (AT_KEYS * 128) + (i & 3) * 32) >> 4), KIND_S, i > 0);
+          mma_ss(stream * 256 + buf * KEYS, q + (((i >> 2) * (L::Q_ROWS * 128) + (i & 3) * 32) >> 4),
+                 k + (((i >> 2) * (KEYS * 128) + (i & 3) * 32) >> 4), KIND_S, i > 0);
         mma_commit(b_s + 8 * buf);
         mma_commit(b_empty + 8 * at);
       };
@@ -543,6 +551,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         const Piece& p = s_piece[taken % AT_PIECES];
         const int n = __shfl_sync(0xffffffffu, p.hi - p.lo, 0), rows = __shfl_sync(0xffffffffu, p.rows, 0);
         release();
+        const bool turn = MODE == 2 && rows > 128;
         if (MODE == 2 && stream * 128 >= rows) {  // no rows for this stream
           for (int i = 0; ok && i < 2 * n; i++, advance()) {
             ok = full();
@@ -551,10 +560,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           continue;
         }
         if (!(ok = wait(b_q, units & 1))) break;
-        for (int t = 0; t < min(n, 2); t++, advance()) {
+        for (int t = 0; t < min(n, BUFS); t++, advance()) {
           if (!(ok = full())) break;
           tmem_fence_after();
-          if (elect_one()) scores((nt + t) & 1, st);
+          if (elect_one()) scores((nt + t) % BUFS, st);
           __syncwarp();
         }
         // the first output of a unit when the last one's has been read
@@ -562,26 +571,29 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         for (int t = 0; t < n; t++, nt++) {
           // what is there early is waited for first: nothing but the weights is on the way from them to
           // the next scores
-          const uint32_t sv = st, buf = nt & 1;
+          const uint32_t sv = st, buf = nt % BUFS;
           if (!(ok = full())) break;
           advance();
           const uint32_t sk = st;
-          const bool more = t + 2 < n;
+          const bool more = t + BUFS < n;
           if (more) {
             if (!(ok = full())) break;
             advance();
           }
-          const uint32_t v = mma_desc(s_ring + sv * L::STAGE, AT_KEYS * 128);
-          if (!(ok = wait(b_p + 8 * buf, (nt >> 1) & 1))) break;
+          const uint32_t v = mma_desc(s_ring + sv * L::STAGE, KEYS * 128);
+          if (!(ok = wait(b_p + 8 * buf, (nt / BUFS) & 1))) break;
+          if (turn && (stream || turns > 0) && !(ok = wait(stream ? b_turn - 80 : b_turn + 80, (turns + 1 - stream) & 1))) break;
+          turns += turn;
           tmem_fence_after();
           if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < AT_KEYS / 16; i++)  // O += P V
-              mma_ts(stream * 256 + 128, stream * 256 + buf * 64 + i * 8, v + i * (2048 >> 4), KIND_O, t > 0 || i > 0);
+            for (int i = 0; i < KEYS / 16; i++)  // O += P V
+              mma_ts(stream * 256 + 128, stream * 256 + buf * KEYS + i * 8, v + i * (2048 >> 4), KIND_O, t > 0 || i > 0);
             mma_commit(b_v);
             mma_commit(b_empty + 8 * sv);
             if (t == n - 1) mma_commit(b_o);
             if (more) scores(buf, sk);
+            if (turn) bar_arrive(b_turn);
           }
           __syncwarp();
         }
@@ -596,6 +608,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     }
     __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax
     const int wq = warp & 3, row = wq * 32 + lane;  // row = also its lane of tensor memory
     const uint32_t t_s = ((uint32_t)(wq * 32) << 16) + stream * 256, t_o = t_s + 128;
@@ -660,68 +673,30 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         seen.mask = (uint64_t)a.mask[p.t0 + tok];
         if (p.n < 64) seen.mask &= (1ull << p.n) - 1;
       }
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, mc = 0.f, l = 0.f;  // mc = m c, or 0 while the row has seen nothing
+      const int lo = p.lo;
+      const uint64_t c2 = pair64(c, c);
 
-      for (int t = 0; t < n; t++, nt++) {
-        const int k0 = (p.lo + t) * AT_KEYS;
-        const bool masked = k0 + AT_KEYS > open;
-        const uint32_t buf = nt & 1;
-        wait(b_s + 8 * buf, (nt >> 1) & 1);
-        tmem_fence_after();
-        uint32_t s[64];
-        if (active) {
-          tmem_ld32(s, t_s + buf * 64);
-          tmem_ld32(s + 32, t_s + buf * 64 + 32);
-          tmem_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-              const uint32_t w = seen.bits(k0 + 32 * i);
-#pragma unroll
-              for (int e = 0; e < 32; e++)
-                if (!((w >> e) & 1)) s[32 * i + e] = 0xff800000u;
-            }
-          }
-          float top[4];
-#pragma unroll
-          for (int i = 0; i < 4; i++) top[i] = fmaxf(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-#pragma unroll
-          for (int i = 8; i < 64; i += 2)
-            top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-          const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-          const bool grow = live && mx > m && !((mx - m) * c <= 8.f);
-          if (t > 0 && __any_sync(0xffffffffu, grow)) {
-            // the products of the tile before may still run
-            wait(b_v, (nt + 1) & 1);
-            tmem_fence_after();
-            const float f = grow ? exp2_fast((m - mx) * c) : 1.f;
-#pragma unroll 1
-            for (int i = 0; i < D / 32; i++) {
-              uint32_t o[32];
-              tmem_ld32(o, t_o + 32 * i);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(t_o + 32 * i, o);
-            }
-            l *= f;
-          }
-          if (t == 0 || grow) m = mx;
-        }
-        if (masked) {
+      // One tile.  Nearly all are seen by every row: those have a body of their own, short
+      // enough for the instruction cache (the loop with both took 1,500 cycles a tile instead of 1,200).
+      auto tile = [&](int t, auto some_hidden) {
+        constexpr bool MASKED = decltype(some_hidden)::value;
+        const int k0 = (lo + t) * KEYS;
+        if (MASKED) {
           // Values of keys past the request's end become 0; so do infinities and NaN of
           // keys that only some rows see: 0 * inf in a product would reach the others.
           // (Rows that do see them get them back below.)  Streams that share a tile leave it to the first.
           if (MODE != 2 || stream == 0) {
-            const uint32_t at = ring0 + (n == 1 ? 1 : t == n - 1 ? 2 * n - 1 : 2 * t + 2);
+            const uint32_t at = ring0 + (BUFS == 1 ? 2 * t + 1 : n == 1 ? 1 : t == n - 1 ? 2 * n - 1 : 2 * t + 2);
             wait(b_full + 8 * (at % NST), (at / NST) & 1);
-            const int kr = row & 63, half = row >> 6, key = k0 + kr;  // a thread has half a row
+            constexpr int PARTS = 128 / KEYS;  // threads of a row
+            const int kr = row % KEYS, part = row / KEYS, key = k0 + kr;
             if (key >= open) {
               uint8_t* v = smem + (s_ring - base) + (at % NST) * L::STAGE + kr * 128;
               bool bad = false;
 #pragma unroll 4
-              for (int i = half * (D / 16); i < (half + 1) * (D / 16); i++) {
-                uint4* x = reinterpret_cast<uint4*>(v + (i >> 3) * (AT_KEYS * 128) + (((i & 7) ^ (kr & 7)) << 4));
+              for (int i = part * (D / 8 / PARTS); i < (part + 1) * (D / 8 / PARTS); i++) {
+                uint4* x = reinterpret_cast<uint4*>(v + (i >> 3) * (KEYS * 128) + (((i & 7) ^ (kr & 7)) << 4));
                 if (key >= p.len) {
                   *x = make_uint4(0, 0, 0, 0);
                 } else {
@@ -745,19 +720,67 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           }
           if (MODE == 2 && p.rows > 128) asm volatile("bar.sync 3, 256;" ::: "memory");
         }
+        const uint32_t buf = nt % BUFS;
+        wait(b_s + 8 * buf, (nt / BUFS) & 1);
+        tmem_fence_after();
+        uint32_t s[KEYS];
         if (active) {
-          const float mc = m == -INFINITY ? 0.f : m * c;
-          const uint64_t c2 = pair64(c, c), mc2 = pair64(-mc, -mc);
-          uint64_t sum[2] = {0, 0};
-          uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 32; e++) {
-            const float2 x = unpair64(fma2(pair64(s[2 * e], s[2 * e + 1]), c2, mc2));
-            const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
-            sum[e & 1] = add2(sum[e & 1], pair64(p0, p1));
-            w[e] = pack2<T>(p0, p1);
+          for (int i = 0; i < KEYS; i += 32) tmem_ld32(s + i, t_s + buf * KEYS + i);
+          tmem_wait_ld();
+          if (MASKED) {
+#pragma unroll
+            for (int i = 0; i < KEYS / 32; i++) {
+              const uint32_t w = seen.bits(k0 + 32 * i);
+#pragma unroll
+              for (int e = 0; e < 32; e++)
+                if (!((w >> e) & 1)) s[32 * i + e] = 0xff800000u;
+            }
           }
-          tmem_st32(t_s + buf * 64, w);
+          float top[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) top[i] = fmaxf(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+#pragma unroll
+          for (int i = 8; i < KEYS; i += 2)
+            top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+          const bool grow = t == 0 || (live && mx > m && !(fmaf(mx, c, -mc) <= 8.f));
+          if (__any_sync(0xffffffffu, grow)) {
+            if (t > 0) {
+              // the products of the tile before may still run
+              wait(b_v, (nt + 1) & 1);
+              tmem_fence_after();
+              const float f = grow ? exp2_fast((m - mx) * c) : 1.f;
+#pragma unroll 1
+              for (int i = 0; i < D / 32; i++) {
+                uint32_t o[32];
+                tmem_ld32(o, t_o + 32 * i);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(t_o + 32 * i, o);
+              }
+              l *= f;
+            }
+            if (grow) {
+              m = mx;
+              mc = m == -INFINITY ? 0.f : m * c;
+            }
+          }
+          const uint64_t mc2 = pair64(-mc, -mc);
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < KEYS / 64; i++) {
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; e++) {
+              const float2 x = unpair64(fma2(pair64(s[64 * i + 2 * e], s[64 * i + 2 * e + 1]), c2, mc2));
+              const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
+              sum[e & 1] = add2(sum[e & 1], pair64(p0, p1));
+              w[e] = pack2<T>(p0, p1);
+            }
+            tmem_st32(t_s + buf * KEYS + 32 * i, w);
+          }
           const float2 l2 = unpair64(add2(sum[0], sum[1]));
           l += l2.x + l2.y;
           tmem_wait_st();
@@ -765,13 +788,18 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(b_p + 8 * buf);
-        if (t == n - 1) {  // the queries have been read for the last time
-          more = coming(taken + 1);
-          if (more && has_rows(taken + 1)) {
-            fetch(taken + 1);
-            fetched();
-          }
-        }
+        nt++;
+      };
+      const int clear = max(0, min(n, open / KEYS - lo));
+#pragma unroll 1
+      for (int t = 0; t < clear; t++) tile(t, std::false_type());
+#pragma unroll 1
+      for (int t = clear; t < n; t++) tile(t, std::true_type());
+      // the queries have been read for the last time: the next ones come in under the last products
+      more = coming(taken + 1);
+      if (more && has_rows(taken + 1)) {
+        fetch(taken + 1);
+        fetched();
       }
       wait(b_o, units & 1);
       tmem_fence_after();
@@ -819,8 +847,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       if (row == 0 && (MODE != 2 || stream == 0)) s_bad[(taken + 2) & 7] = 0;
       if (bad && live) {
         // the values taken out above, for the rows that see them: any weight makes them infinite or NaN
-        const int to = min(p.len, p.hi * AT_KEYS);
-        for (int j = max(open, p.lo * AT_KEYS); j < to; j++) {
+        const int to = min(p.len, p.hi * KEYS);
+        for (int j = max(open, p.lo * KEYS); j < to; j++) {
           const int64_t id = a.table[(int64_t)p.r * a.table_stride + (j >> a.log2_bs)];
           if (!seen.has(j) || id < 0 || id >= a.n_blocks) continue;
           const T* v = static_cast<const T*>(a.v) + id * a.s_block + p.h * a.s_head + (j & ((1 << a.log2_bs) - 1)) * a.s_token;
@@ -1068,7 +1096,7 @@ extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const
                   cache->stride[2], cache->log2_block, ws->part, ws->counters};
   cudaStream_t st = (cudaStream_t)cuda_stream;
   // an upper bound of the line that the kernel divides
-  const double tiles = ((double)(table_width << cache->log2_block) / AT_KEYS + 1 + AT_UNIT_COST + AT_MIN_SHARE) * cache->n_heads;
+  const double tiles = ((double)(table_width << cache->log2_block) / 64 + 1 + AT_UNIT_COST + AT_MIN_SHARE) * cache->n_heads;
   if (tiles * ((double)T * group / 32 + (double)R) >= 2e9) {
     tk_set_error("%s: %lld tokens over tables of %lld blocks are too much work for one call", where, (long long)T,
                  (long long)table_width);
