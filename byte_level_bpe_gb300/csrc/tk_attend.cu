@@ -23,10 +23,9 @@
 namespace tk {
 
 constexpr int AT_THREADS = 384;  // loads and products of two streams (4 warps), their softmax (2 x 4 warps)
-constexpr int AT_UNIT_COST = 2;  // what starting a unit costs, in tiles
+constexpr int AT_UNIT_COST = 3;  // what starting a unit costs, in tiles
 constexpr int AT_MIN_SHARE = 8;  // least share of a worker, in tiles
 constexpr int AT_SNAP = 4;       // a unit is not cut nearer to its ends than this, in tiles
-constexpr int AT_PAD = 8;        // what a worker may do more, in tiles, if it has a single piece for that
 
 struct AttendArgs {
   const void* q;
@@ -398,7 +397,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     if (units > 0 && units < workers) {
       // shares that give the units no more workers than there are
       const int share = max(AT_MIN_SHARE, min(over(longest, workers / units), over(total, workers - units)));
-      if (share <= plan.share + AT_PAD) {
+      // What a worker may do more if it has a single piece for that.  Up to 128 rows memory is the
+      // bound, which fewer workers reach too: 32 requests of 8k tokens, 256 units for 304
+      // workers, take 183 us padded (128 tiles each) and 206 us divided evenly (108).
+      if (share <= plan.share + 8 + (MODE == 2 ? 0 : plan.share / 4)) {
         plan.share = share;
         plan.padded = true;
         mine = 0;
@@ -438,9 +440,9 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     taken++;
   };
 
-  // registers: 384 x 168 at launch = 128 x 104 + 256 x 200
+  // registers: 384 x 168 at launch = 128 x 104 + 256 x 200, where a softmax thread holds 128 scores
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (MODE == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 0 || (warp == 3 && MODE != 2)) {
       // ---- loads, in the order of their use: K0 K1 V0 K2 V1 K3 ... with two tiles' scores, K0 V0 K1 V1 ... with one
       Walk<ROWS> walk;
@@ -608,7 +610,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if (MODE == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax
     const int wq = warp & 3, row = wq * 32 + lane;  // row = also its lane of tensor memory
     const uint32_t t_s = ((uint32_t)(wq * 32) << 16) + stream * 256, t_o = t_s + 128;
@@ -677,12 +679,12 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       const int lo = p.lo;
       const uint64_t c2 = pair64(c, c);
 
-      // One tile.  Nearly all are seen by every row: those have a body of their own, short
-      // enough for the instruction cache (the loop with both took 1,500 cycles a tile instead of 1,200).
+      // One tile.  Nearly all are seen by every row; where the softmax is the bound (MODE 2) those have a
+      // body of their own.
       auto tile = [&](int t, auto some_hidden) {
-        constexpr bool MASKED = decltype(some_hidden)::value;
         const int k0 = (lo + t) * KEYS;
-        if (MASKED) {
+        const bool hidden = decltype(some_hidden)::value && (MODE == 2 || k0 + KEYS > open);
+        if (hidden) {
           // Values of keys past the request's end become 0; so do infinities and NaN of
           // keys that only some rows see: 0 * inf in a product would reach the others.
           // (Rows that do see them get them back below.)  Streams that share a tile leave it to the first.
@@ -728,7 +730,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
 #pragma unroll
           for (int i = 0; i < KEYS; i += 32) tmem_ld32(s + i, t_s + buf * KEYS + i);
           tmem_wait_ld();
-          if (MASKED) {
+          if (hidden) {
 #pragma unroll
             for (int i = 0; i < KEYS / 32; i++) {
               const uint32_t w = seen.bits(k0 + 32 * i);
@@ -790,9 +792,12 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         if (lane == 0) bar_arrive(b_p + 8 * buf);
         nt++;
       };
-      const int clear = max(0, min(n, open / KEYS - lo));
+      int clear = 0;
+      if constexpr (MODE == 2) {
+        clear = max(0, min(n, open / KEYS - lo));
 #pragma unroll 1
-      for (int t = 0; t < clear; t++) tile(t, std::false_type());
+        for (int t = 0; t < clear; t++) tile(t, std::false_type());
+      }
 #pragma unroll 1
       for (int t = clear; t < n; t++) tile(t, std::true_type());
       // the queries have been read for the last time: the next ones come in under the last products
