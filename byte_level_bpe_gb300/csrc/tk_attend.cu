@@ -266,7 +266,7 @@ struct AttendShape {
   static constexpr int PIECES = BARS + 8 * N_BARS;
   static constexpr int SMALL = PIECES + RINGS * AT_PIECES * (int)sizeof(Piece);
   // start of the walk (2 x 2), sums, units and longest of the warps, tensor memory, abort, non-finite values (2 x 8)
-  static constexpr int TOTAL = SMALL + 16 + 12 * (AT_THREADS / 32) + 72;
+  static constexpr int TOTAL = SMALL + 16 + 16 * (AT_THREADS / 32) + 72;
   static_assert(SMALL % 8 == 0 && TOTAL <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -306,7 +306,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
   int* s_sum = s_walk + 4;
   int* s_units = s_sum + AT_THREADS / 32;
   int* s_longest = s_units + AT_THREADS / 32;
-  volatile int* s_int = reinterpret_cast<volatile int*>(s_longest + AT_THREADS / 32);
+  int* s_coarse = s_longest + AT_THREADS / 32;
+  volatile int* s_int = reinterpret_cast<volatile int*>(s_coarse + AT_THREADS / 32);
   volatile int* abort = s_int + 1;
   volatile int* s_bad = s_int + 2 + 8 * ring;  // by piece
 
@@ -349,7 +350,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
   {
     const int R = (int)a.R, per = (R + AT_THREADS - 1) / AT_THREADS;
     const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
-    int mine = 0, units = 0, longest = 0, before;
+    int mine = 0, units = 0, longest = 0, before, coarse = 0;
     for (int r = r0; r < r1; r++) {
       const Request q = load_request(a, r);
       if (!q.good && blockIdx.x == 0 && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = r;
@@ -357,6 +358,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       mine += w.length;
       units += w.units;
       longest = max(longest, w.longest);
+      coarse = min(coarse + (w.length >> 10) + 1, 1 << 21);
     }
     // the sum over the threads before this one, and over all
     auto scan = [&](int x, int& all) {
@@ -380,16 +382,25 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     };
     units = __reduce_add_sync(0xffffffffu, units);
     longest = __reduce_max_sync(0xffffffffu, longest);
+    coarse = __reduce_add_sync(0xffffffffu, coarse);
     if (lane == 0) {
       s_units[warp] = units;
       s_longest[warp] = longest;
+      s_coarse[warp] = coarse;
     }
     before = scan(mine, total);
-    units = 0;
+    units = coarse = 0;
 #pragma unroll
     for (int w = 0; w < AT_THREADS / 32; w++) {
       units += s_units[w];
       longest = max(longest, s_longest[w]);
+      coarse += s_coarse[w];
+    }
+    // offsets that run over each other may ask for any amount: nothing is done then
+    const bool much = coarse >= 1 << 21;
+    if (much) {
+      if (blockIdx.x == 0 && tid == 0 && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = -1;
+      total = mine = units = 0;
     }
     const int workers = gridDim.x * WORKERS;
     auto over = [](int x, int y) { return (int)((unsigned)(x + y - 1) / (unsigned)y); };
@@ -746,7 +757,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           for (int i = 8; i < KEYS; i += 2)
             top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
           const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-          const bool grow = t == 0 || (live && mx > m && !(fmaf(mx, c, -mc) <= 8.f));
+          const bool grow = t == 0 || (live && mx > m && !((mx - m) * c <= 8.f));
           if (__any_sync(0xffffffffu, grow)) {
             if (t > 0) {
               // the products of the tile before may still run
@@ -1069,6 +1080,7 @@ extern "C" int tk_kv_status(tk_kv_workspace* ws, int64_t* h_request, void* cuda_
   if (s.code) {
     if (h_request) *h_request = s.request;
     if (s.code == TK_E_TIMEOUT) tk_set_error("tk_kv_attend: a wait on the device gave up");
+    else if (s.request < 0) tk_set_error("tk_kv_attend: offsets that contradict each other");
     else tk_set_error("tk_kv_attend: request %lld: lengths outside the call's limits", (long long)s.request);
   }
   return s.code;
@@ -1085,12 +1097,14 @@ extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const
   if (cache->head_dim != 64 && cache->head_dim != 128) return attend_arg(where, "head_dim is neither 64 nor 128");
   if (n_q_heads < 1 || n_q_heads > 1024 || n_q_heads % cache->n_heads)
     return attend_arg(where, "n_q_heads is no multiple of the cache's heads up to 1,024");
-  if (R < 0 || T < 0 || R > INT32_MAX || T > 1 << 26 || max_new < 0 || table_width < 0 || table_stride < table_width)
+  if (R < 0 || T < 0 || R > 1 << 20 || T > 1 << 26 || max_new < 0 || table_width < 0 || table_stride < table_width)
     return attend_arg(where, "bad size");
   if (q_stride < (int64_t)n_q_heads * cache->head_dim || q_stride % 8)
     return attend_arg(where, "q_stride is below a token's elements or no multiple of 8");
   if (!(scale > 0.f) || scale > 3e38f) return attend_arg(where, "scale is not a positive number");
   if (T * n_q_heads > INT32_MAX) return attend_arg(where, "T times n_q_heads is above 2^31");
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != cache->device) return attend_arg(where, "the current device is not the cache's");
   if (T == 0 || R == 0) return TK_OK;
   if (!d_q || !d_off || !d_len || !d_out || (table_width > 0 && !d_table)) return attend_arg(where, "null pointer");
   if ((((uintptr_t)d_q | (uintptr_t)d_out) & 15) != 0) return attend_arg(where, "a buffer is not 16-byte aligned");
@@ -1100,14 +1114,15 @@ extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const
                   cache->v, cache->n_blocks, cache->stride[0], cache->stride[1],
                   cache->stride[2], cache->log2_block, ws->part, ws->counters};
   cudaStream_t st = (cudaStream_t)cuda_stream;
+  const int64_t rows = std::min(max_new, T) * group;  // of a request and key head
   // an upper bound of the line that the kernel divides
-  const double tiles = ((double)(table_width << cache->log2_block) / 64 + 1 + AT_UNIT_COST + AT_MIN_SHARE) * cache->n_heads;
-  if (tiles * ((double)T * group / 32 + (double)R) >= 2e9) {
+  const int unit_rows = rows <= 32 ? 32 : rows <= 128 ? 128 : 256, keys = rows <= 128 ? 64 : 128;
+  const double tiles = (double)(table_width << cache->log2_block) / keys + 1 + AT_UNIT_COST + AT_MIN_SHARE;
+  if (tiles * cache->n_heads * ((double)T * group / unit_rows + (double)R) >= 1e9) {
     tk_set_error("%s: %lld tokens over tables of %lld blocks are too much work for one call", where, (long long)T,
                  (long long)table_width);
     return TK_E_LIMIT;
   }
-  const int64_t rows = std::min(max_new, T) * group;  // of a request and key head
   cudaError_t e;
   if (cache->type == TK_BF16)
     e = cache->head_dim == 64 ? attend_pick<__nv_bfloat16, 64>(a, cache, rows, ws->sms, st)

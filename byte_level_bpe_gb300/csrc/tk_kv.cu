@@ -585,6 +585,8 @@ extern "C" int tk_kv_append(const tk_kv_cache* cache, const void* d_qkv, int64_t
   if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16 || (rot_dim > 0 && !d_rope))
     return kv_arg(where, "rot_dim is not a multiple of 16 up to head_dim, or has no table");
   if (!(eps >= 0.f)) return kv_arg(where, "eps is negative");
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != cache->device) return kv_arg(where, "the current device is not the cache's");
   if (T == 0) return TK_OK;
   if (!d_qkv || !d_slot || !d_q || (rot_dim > 0 && !d_pos)) return kv_arg(where, "null pointer");
   if (!aligned16(d_qkv) || !aligned16(d_q) || !aligned16(d_rope) || !aligned16(d_q_gain) || !aligned16(d_k_gain))

@@ -602,6 +602,67 @@ def test_attend_many_requests(tk):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("new,ctx,hq,hk,d,bs,tree", [
+    ([64], [9000], 16, 2, 128, 128, True),          # 512 rows a head, many pieces each
+    ([64, 3], [3001, 70], 40, 8, 64, 32, True),     # 320 rows: a second stream with part of them
+    ([16, 5, 16], [20000, 300, 0], 8, 1, 128, 16, True),  # one full row tile
+    ([1], [33333], 6, 1, 64, 64, False), ([1] * 3, [9000, 8000, 40], 4, 4, 128, 16, False),
+    ([500, 0, 37], [2000, 50, 0], 8, 2, 64, 64, False), ([1000], [0], 3, 1, 128, 16, False)])
+def test_attend_divided(tk, dtype, new, ctx, hq, hk, d, bs, tree):
+    """Caches long enough to be divided over the GPU, and units joined again; oracle in 64 bits on the GPU."""
+    gen = torch.Generator().manual_seed(sum(ctx) + d)
+    q, k, v, off, lens, table = _attend_case(gen, new, ctx, hq, hk, d, bs, dtype)
+    masks = _tree_masks(gen, new) if tree else None
+    c = lambda x: None if x is None else x.cuda()  # noqa: E731
+    cache, ws = tk.KVCache(c(k), c(v)), tk.KVWorkspace()
+    got, lse = cache.attend(c(q), c(off), c(lens), c(table), ws, masks=c(masks), max_new=max(new), lse=True)
+    ws.status()
+    again = cache.attend(c(q), c(off), c(lens), c(table), ws, masks=c(masks), max_new=max(new))
+    assert torch.equal(got, again)  # the order of the CTAs changes nothing
+    for r, (n, x) in enumerate(zip(new, ctx)):
+        if not n:
+            continue
+        place = torch.arange(x + n)
+        rows = table[r].long()[place // bs]
+        kk, vv = (c(y[rows, :, place % bs]).double() for y in (k, v))
+        i, j = torch.arange(n)[:, None], place[None] - x
+        seen = j <= i if masks is None else (j < 0) | ((masks[int(off[r]):int(off[r]) + n, None] >> j.clamp(min=0)) & 1 != 0)
+        for h in range(hq):
+            qq = c(q[int(off[r]):int(off[r]) + n, h]).double()
+            s = (qq @ kk[:, h * hk // hq].T * d ** -0.5).masked_fill(~c(seen), -np.inf)
+            w = torch.softmax(s, 1)
+            o, a = w @ vv[:, h * hk // hq], w @ vv[:, h * hk // hq].abs()
+            big = ((qq.abs() @ kk[:, h * hk // hq].abs().T).max(1).values * d ** -0.5)[:, None]
+            tol = 1.02 * U[dtype] * (o.abs() + a) + 2.0 ** -15 * (1 + big) * a + 2.0 ** -24
+            if dtype == torch.float16:
+                tol = tol + (x + n) * 2.0 ** -24 * vv.abs().max()
+            at = slice(int(off[r]), int(off[r]) + n)
+            _close(got[at, h], o.cpu(), tol.cpu(), (r, h))
+            err = (lse[at, h].double() - torch.logsumexp(s, 1)).abs()
+            assert bool((err <= 2.0 ** -16 * (1 + big[:, 0])).all())
+
+
+@pytest.mark.gpu
+def test_attend_offsets_that_contradict_each_other(tk):
+    """Nothing outside the buffers is touched, and the status tells."""
+    gen = torch.Generator().manual_seed(12)
+    q, k, v, off, lens, table = _attend_case(gen, [3, 2, 4], [20, 30, 10], 4, 2, 64, 16, torch.bfloat16)
+    cache, ws = tk.KVCache(k.cuda(), v.cuda()), tk.KVWorkspace()
+    for bad in ([0, 3, 1, 9], [-5, 3, 5, 9], [0, 3, 1 << 40, 9], [9, 6, 3, 0]):
+        guard = torch.full((9 + 64, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        cache.attend(q.cuda(), torch.tensor(bad, device="cuda"), lens.cuda(), table.cuda(), ws, out=guard[32:41])
+        with pytest.raises(tk.TkError):
+            ws.status()
+        assert bool((guard[:32] == 7).all()) and bool((guard[41:] == 7).all())
+    many = torch.tensor([0, 9] * 9000 + [0], device="cuda")  # requests over each other
+    ln = torch.full((18000,), 9, dtype=torch.int32, device="cuda")
+    cache.attend(q.cuda(), many, ln, torch.zeros(18000, 3, dtype=torch.int32, device="cuda"), ws)
+    with pytest.raises(tk.TkError):
+        ws.status()
+
+
+@pytest.mark.gpu
 def test_attend_long_cache_past_32_bits(tk):
     """Blocks more than 2^31 elements into the pool, and a request of 70,001 tokens."""
     bs, hk, d, n = 128, 2, 128, 3
