@@ -71,7 +71,7 @@ __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t* s_warp, int64_t
 // launch does it all.  A new block's table entry is written by the token at its
 // first place.  The last CTA writes the lengths and the totals.  A thread has four
 // tokens and looks a block up where it begins: 5.3 M tokens of 4,096 prompts, bound by
-// instructions at first (37 us), take 20 us, the outputs' 85 MB 13 us.
+// instructions at first (37 us), take 26 us; the 85 MB of outputs alone take 13 us.
 __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs a) {
   __shared__ int64_t s_warp[PLAN_THREADS / 32];
   __shared__ int s_off[PLAN_THREADS + 1];  // from t0 on
@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs a) {
       s_placed[tid] = need == 0 || (need > 0 && base + need <= a.n_free);
       s_base[tid] = (int)base - ((s_ctx[tid] + up) >> a.log2_bs);  // in range where it is used
     }
-    __syncthreads();
+    // the requests that begin in this CTA's tokens: the search below is among them
+    const int in = max(1, __syncthreads_count(tid < nr && s_off[tid] < count));
     const int hi = min(count, s_off[nr]);
     for (int g = (lo & ~(PLAN_ITEMS - 1)) + tid * PLAN_ITEMS; g < hi; g += PLAN_THREADS * PLAN_ITEMS) {
       int pos[PLAN_ITEMS], req[PLAN_ITEMS];
@@ -159,44 +160,53 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs a) {
       // the request of the first token: the last that starts at or before it
       const int from = max(g, lo);
       int k = 0;
-      for (int b = nr; b > 1;) {
+      for (int b = in; b > 1;) {
         const int h = b >> 1;
         if (s_off[k + h] <= from) k += h;
         b -= h;
       }
-      int start = s_off[k], next = s_off[k + 1], c = s_ctx[k], blk = -1, id = -1;
+      const bool whole = g >= lo && g + PLAN_ITEMS <= hi;
+      // of request k: spot = t + shift; its slots are first + (spot & within), first changes with the block
+      int start, next, shift, within, blk;
+      int64_t first;
+      auto enter = [&]() {
+        start = s_off[k];
+        next = k + 1 < nr ? s_off[k + 1] : INT32_MAX;
+        shift = (int)((unsigned)s_ctx[k] - (unsigned)start);
+        within = s_placed[k] ? up : 0;
+        blk = s_placed[k] ? -1 : INT32_MAX;  // not placed: no block is looked up
+        first = -1;
+      };
+      enter();
 #pragma unroll
       for (int j = 0; j < PLAN_ITEMS; j++) {
         const int t = g + j;
-        if (t < lo || t >= hi) continue;
-        while (t >= next && k + 1 < nr) {
+        if (!whole && (t < lo || t >= hi)) continue;
+        while (t >= next) {
           k++;
-          start = next;
-          next = s_off[k + 1];
-          c = s_ctx[k];
-          blk = -1;
+          enter();
         }
-        const int i = t - start, spot = (int)((unsigned)c + (unsigned)i);
+        const int spot = (int)((unsigned)t + (unsigned)shift);
+        if (blk != INT32_MAX && blk != spot >> a.log2_bs) {
+          blk = spot >> a.log2_bs;
+          const int c = s_ctx[k];
+          int32_t* entry = a.table + (r0 + k) * a.table_stride + blk;
+          int id = -1;
+          if (t < start || blk >= a.table_width) {
+            id = -1;  // offsets or lengths that contradict each other
+          } else if (blk < (c + up) >> a.log2_bs) {
+            id = *entry;
+          } else if ((unsigned)(s_base[k] + blk) < (uint64_t)a.n_free) {
+            id = a.free_ids[s_base[k] + blk];
+            if ((spot & up) == 0) *entry = id;
+          }
+          first = (int64_t)id * (up + 1);
+        }
         req[j] = (int)r0 + k;
         pos[j] = spot;
-        slot[j] = -1;
-        if (s_placed[k] && i >= 0) {
-          if (blk != spot >> a.log2_bs) {
-            blk = spot >> a.log2_bs;
-            int32_t* entry = a.table + (r0 + k) * a.table_stride + blk;
-            id = -1;
-            if (blk >= a.table_width) {
-              id = -1;  // lengths that contradict each other
-            } else if (blk < (c + up) >> a.log2_bs) {
-              id = *entry;
-            } else if ((unsigned)(s_base[k] + blk) < (uint64_t)a.n_free) {
-              id = a.free_ids[s_base[k] + blk];
-              if ((spot & up) == 0) *entry = id;
-            }
-          }
-          slot[j] = (int64_t)id * (up + 1) + (spot & up);
-        }
+        slot[j] = first + (spot & within);
         if (a.parent) {
+          const int i = t - start;
           uint64_t m = 0;
           int depth = 0;
           if (i >= 0 && i < KV_TREE_MAX) {
@@ -210,11 +220,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs a) {
             }
           }
           mask[j] = (int64_t)m;
-          pos[j] = c + depth;
+          pos[j] = s_ctx[k] + depth;
         }
       }
       const int64_t at = t0 + g;
-      if (g >= lo && g + PLAN_ITEMS <= hi) {
+      if (whole) {
         *reinterpret_cast<int4*>(a.pos + at) = make_int4(pos[0], pos[1], pos[2], pos[3]);
         *reinterpret_cast<int4*>(a.req + at) = make_int4(req[0], req[1], req[2], req[3]);
         *reinterpret_cast<longlong2*>(a.slot + at) = make_longlong2(slot[0], slot[1]);
