@@ -7,12 +7,17 @@
 // tensor cores; 128 rows are one tile whether they are all in use or not: for 128
 // keys the two products take about 1,300 cycles against the 2,850 that their
 // 64 KB of keys and values take from HBM (head_dim 128), so padding costs nothing while
-// memory is the bound.  Keys come in tiles of 64.  With a running maximum m and sum l,
+// memory is the bound.  With a running maximum m and sum l,
 //   p_j = 2^(c (s_j - m)), c = scale log2(e),  l += sum p_j,  O += P V,
 // and O is rescaled in tensor memory only when m grows by more than 2^8 in p
 // (p and l are relative to the same m, so the quotient is exact either way).
 // S, m, l and O are fp32; P is rounded to the cache's type, which the tensor
 // cores ask for: an error of half an ulp in each weight.
+//
+// Bounds, on one GB300: HBM up to 128 rows (one token of 128 requests over 6k,
+// 3.25 GB: 480 us, 6.8 TB/s); above, the tensor cores and the latency of the chain from one
+// tile's scores to the next one's (64 drafted tokens over 131k, 512 rows a head: 204 us,
+// 1.35 PFLOP/s); a short call its chain of first accesses (200 keys: 9 us).
 #include <algorithm>
 #include <new>
 #include <type_traits>
@@ -248,9 +253,14 @@ __device__ __forceinline__ uint32_t nonfinite2<__half>(uint32_t w) {
 }
 
 // MODE 0 and 1: a CTA's two streams are workers of their own, with units of at
-// most 32 or 128 rows (0: less room for queries, more for tiles in flight).  MODE
-// 2: a CTA is one worker with units of 256 rows, each stream has 128 of them and both
-// read every tile.
+// most 32 or 128 rows (0: less room for queries, more for tiles in flight), so
+// that one's starts and ends run under the other's tiles.  MODE 2: a CTA is one worker with
+// units of 256 rows, each stream has 128 of them and both read every tile.  A stream
+// has 128 columns of tensor memory for scores.  64-key tiles leave room for the
+// scores of two, so that products run under the softmax of their own stream; with
+// 128-key tiles they run under the other stream's, and read the queries half as often
+// from shared memory (for 128 rows and 64 keys that is the products' bound: 48 cycles instead of 32 for
+// k = 16).  64 drafted tokens over 131k take 218 us with the former and 204 with the latter.
 template <int D, int MODE>
 struct AttendShape {
   static constexpr int RINGS = MODE == 2 ? 1 : 2, ROWS = MODE == 0 ? 32 : MODE == 1 ? 128 : 256;
@@ -279,12 +289,10 @@ __device__ __forceinline__ float* part_at(float* part, int stream, int slot) {
 }
 
 // Warps 0 and 3 load (one per ring), warps 1 and 2 issue the products of streams
-// 0 and 1, warps 4-7 and 8-11 are their softmax, a thread per row.  Tensor memory of a
-// stream: two tiles' scores (64 columns each, the weights over the first half of
-// them) and O (128), 256 columns from 256 * stream.  With two of them the products of
-// the next tile run under the softmax of this one: 128-key tiles, for which there is
-// only one, took 1.7 times as long.  (64-key scores read Q twice as often from
-// shared memory, 96 instead of 64 cycles for 128 keys and k = 16.)
+// 0 and 1, warps 4-7 and 8-11 are their softmax, a thread per row (two threads per row
+// were slower: 267 instead of 222 us for 64 drafted tokens over 131k).  Tensor memory of a
+// stream: scores (128 columns, the weights over the first half of a tile's) and O
+// (128), 256 columns from 256 * stream.
 template <class T, int D, int MODE>
 __global__ void __launch_bounds__(AT_THREADS, 1)
 k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
@@ -564,6 +572,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         const Piece& p = s_piece[taken % AT_PIECES];
         const int n = __shfl_sync(0xffffffffu, p.hi - p.lo, 0), rows = __shfl_sync(0xffffffffu, p.rows, 0);
         release();
+        // Streams that share tiles take turns: products that come in together also end together, and
+        // both streams then wait at once (2,048-token prompts: 211 us without, 200 with).
         const bool turn = MODE == 2 && rows > 128;
         if (MODE == 2 && stream * 128 >= rows) {  // no rows for this stream
           for (int i = 0; ok && i < 2 * n; i++, advance()) {
