@@ -12,7 +12,9 @@
 // and O is rescaled in tensor memory only when m grows by more than 2^8 in p
 // (p and l are relative to the same m, so the quotient is exact either way).
 // S, m, l and O are fp32; P is rounded to the cache's type, which the tensor
-// cores ask for: an error of half an ulp in each weight.
+// cores ask for, and l sums what was rounded: an error of half an ulp in each weight, but
+// none in a weight that is nearly alone (summed before the rounding, the result's error
+// against 64 bits came to 1.6 times that of rounding it alone; so it is 1.1 to 1.4 times).
 //
 // Bounds, on one GB300: HBM up to 128 rows (one token of 128 requests over 6k,
 // 3.25 GB: 480 us, 6.8 TB/s); above, the tensor cores and the latency of the chain from one
@@ -281,11 +283,12 @@ struct AttendShape {
 };
 
 // Partial output of a piece: [D / 4][128 rows][4] normalised, then [128] log2 of
-// the row's sum: lanes are rows, and neighbours in memory.  A stream has at most two: slot 1
+// the row's sum (of rounded weights) and [128] what the sum before rounding is of it: lanes
+// are rows, and neighbours in memory.  A stream has at most two: slot 1
 // if it holds the unit's first tile.
 template <int D>
 __device__ __forceinline__ float* part_at(float* part, int stream, int slot) {
-  return part + (int64_t)(stream * 2 + slot) * (128 * (D + 1));
+  return part + (int64_t)(stream * 2 + slot) * (128 * (D + 2));
 }
 
 // Warps 0 and 3 load (one per ring), warps 1 and 2 issue the products of streams
@@ -293,7 +296,9 @@ __device__ __forceinline__ float* part_at(float* part, int stream, int slot) {
 // were slower: 267 instead of 222 us for 64 drafted tokens over 131k).  Tensor memory of a
 // stream: scores (128 columns, the weights over the first half of a tile's) and O
 // (128), 256 columns from 256 * stream.
-template <class T, int D, int MODE>
+// LSE: the log of the sum is wanted too, and summed before the rounding (without it 64 drafted
+// tokens over 131k take 213 us, with it 224; up to 128 rows the softmax is not the bound, and it is always there).
+template <class T, int D, int MODE, bool LSE>
 __global__ void __launch_bounds__(AT_THREADS, 1)
 k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   using L = AttendShape<D, MODE>;
@@ -696,7 +701,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         seen.mask = (uint64_t)a.mask[p.t0 + tok];
         if (p.n < 64) seen.mask &= (1ull << p.n) - 1;
       }
-      float m = -INFINITY, mc = 0.f, l = 0.f;  // mc = m c, or 0 while the row has seen nothing
+      float m = -INFINITY, mc = 0.f, l = 0.f, l_full = 0.f;  // mc = m c, or 0 while the row has seen nothing
       const int lo = p.lo;
       const uint64_t c2 = pair64(c, c);
 
@@ -784,6 +789,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
                 tmem_st32(t_o + 32 * i, o);
               }
               l *= f;
+              l_full *= f;
             }
             if (grow) {
               m = mx;
@@ -791,7 +797,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
             }
           }
           const uint64_t mc2 = pair64(-mc, -mc);
-          uint64_t sum[2] = {0, 0};
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};  // of the rounded weights, which the product has
+          uint64_t full[2] = {0, 0};            // of the weights
 #pragma unroll
           for (int i = 0; i < KEYS / 64; i++) {
             uint32_t w[32];
@@ -799,13 +806,17 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
             for (int e = 0; e < 32; e++) {
               const float2 x = unpair64(fma2(pair64(s[64 * i + 2 * e], s[64 * i + 2 * e + 1]), c2, mc2));
               const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
-              sum[e & 1] = add2(sum[e & 1], pair64(p0, p1));
+              if (LSE) full[e & 1] = add2(full[e & 1], pair64(p0, p1));
               w[e] = pack2<T>(p0, p1);
+              add_halves(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], w[e], BF);
             }
             tmem_st32(t_s + buf * KEYS + 32 * i, w);
           }
-          const float2 l2 = unpair64(add2(sum[0], sum[1]));
-          l += l2.x + l2.y;
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          if (LSE) {
+            const float2 l2 = unpair64(add2(full[0], full[1]));
+            l_full += l2.x + l2.y;
+          }
           tmem_wait_st();
         }
         tmem_fence_before();
@@ -861,9 +872,12 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           __syncwarp();
         }
         if (live) {
-          const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * c) + log2f(l);
-          if (!whole) __stcg(part + 128 * D + row, lse2);
-          else if (a.lse) a.lse[o_at] = lse2 * 0.69314718055994531f;
+          if (!whole) {
+            __stcg(part + 128 * D + row, l == 0.f ? -INFINITY : mc + log2f(l));
+            if (LSE) __stcg(part + 128 * D + 128 + row, l == 0.f ? 1.f : l_full / l);
+          } else if (LSE && a.lse) {
+            a.lse[o_at] = l == 0.f ? -INFINITY : (mc + log2f(l_full)) * 0.69314718055994531f;
+          }
         }
       }
       tmem_fence_before();
@@ -979,7 +993,16 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           const int64_t at = (int64_t)join_out[k] + (int64_t)tk * a.hq + (gr - tk * a.group);
           *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * D + ch * 4) =
               make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
-          if (a.lse && ch == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+          if (LSE && a.lse && ch == 0) {
+            float full = 0.f;
+#pragma unroll 1
+            for (int pc = 0; pc < np; pc++) {
+              const float* src = part_at<D>(a.part, key + pc * STEP, pc == 0) + 128 * D + rr;
+              const float e = __ldcg(src);
+              if (e != -INFINITY) full = fmaf(exp2_fast(e - top), __ldcg(src + 128), full);
+            }
+            a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(full)) * 0.69314718055994531f;
+          }
         }
       }
       stream_sync();
@@ -998,12 +1021,12 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
   }
 }
 
-template <class T, int D, int MODE>
+template <class T, int D, int MODE, bool LSE>
 static cudaError_t attend_launch(const AttendArgs& a, const tk_kv_cache* cache, int grid, cudaStream_t st) {
   constexpr int bytes = AttendShape<D, MODE>::TOTAL;
   static bool set[64];  // by device
   if (cache->device >= 64 || !set[cache->device]) {
-    const cudaError_t e = cudaFuncSetAttribute(k_kv_attend<T, D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = cudaFuncSetAttribute(k_kv_attend<T, D, MODE, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     if (cache->device < 64) set[cache->device] = true;
   }
@@ -1017,14 +1040,14 @@ static cudaError_t attend_launch(const AttendArgs& a, const tk_kv_cache* cache, 
   cfg.stream = st;
   cfg.attrs = &coop;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_kv_attend<T, D, MODE>, a, cache->map_k, cache->map_v);
+  return cudaLaunchKernelEx(&cfg, k_kv_attend<T, D, MODE, LSE>, a, cache->map_k, cache->map_v);
 }
 
 template <class T, int D>
 static cudaError_t attend_pick(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, int grid, cudaStream_t st) {
-  if (rows <= 32) return attend_launch<T, D, 0>(a, cache, grid, st);
-  if (rows <= 128) return attend_launch<T, D, 1>(a, cache, grid, st);
-  return attend_launch<T, D, 2>(a, cache, grid, st);
+  if (rows <= 32) return attend_launch<T, D, 0, true>(a, cache, grid, st);
+  if (rows <= 128) return attend_launch<T, D, 1, true>(a, cache, grid, st);
+  return a.lse ? attend_launch<T, D, 2, true>(a, cache, grid, st) : attend_launch<T, D, 2, false>(a, cache, grid, st);
 }
 
 }  // namespace tk
@@ -1047,7 +1070,7 @@ extern "C" int tk_kv_workspace_create(tk_kv_workspace** out) {
   cudaError_t e = cudaGetDevice(&ws->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&ws->sms, cudaDevAttrMultiProcessorCount, ws->device);
   // one allocation: the partial outputs of two pieces of every stream, its counters, the status
-  const size_t part = sizeof(float) * 2 * 2 * 128 * (128 + 1) * (size_t)ws->sms,
+  const size_t part = sizeof(float) * 2 * 2 * 128 * (128 + 2) * (size_t)ws->sms,
                counters = sizeof(unsigned) * 2 * 2 * (size_t)ws->sms;
   uint8_t* mem = nullptr;
   if (e == cudaSuccess) e = cudaMalloc(&mem, part + counters + 64 + sizeof(KvStatus));

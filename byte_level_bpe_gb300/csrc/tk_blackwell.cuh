@@ -160,6 +160,17 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// fp32 sums of the two 16-bit halves of w
+__device__ __forceinline__ void add_halves(float& even, float& odd, uint32_t w, bool bf16) {
+  if (bf16)
+    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\nadd.rn.f32.bf16 %0, a, %0;\nadd.rn.f32.bf16 %1, b, %1;\n}"
+        : "+f"(even), "+f"(odd)
+        : "r"(w));
+  else
+    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\nadd.rn.f32.f16 %0, a, %0;\nadd.rn.f32.f16 %1, b, %1;\n}"
+        : "+f"(even), "+f"(odd)
+        : "r"(w));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
