@@ -71,7 +71,7 @@ __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t* s_warp, int64_t
 // launch does it all.  A new block's table entry is written by the token at its
 // first place.  The last CTA writes the lengths and the totals.  A thread has four
 // tokens and looks a block up where it begins: 5.3 M tokens of 4,096 prompts, bound by
-// instructions at first (37 us), take 26 us; the 85 MB of outputs alone take 13 us.
+// instructions at first (37 us), take 23 us; the 85 MB of outputs alone take 13 us.
 __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs a) {
   __shared__ int64_t s_warp[PLAN_THREADS / 32];
   __shared__ int s_off[PLAN_THREADS + 1];  // from t0 on
@@ -171,18 +171,39 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs a) {
       int64_t first;
       auto enter = [&]() {
         start = s_off[k];
-        next = k + 1 < nr ? s_off[k + 1] : INT32_MAX;
+        next = k + 1 < nr ? s_off[k + 1] : hi;  // the last one's tokens end the step
         shift = (int)((unsigned)s_ctx[k] - (unsigned)start);
         within = s_placed[k] ? up : 0;
         blk = s_placed[k] ? -1 : INT32_MAX;  // not placed: no block is looked up
         first = -1;
       };
       enter();
+      if (whole && g >= start && g + PLAN_ITEMS <= next && within && !a.parent) {
+        // nearly always: the four are one placed request's and lie in one block or two (looked up
+        // in turn they took 26 us instead of 23 for 5.3 M tokens)
+        const int c = s_ctx[k], have = (c + up) >> a.log2_bs, s0 = g + shift, b0 = s0 >> a.log2_bs,
+                  b1 = (s0 + PLAN_ITEMS - 1) >> a.log2_bs;
+        int32_t* row = a.table + (r0 + k) * a.table_stride;
+        const int32_t* fresh = a.free_ids + s_base[k];
+        const int id0 = b0 < have ? row[b0] : fresh[b0], id1 = b1 < have ? row[b1] : fresh[b1];
+        if ((s0 & up) == 0 && b0 >= have) row[b0] = id0;
+        if (b1 != b0 && b1 >= have) row[b1] = id1;
+#pragma unroll
+        for (int j = 0; j < PLAN_ITEMS; j++)
+          slot[j] = (int64_t)((s0 + j) >> a.log2_bs == b0 ? id0 : id1) * (up + 1) + ((s0 + j) & up);
+        const int64_t at = t0 + g;
+        const int q = (int)r0 + k;
+        *reinterpret_cast<int4*>(a.pos + at) = make_int4(s0, s0 + 1, s0 + 2, s0 + 3);
+        *reinterpret_cast<int4*>(a.req + at) = make_int4(q, q, q, q);
+        *reinterpret_cast<longlong2*>(a.slot + at) = make_longlong2(slot[0], slot[1]);
+        *reinterpret_cast<longlong2*>(a.slot + at + 2) = make_longlong2(slot[2], slot[3]);
+        continue;
+      }
 #pragma unroll
       for (int j = 0; j < PLAN_ITEMS; j++) {
         const int t = g + j;
         if (!whole && (t < lo || t >= hi)) continue;
-        while (t >= next) {
+        while (t >= next && k + 1 < nr) {
           k++;
           enter();
         }
