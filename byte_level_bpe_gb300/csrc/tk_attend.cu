@@ -17,9 +17,9 @@
 // against 64 bits came to 1.6 times that of rounding it alone; so it is 1.1 to 1.4 times).
 //
 // Bounds, on one GB300: HBM up to 128 rows (one token of 128 requests over 6k,
-// 3.25 GB: 480 us, 6.8 TB/s); above, the tensor cores and the latency of the chain from one
-// tile's scores to the next one's (64 drafted tokens over 131k, 512 rows a head: 204 us,
-// 1.35 PFLOP/s); a short call its chain of first accesses (200 keys: 9 us).
+// 3.25 GB: 485 us, 6.7 TB/s); above, the tensor cores and the latency of the chain from one
+// tile's scores to the next one's (64 drafted tokens over 131k, 512 rows a head: 213 us,
+// 1.29 PFLOP/s); a short call its chain of first accesses (200 keys: 9 us).
 #include <algorithm>
 #include <new>
 #include <type_traits>
@@ -97,7 +97,7 @@ __device__ __forceinline__ int key_tiles(int keys) {
 // gathered in one; a cut within AT_SNAP of a unit's start or end moves there.
 // Padded: there are fewer units than workers; a unit's length is rounded up to
 // whole shares and divided evenly over its workers, each of which has that one piece.
-// (The host keeps the line under 2^31.)
+// (A line of 2^31 and more is refused.)
 struct Plan {
   int share;
   bool padded;
@@ -109,17 +109,18 @@ struct UnitSum {
 template <int ROWS>
 __device__ __forceinline__ UnitSum request_work(const AttendArgs& a, const Request& q, const Plan& plan) {
   UnitSum w = {0, 0, 0};
+  int64_t length = 0;
   const int rows = q.n * a.group;
   const bool same = a.mask || !q.good || rows <= ROWS;  // every row tile has the request's keys
   for (int row0 = 0; row0 < rows; row0 += ROWS) {
     const int cost = key_tiles<ROWS>(unit_keys<ROWS>(a, q, row0)) + AT_UNIT_COST;
     const int tiles = same ? (rows + ROWS - 1) / ROWS : 1;
-    w.length += (plan.padded ? ((unsigned)(cost + plan.share - 1) / (unsigned)plan.share) * plan.share : cost) * tiles;
+    length += (int64_t)(plan.padded ? ((unsigned)(cost + plan.share - 1) / (unsigned)plan.share) * plan.share : cost) * tiles;
     w.units += tiles;
     w.longest = max(w.longest, cost);
     if (same) break;
   }
-  w.length *= a.hk;
+  w.length = (int)min(length * a.hk, (int64_t)INT32_MAX);
   w.units *= a.hk;
   return w;
 }
@@ -409,7 +410,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       longest = max(longest, s_longest[w]);
       coarse += s_coarse[w];
     }
-    // offsets that run over each other may ask for any amount: nothing is done then
+    // more than the line's 32 bits hold (offsets that run over each other may ask for any amount):
+    // nothing is done then
     const bool much = coarse >= 1 << 21;
     if (much) {
       if (blockIdx.x == 0 && tid == 0 && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = -1;
@@ -1113,7 +1115,7 @@ extern "C" int tk_kv_status(tk_kv_workspace* ws, int64_t* h_request, void* cuda_
   if (s.code) {
     if (h_request) *h_request = s.request;
     if (s.code == TK_E_TIMEOUT) tk_set_error("tk_kv_attend: a wait on the device gave up");
-    else if (s.request < 0) tk_set_error("tk_kv_attend: offsets that contradict each other");
+    else if (s.request < 0) tk_set_error("tk_kv_attend: more work than one call takes, or offsets that contradict each other");
     else tk_set_error("tk_kv_attend: request %lld: lengths outside the call's limits", (long long)s.request);
   }
   return s.code;
@@ -1148,14 +1150,6 @@ extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const
                   cache->stride[2], cache->log2_block, ws->part, ws->counters};
   cudaStream_t st = (cudaStream_t)cuda_stream;
   const int64_t rows = std::min(max_new, T) * group;  // of a request and key head
-  // an upper bound of the line that the kernel divides
-  const int unit_rows = rows <= 32 ? 32 : rows <= 128 ? 128 : 256, keys = rows <= 128 ? 64 : 128;
-  const double tiles = (double)(table_width << cache->log2_block) / keys + 1 + AT_UNIT_COST + AT_MIN_SHARE;
-  if (tiles * cache->n_heads * ((double)T * group / unit_rows + (double)R) >= 1e9) {
-    tk_set_error("%s: %lld tokens over tables of %lld blocks are too much work for one call", where, (long long)T,
-                 (long long)table_width);
-    return TK_E_LIMIT;
-  }
   cudaError_t e;
   if (cache->type == TK_BF16)
     e = cache->head_dim == 64 ? attend_pick<__nv_bfloat16, 64>(a, cache, rows, ws->sms, st)

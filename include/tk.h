@@ -391,18 +391,18 @@ void tk_kv_workspace_free(tk_kv_workspace* ws);
  *       cache's type for the product with the values.  Tokens that the mask
  *       hides, and cache places past d_len, have no influence, whatever they hold.
  *
- * R <= 2^20, T <= 2^26, T * n_q_heads < 2^31.  TK_E_LIMIT: tables so wide, for
- * so many tokens, that the call could come to 10^9 tiles of keys.  The launch
- * is cooperative (one CTA for each SM); a call uses the workspace until it ends, so
- * calls in flight at the same time need one each.
+ * R <= 2^20, T <= 2^26, T * n_q_heads < 2^31.  The launch is cooperative (one CTA
+ * for each SM); a call uses the workspace until it ends, so calls in flight at
+ * the same time need one each.
  *
  * Found on the device: a request with more than max_new new tokens, with more
  * than 64 under a mask, with d_len below its new tokens, or past table_width
  * blocks.  Its rows are 0 (lse -infinity), and tk_kv_status tells of it.  A
  * block id outside the cache reads as zeros.  Tokens of no request are not written.
+ * A call of 2^31 tiles of keys (of all row tiles and heads) or more does nothing.
  * tk_kv_status waits for cuda_stream and gives what the workspace's calls
  * since the last tk_kv_status met first: TK_OK, TK_E_LIMIT (h_request: the
- * request; -1 if the offsets contradict each other) or TK_E_TIMEOUT (a wait
+ * request; -1 if the call did nothing) or TK_E_TIMEOUT (a wait
  * on the device gave up, never expected; the outputs are unspecified).
  */
 int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const void* d_q, int64_t q_stride,
