@@ -8,9 +8,9 @@
 // keys the two products take about 1,300 cycles against the 2,850 that their
 // 64 KB of keys and values take from HBM (head_dim 128), so padding costs nothing while
 // memory is the bound.  With a running maximum m and sum l,
-//   p_j = 2^(c (s_j - m)), c = scale log2(e),  l += sum p_j,  O += P V,
+//   p_j = 2^(c (s_j - m) + UP), c = scale log2(e),  l += sum p_j,  O += P V,
 // and O is rescaled in tensor memory only when m grows by more than 2^8 in p
-// (p and l are relative to the same m, so the quotient is exact either way).
+// (p and l are relative to the same m and UP, so the quotient is exact either way).
 // S, m, l and O are fp32; P is rounded to the cache's type, which the tensor
 // cores ask for, and l sums what was rounded: an error of half an ulp in each weight, but
 // none in a weight that is nearly alone (summed before the rounding, the result's error
@@ -305,6 +305,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
   using L = AttendShape<D, MODE>;
   constexpr int ROWS = L::ROWS, KEYS = L::KEYS, BUFS = L::BUFS, HALVES = D / 64, NST = L::STAGES;
   constexpr bool BF = Pair<T>::BF;
+  // fp16 weights have their range below 2^15: with m's weight at 2^7 those 2^8 above it (before O is
+  // rescaled) still fit, and one is lost at 2^-32 of m's instead of 2^-25: a million keys that
+  // are each just below come to half an ulp of one of m's weight.
+  constexpr float UP = BF ? 0.f : 7.f;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle goes by address bits
   const uint32_t base = smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -703,7 +707,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         seen.mask = (uint64_t)a.mask[p.t0 + tok];
         if (p.n < 64) seen.mask &= (1ull << p.n) - 1;
       }
-      float m = -INFINITY, mc = 0.f, l = 0.f, l_full = 0.f;  // mc = m c, or 0 while the row has seen nothing
+      float m = -INFINITY, mc = 0.f, l = 0.f, l_full = 0.f;  // mc = m c - UP, or 0 while the row has seen nothing
       const int lo = p.lo;
       const uint64_t c2 = pair64(c, c);
 
@@ -795,7 +799,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
             }
             if (grow) {
               m = mx;
-              mc = m == -INFINITY ? 0.f : m * c;
+              mc = m == -INFINITY ? 0.f : fmaf(m, c, -UP);
             }
           }
           const uint64_t mc2 = pair64(-mc, -mc);

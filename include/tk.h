@@ -388,7 +388,8 @@ void tk_kv_workspace_free(tk_kv_workspace* ws);
  *       (fp32, NULL = not wanted): the natural log of the row's sum of
  *       exponentials.  A row that sees nothing gives 0 and -infinity.
  *       Scores, softmax and sums are fp32; the weights are rounded to the
- *       cache's type for the product with the values.  Tokens that the mask
+ *       cache's type for the product with the values (fp16: a weight below about 2^-32 of the
+ *       row's largest counts as 0).  Tokens that the mask
  *       hides, and cache places past d_len, have no influence, whatever they hold.
  *
  * R <= 2^20, T <= 2^26, T * n_q_heads < 2^31.  The launch is cooperative (one CTA

@@ -1,0 +1,58 @@
+"""Ranges and misuse of the paged cache calls (tk_kv_*): what must hold past the ordinary cases."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_kv import U, _close  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def tk():
+    import byte_level_bpe_gb300 as tk
+    return tk
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("hq,hk,n", [(2, 1, 1), (64, 1, 1), (16, 1, 20)])
+@pytest.mark.parametrize("below", [9.0, 15.0, 18.0])
+@pytest.mark.parametrize("at", [0, 17321])
+@pytest.mark.parametrize("R", [1, 320])
+def test_attend_one_strong_key(tk, dtype, hq, hk, n, below, at, R):
+    """One key of value 0 takes nearly all the weight; the others, e^-below each, carry the output. (Many requests, here
+    over one request's blocks, are not divided over the GPU: the key then stands against all others at once.)
+
+    As in test_kv, |err| <= 1.02 u (|o| + A) + 2^-15 (1 + S) A, and in fp16 each weight is off by at most half a
+    subnormal step, 2^-25, of a row whose largest weight is at least 2^7: n 2^-32 max|v| in all, and half a
+    step of the result, 2^-25.
+    """
+    L, bs, d = 40000, 64, 128
+    gen = torch.Generator(device="cuda").manual_seed(at + n)
+    k = torch.zeros(L // bs, hk, bs, d, device="cuda")
+    k[..., 1:] = 0.02 * torch.randn(L // bs, hk, bs, d - 1, generator=gen, device="cuda")
+    v = 1 + 0.5 * torch.rand(L // bs, hk, bs, d, generator=gen, device="cuda")
+    k[at // bs, :, at % bs] = 0
+    k[at // bs, :, at % bs, 0] = below
+    v[at // bs, :, at % bs] = 0
+    k, v = k.to(dtype), v.to(dtype)
+    q = torch.randn(R * n, hq, d, generator=gen, device="cuda")
+    q[..., 0] = 1
+    q = q.to(dtype)
+    table = torch.arange(L // bs, dtype=torch.int32, device="cuda").repeat(R, 1)
+    off, lens = torch.arange(R + 1, device="cuda") * n, torch.full((R,), L, dtype=torch.int32, device="cuda")
+    cache, ws = tk.KVCache(k, v), tk.KVWorkspace()
+    got, got_lse = cache.attend(q, off, lens, table, ws, scale=1.0, max_new=n, lse=True)
+    ws.status()
+    q, got, got_lse = q[-n:], got[-n:], got_lse[-n:]  # the last request's
+    kk, vv = (x.transpose(0, 1).reshape(hk, L, d).double()[0] for x in (k, v))
+    seen = torch.arange(L, device="cuda")[None] <= L - n + torch.arange(n, device="cuda")[:, None]
+    s = torch.einsum("nhd,ld->nhl", q.double(), kk).masked_fill(~seen[:, None], -np.inf)
+    w = torch.softmax(s, 2)
+    o, a = w @ vv, w @ vv.abs()
+    big = torch.einsum("nhd,ld->nhl", q.double().abs(), kk.abs()).amax(2)[..., None]
+    tol = 1.02 * U[dtype] * (o.abs() + a) + 2.0 ** -15 * (1 + big) * a
+    if dtype == torch.float16:
+        tol = tol + L * 2.0 ** -32 * vv.max() + 2.0 ** -25
+    _close(got, o.cpu(), tol.cpu())
+    assert bool(((got_lse.double() - torch.logsumexp(s, 2)).abs() <= 2.0 ** -16 * (1 + big[..., 0])).all())
