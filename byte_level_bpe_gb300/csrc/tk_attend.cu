@@ -1105,6 +1105,9 @@ extern "C" int tk_kv_status(tk_kv_workspace* ws, int64_t* h_request, void* cuda_
   using namespace tk;
   if (h_request) *h_request = -1;
   if (!ws) return attend_arg("tk_kv_status", "null workspace");
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != ws->device)
+    return attend_arg("tk_kv_status", "the current device is not the workspace's");
   KvStatus s = {};
   cudaStream_t st = (cudaStream_t)cuda_stream;
   cudaError_t e = cudaMemcpyAsync(&s, ws->status, sizeof(s), cudaMemcpyDeviceToHost, st);

@@ -16,15 +16,18 @@ from . import native
 
 _T = None  # torch, once a CUDA device has been seen
 _raw_stream = None
+_current_device = None
 
 
 def _torch():
-    global _T, _raw_stream
+    global _T, _raw_stream, _current_device
     if _T is None:
         import torch
         if not torch.cuda.is_available():
             raise RuntimeError("byte_level_bpe_gb300 needs a CUDA device (no CPU fallback)")
-        # the current stream's handle without the object around it, where torch has that
+        # the current device's index and its current stream's handle without the objects around them,
+        # where torch has that
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda index: torch.cuda.current_stream(index).cuda_stream)
         _T = torch
@@ -37,6 +40,12 @@ def _torch():
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
+
+
+def _need_current(index):
+    """Kernels and handles go to the current device, so it has to be the tensors'."""
+    if _current_device() != index:
+        raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
 
 
 def _stream(stream, index):
@@ -82,6 +91,7 @@ def kv_plan(offsets, context, table, free, block_size, n_tokens, parents=None, c
     i32, i64 = torch.int32, torch.int64
     R, T = context.numel(), n_tokens
     p_table, stride, W = _table(table, R, i32, index)
+    _need_current(index)
     p_off = _vector(offsets, "offsets", i64, R + 1, index)
     p_ctx = _vector(context, "context", i32, R, index)
     n_free = free.numel()
@@ -118,15 +128,15 @@ class KVWorkspace:
     """Scratch of one `attend` in flight (tk_kv_workspace): one per stream."""
 
     def __init__(self):
-        _torch()
         self._h = None
+        self._index = _torch().cuda.current_device()
         self._h = native.tk_kv_workspace_create()
 
     def status(self, stream=None):
         """Waits for the stream; raises TkError for the first request that an
         attend on this workspace could not take (tk_kv_status)."""
-        torch = _torch()
-        native.tk_kv_status(self._h, _stream(stream, torch.cuda.current_device()))
+        _need_current(self._index)
+        native.tk_kv_status(self._h, _stream(stream, self._index))
 
     def close(self):
         if self._h is not None:
@@ -155,6 +165,7 @@ class KVCache:
         self._h = None
         self.k, self.v, self.device, self.dtype = k, v, k.device, k.dtype
         self._index = k.get_device()
+        _need_current(self._index)
         self.n_blocks, self.kv_heads, self.block_size, self.head_dim = k.shape
         # the stride of a dimension of one element is arbitrary in torch
         d = self.head_dim

@@ -274,7 +274,9 @@ int tk_last_cache_stats(const tk_workspace* ws, int64_t* hits, int64_t* inserts)
  * them back for the new tokens, which may be drafted trees.  The pages have
  * no counterpart: these are engineering entry points of this library.
  *
- * They only queue work on cuda_stream: none waits for the device, allocates
+ * All buffers, handles and the stream belong to the current device (a handle is refused
+ * where another one is current; of plain pointers the caller has to see to it).
+ * The calls only queue work on cuda_stream: none waits for the device, allocates
  * or copies to the host, and all may be captured into a CUDA graph.  What is
  * wrong with the arguments comes back as TK_E_ARG / TK_E_LIMIT; what is wrong
  * with the data is found on the device, never reads or writes outside the

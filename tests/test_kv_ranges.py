@@ -13,6 +13,69 @@ def tk():
     return tk
 
 
+class OnCuda(torch.Tensor):
+    """A tensor of the host that says it is on cuda:0: for what the calls check before they reach the library."""
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return 0
+
+
+def on_cuda(x):
+    return x.as_subclass(OnCuda)
+
+
+class Library:
+    """In libtk's place: notes the calls and their arguments."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def host(monkeypatch):
+    """The calls without a GPU. host.device is the current one."""
+    from byte_level_bpe_gb300 import kv, native
+    lib = Library()
+    lib.device = 0
+    monkeypatch.setattr(kv, "_T", torch)
+    monkeypatch.setattr(kv, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(kv, "_current_device", lambda: lib.device, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: lib.device)
+    monkeypatch.setattr(native, "load", lambda: lib)
+    return lib
+
+
+def host_inputs(R=3, T=6, W=4, hq=4, hk=2, d=64, bs=16):
+    i32, i64 = torch.int32, torch.int64
+    z = lambda *s, t=torch.bfloat16: on_cuda(torch.zeros(*s, dtype=t))  # noqa: E731
+    return dict(off=z(R + 1, t=i64), ctx=z(R, t=i32), table=z(R, W, t=i32), free=z(8, t=i32), pos=z(T, t=i32),
+                slots=z(T, t=i64), qkv=z(T, (hq + 2 * hk) * d), q=z(T, hq, d), k=z(8, hk, bs, d), v=z(8, hk, bs, d), T=T, hq=hq)
+
+
+def test_tensors_of_another_device_are_refused(tk, host):
+    """A kernel would start on the current device, ordered after nothing on the tensors'."""
+    x = host_inputs()
+    tk.kv_plan(x["off"], x["ctx"], x["table"], x["free"], 16, x["T"])
+    cache, ws = tk.KVCache(x["k"], x["v"]), tk.KVWorkspace()
+    ws.status()
+    assert [name for name, _ in host.calls] == ["tk_kv_plan", "tk_kv_cache_create", "tk_kv_workspace_create", "tk_kv_status"]
+    host.device = 1
+    for bad in (lambda: tk.kv_plan(x["off"], x["ctx"], x["table"], x["free"], 16, x["T"]), lambda: tk.KVCache(x["k"], x["v"]),
+                ws.status):
+        with pytest.raises(ValueError):
+            bad()
+    assert len(host.calls) == 4
+    host.device = 0
+    del cache
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("hq,hk,n", [(2, 1, 1), (64, 1, 1), (16, 1, 20)])
