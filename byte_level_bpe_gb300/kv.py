@@ -58,6 +58,15 @@ def _vector(x, name, dtype, n, index):
     return x.data_ptr()
 
 
+def _row_stride(stride, rows, width, name):
+    """Elements from a row to the next; of one row or empty ones torch's stride says nothing."""
+    if rows < 2 or width == 0:
+        return width
+    if stride < width:
+        raise ValueError(f"the rows of {name} must not overlap (an expanded tensor is not taken)")
+    return stride
+
+
 def _table(table, R, dtype, index):
     """(address, row stride, width) of a block table."""
     if table.dim() != 2 or table.dtype is not dtype or table.get_device() != index or index < 0 or table.shape[0] != R:
@@ -66,7 +75,7 @@ def _table(table, R, dtype, index):
     W = table.shape[1]
     if unit != 1 and W > 1:
         raise ValueError("the rows of table must be contiguous")
-    return table.data_ptr(), stride if R > 1 and stride > W else W, W
+    return table.data_ptr(), _row_stride(stride, R, W, "table"), W
 
 
 class KVPlan(NamedTuple):
@@ -204,7 +213,7 @@ class KVCache:
         elif (out.shape != (T, q_heads, d) or out.dtype is not self.dtype or not out.is_contiguous()
               or out.get_device() != index):
             raise ValueError("out must be a contiguous tensor [T, q_heads, head_dim] of the cache's type")
-        rc = native.load().tk_kv_append(self._h, qkv.data_ptr(), row if T > 1 and row > width else width, T, q_heads, p_qg,
+        rc = native.load().tk_kv_append(self._h, qkv.data_ptr(), _row_stride(row, T, width, "qkv"), T, q_heads, p_qg,
                                         p_kg, eps, p_rope, n_rope, rot, 1 if neighbours else 0, p_pos, p_slot,
                                         out.data_ptr(), _stream(stream, index))
         if rc:
@@ -235,7 +244,7 @@ class KVCache:
         elif out.shape != q.shape or out.dtype is not self.dtype or not out.is_contiguous() or out.get_device() != index:
             raise ValueError("out must be a contiguous tensor of q's shape and type")
         sums = torch.empty((T, hq), dtype=torch.float32, device=self.device) if lse else None
-        rc = native.load().tk_kv_attend(self._h, workspace._h, q.data_ptr(), step if T > 1 else hq * d, hq, p_off, R, T,
+        rc = native.load().tk_kv_attend(self._h, workspace._h, q.data_ptr(), _row_stride(step, T, hq * d, "q"), hq, p_off, R, T,
                                         T if max_new is None else max_new, p_len, p_table, stride, W, p_mask,
                                         d ** -0.5 if scale is None else scale, out.data_ptr(),
                                         sums.data_ptr() if lse else None, _stream(stream, index))

@@ -76,6 +76,31 @@ def test_tensors_of_another_device_are_refused(tk, host):
     del cache
 
 
+def test_rows_that_overlap_are_refused(tk, host):
+    """Expanded (stride 0) and overlapping tensors: packed rows in their place would lie past their storage."""
+    x = host_inputs()
+    cache, ws = tk.KVCache(x["k"], x["v"]), tk.KVWorkspace()
+    seen = len(host.calls)
+
+    def calls(table, qkv, q):
+        return (lambda: tk.kv_plan(x["off"], x["ctx"], table, x["free"], 16, x["T"]),
+                lambda: cache.attend(x["q"], x["off"], x["ctx"], table, ws),
+                lambda: cache.append(qkv, x["pos"], x["slots"], x["hq"]), lambda: cache.attend(q, x["off"], x["ctx"], x["table"], ws))
+
+    for bad in calls(x["table"][:1].expand(3, 4), x["qkv"][:1].expand(6, -1), x["q"][:1].expand(6, -1, -1)) + calls(
+            x["table"].as_strided((3, 4), (2, 1)), x["qkv"].as_strided((6, 512), (64, 1)), x["q"].as_strided((6, 4, 64), (64, 64, 1))):
+        with pytest.raises(ValueError):
+            bad()
+    assert len(host.calls) == seen
+    # rows further apart are passed on, of a single or empty row no stride is taken from torch
+    wide = on_cuda(torch.zeros(3, 9, dtype=torch.int32))[:, :4]
+    one = x["table"][:1].expand(1, 4).as_strided((1, 4), (0, 1))
+    tk.kv_plan(x["off"], x["ctx"], wide, x["free"], 16, x["T"])
+    tk.kv_plan(x["off"][:2], x["ctx"][:1], one, x["free"], 16, x["T"])
+    tk.kv_plan(x["off"], x["ctx"], wide[:, :0], x["free"], 16, x["T"])
+    assert [args[6:8] for _, args in host.calls[seen:]] == [(9, 4), (4, 4), (0, 0)]
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("hq,hk,n", [(2, 1, 1), (64, 1, 1), (16, 1, 20)])
