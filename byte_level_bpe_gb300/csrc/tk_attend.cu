@@ -1085,6 +1085,8 @@ extern "C" int tk_kv_workspace_create(tk_kv_workspace** out) {
     ws->counters = reinterpret_cast<unsigned*>(mem + part);
     ws->status = reinterpret_cast<KvStatus*>(mem + (part + counters + 63) / 64 * 64);
     e = cudaMemset(ws->counters, 0, counters + 64 + sizeof(KvStatus));
+    // a first call on a stream that does not wait for the legacy one would find them as they were
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
   }
   if (e != cudaSuccess) {
     tk_set_error("%s: %s", where, cudaGetErrorString(e));

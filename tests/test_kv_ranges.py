@@ -102,6 +102,32 @@ def test_rows_that_overlap_are_refused(tk, host):
 
 
 @pytest.mark.gpu
+def test_new_workspace_is_clear_on_any_stream(tk):
+    """Its counters are cleared on the legacy stream; torch's side streams do not wait for that one."""
+    L, bs = 20000, 64
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    k, v = torch.randn(2, L // bs + 1, 1, bs, 64, generator=gen, device="cuda").bfloat16()
+    q = torch.randn(3, 2, 64, generator=gen, device="cuda").bfloat16()
+    table = torch.arange(L // bs + 1, dtype=torch.int32, device="cuda")[None]
+    off, lens = torch.tensor([0, 3], device="cuda"), torch.tensor([L], dtype=torch.int32, device="cuda")
+    cache, first = tk.KVCache(k, v), tk.KVWorkspace()
+    want = cache.attend(q, off, lens, table, first)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    work = torch.randn(8192, 8192, device="cuda").bfloat16()
+    for _ in range(40):  # some 20 ms
+        work = (work @ work).clamp(-1, 1)
+    done = torch.cuda.Event()
+    done.record()
+    ws = tk.KVWorkspace()
+    assert done.query()  # the stream on which it was cleared is past that
+    with torch.cuda.stream(side):
+        got = cache.attend(q, off, lens, table, ws)
+        ws.status()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("hq,hk,n", [(2, 1, 1), (64, 1, 1), (16, 1, 20)])
 @pytest.mark.parametrize("below", [9.0, 15.0, 18.0])
