@@ -304,6 +304,8 @@ enum { TK_BF16 = 1, TK_F16 = 2 };
  * need.  A request is placed if d_ctx[r] >= 0, its blocks fit table_width, a
  * tree holds at most 64 tokens, and the free list reaches; the others take no
  * part in what follows (slots -1, their table rows as they were).  R, T < 2^31.
+ * Offsets that start below 0 or decrease place nothing: every token counts as
+ * padding, d_info[3] is the first such request, with TK_E_LIMIT.
  *
  *   d_table: the new blocks are written behind the filled ones.
  *   d_slot[T]: block * block_size + place in the block of every new token, or

@@ -101,6 +101,49 @@ def test_rows_that_overlap_are_refused(tk, host):
     assert [args[6:8] for _, args in host.calls[seen:]] == [(9, 4), (4, 4), (0, 0)]
 
 
+def guarded_plan(tk, off, ctx, T, bs=16, W=3, parents=None, free=20):
+    """kv_plan over a table between guard rows and columns. Returns the plan and the table; nothing outside it is written."""
+    R = len(ctx)
+    big = torch.full((R + 2, W + 4), 77, dtype=torch.int32, device="cuda")
+    table = big[1:-1, 2:2 + W]
+    table[:] = 1000 + torch.arange(R * W, device="cuda").view(R, W)
+    ids = torch.full((free + 64,), 1 << 29, dtype=torch.int32, device="cuda")
+    ids[32:32 + free] = torch.arange(free, device="cuda")
+    i64 = torch.tensor(off, dtype=torch.int64, device="cuda")
+    i32 = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+    par = None if parents is None else torch.tensor(parents, dtype=torch.int32, device="cuda")
+    p = tk.kv_plan(i64, i32, table, ids[32:32 + free], bs, T, parents=par)
+    after = table.clone()
+    table[:] = 77
+    assert bool((big == 77).all())
+    return p, after
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("T", [9, 3000])
+@pytest.mark.parametrize("off,who", [([9, 6, 3, 0], 0), ([-5, 3, 5, 9], 0), ([0, 3, 1 << 62, 9], 2), ([0, 9, 0, 9], 1),
+                                     ([-(1 << 63), (1 << 63) - 1, (1 << 63) - 1, (1 << 63) - 1], 0), ([0, 9, 8, 9], 1),
+                                     ([0] + [9, 0] * 1000, 1)])
+def test_plan_offsets_that_contradict_each_other(tk, off, who, T, tree):
+    """Nothing is placed, nothing outside the buffers is written, and the status tells of the first."""
+    R = len(off) - 1
+    p, table = guarded_plan(tk, off, [2] * R, T, parents=[-1] * T if tree else None)
+    assert p.info.tolist() == [0, 0, tk.native.TK_E_LIMIT, who]
+    assert bool((table == 1000 + torch.arange(R * 3, device="cuda").view(R, 3)).all())
+    assert bool((p.slots == -1).all()) and bool((p.requests == -1).all()) and bool((p.lengths == 2).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("end", [(1 << 63) - 1, (1 << 62), (1 << 32) + 5, (1 << 31) - 128 - 2, (1 << 31) - 1])
+@pytest.mark.parametrize("ctx", [2, 16, (1 << 31) - 1])
+def test_plan_more_tokens_than_positions(tk, end, ctx):
+    """A request whose end is past 31 bits, or 63, is not placed, however its sums would wrap."""
+    p, table = guarded_plan(tk, [0, end], [ctx], 5000)
+    assert p.info.tolist() == [0, 0, tk.native.TK_E_LIMIT, 0] and p.lengths.tolist() == [ctx]
+    assert table.tolist() == [[1000, 1001, 1002]] and bool((p.slots == -1).all())
+
+
 @pytest.mark.gpu
 def test_new_workspace_is_clear_on_any_stream(tk):
     """Its counters are cleared on the legacy stream; torch's side streams do not wait for that one."""
