@@ -36,7 +36,7 @@ struct PlanArgs {
 // What a request with the offsets [o, e) asks of the free list: blocks, or -1 if
 // it cannot be placed whatever the list holds.  Nothing is added before it is known to fit.
 __device__ __forceinline__ int plan_need(const PlanArgs& a, int64_t o, int64_t e, int ctx) {
-  if (o < 0 || e < o || ctx < 0 || e - o > INT32_MAX - 128 - ctx || (a.parent && e - o > KV_TREE_MAX)) return -1;
+  if (o < 0 || e < o || e > a.T || ctx < 0 || e - o > INT32_MAX - 128 - ctx || (a.parent && e - o > KV_TREE_MAX)) return -1;
   const int up = (1 << a.log2_bs) - 1, want = (ctx + (int)(e - o) + up) >> a.log2_bs;
   return want > a.table_width ? -1 : want - ((ctx + up) >> a.log2_bs);
 }

@@ -93,7 +93,8 @@ def kv_plan(offsets, context, table, free, block_size, n_tokens, parents=None, c
     offsets int64[R+1], context int32[R] (tokens cached already), table
     int32[R, W] (filled in place behind ceil(context / block_size) blocks),
     free int32[n] block ids, n_tokens = the new tokens (offsets[R], or more:
-    the rest is padding), parents int32[T] for drafted trees, cursor: one
+    the rest is padding; with
+    fewer, requests that end past it are not placed), parents int32[T] for drafted trees, cursor: one
     int64 on the device, e.g. an earlier plan's info[:1]."""
     torch = _torch()
     index = table.get_device()

@@ -288,7 +288,7 @@ enum { TK_BF16 = 1, TK_F16 = 2 };
  * tk_kv_plan -- block tables and slot maps from request lengths.
  *
  *   d_off[R+1]: request r's new tokens are d_off[r] .. d_off[r+1) (the encode's
- *       d_out_offsets); d_off[0] = 0, non-decreasing, d_off[R] <= T.  Tokens past
+ *       d_out_offsets); d_off[0] = 0, non-decreasing.  Tokens past
  *       d_off[R] are padding: position 0, slot -1, request -1, mask 0.
  *   d_ctx[R]: tokens of r already in the cache.  d_table[R][table_stride]: its
  *       blocks in order, the first ceil(ctx/block_size) of them filled in.
@@ -301,7 +301,7 @@ enum { TK_BF16 = 1, TK_F16 = 2 };
  *   block_size: a power of two, 16 to 128.
  *
  * In the order of the requests each takes the free blocks that its new tokens
- * need.  A request is placed if d_ctx[r] >= 0, its blocks fit table_width, a
+ * need.  A request is placed if d_ctx[r] >= 0, d_off[r+1] <= T, its blocks fit table_width, a
  * tree holds at most 64 tokens, and the free list reaches; the others take no
  * part in what follows (slots -1, their table rows as they were).  R, T < 2^31.
  * Offsets that start below 0 or decrease place nothing: every token counts as

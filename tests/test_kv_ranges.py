@@ -145,6 +145,17 @@ def test_plan_more_tokens_than_positions(tk, end, ctx):
 
 
 @pytest.mark.gpu
+def test_plan_with_fewer_tokens_than_the_offsets(tk):
+    """Requests whose tokens got no slot are not reported as stored."""
+    p, table = guarded_plan(tk, [0, 5, 30, 31], [2, 2, 2], 29)
+    assert p.info.tolist() == [0, 0, tk.native.TK_E_LIMIT, 1] and p.lengths.tolist() == [7, 2, 2]
+    assert p.slots.tolist() == [16 * 1000 + 2 + i for i in range(5)] + [-1] * 24
+    p, table = guarded_plan(tk, [0, 5, 30, 31], [2, 16, 2], 30)
+    assert p.info.tolist() == [2, 2, tk.native.TK_E_LIMIT, 2] and p.lengths.tolist() == [7, 41, 2]
+    assert p.slots.tolist() == [16 * 1000 + 2 + i for i in range(5)] + list(range(25))
+
+
+@pytest.mark.gpu
 def test_new_workspace_is_clear_on_any_stream(tk):
     """Its counters are cleared on the legacy stream; torch's side streams do not wait for that one."""
     L, bs = 20000, 64
