@@ -143,7 +143,20 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs a) {
   plan_scan(sum, s_warp, &used);
   if (__syncthreads_or(bad)) r0 = a.R;
 
+  auto nobody = [&](int from, int to) {  // tokens of no request
+    for (int t = from + tid; t < to; t += PLAN_THREADS) {
+      const int64_t at = t0 + t;
+      a.pos[at] = 0;
+      a.req[at] = -1;
+      a.slot[at] = -1;
+      if (a.parent) a.mask[at] = 0;
+    }
+  };
   int lo = 0;  // tokens before lo are written
+  if (r0 == 0 && a.R > 0) {  // what comes before the first request
+    lo = (int)min((int64_t)count, max((int64_t)0, a.off[0] - t0));
+    nobody(0, lo);
+  }
   while (lo < count && r0 < a.R) {
     const int nr = (int)min((int64_t)PLAN_THREADS, a.R - r0);
     int need = 0;
@@ -224,7 +237,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs a) {
           int32_t* entry = a.table + (r0 + k) * a.table_stride + blk;
           int id = -1;
           if (t < start || blk >= a.table_width) {
-            id = -1;  // offsets or lengths that contradict each other
+            id = -1;  // of no request's tokens
           } else if (blk < (c + up) >> a.log2_bs) {
             id = *entry;
           } else if ((unsigned)(s_base[k] + blk) < (uint64_t)a.n_free) {
@@ -280,13 +293,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs a) {
     r0 += nr;
     __syncthreads();  // the batch's shared arrays have been read
   }
-  for (int t = lo + tid; t < count; t += PLAN_THREADS) {  // tokens of no request
-    const int64_t at = t0 + t;
-    a.pos[at] = 0;
-    a.req[at] = -1;
-    a.slot[at] = -1;
-    if (a.parent) a.mask[at] = 0;
-  }
+  nobody(lo, count);
 }
 
 // -------------------------------------------------------------- tk_kv_append

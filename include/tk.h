@@ -288,7 +288,7 @@ enum { TK_BF16 = 1, TK_F16 = 2 };
  * tk_kv_plan -- block tables and slot maps from request lengths.
  *
  *   d_off[R+1]: request r's new tokens are d_off[r] .. d_off[r+1) (the encode's
- *       d_out_offsets); d_off[0] = 0, non-decreasing.  Tokens past
+ *       d_out_offsets); non-decreasing.  Tokens before d_off[0] and past
  *       d_off[R] are padding: position 0, slot -1, request -1, mask 0.
  *   d_ctx[R]: tokens of r already in the cache.  d_table[R][table_stride]: its
  *       blocks in order, the first ceil(ctx/block_size) of them filled in.

@@ -156,6 +156,26 @@ def test_plan_with_fewer_tokens_than_the_offsets(tk):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("first", [1, 3, 4, 7, 2048, 5001])
+def test_plan_tokens_before_the_first_request(tk, first, tree):
+    """Offsets may be a part of a longer batch's: what comes before them has no slot."""
+    n = [9, 0, 40, 3]
+    ctx = [20, 5, 0, 31]
+    off = np.cumsum([first] + n)
+    T = int(off[-1]) + 6
+    par = np.full(T, -1, np.int32)
+    p, table = guarded_plan(tk, off.tolist(), ctx, T, W=4, parents=par.tolist() if tree else None)
+    q, same = guarded_plan(tk, (off - first).tolist(), ctx, T - first, W=4, parents=par[first:].tolist() if tree else None)
+    assert torch.equal(table, same) and torch.equal(p.info, q.info) and torch.equal(p.lengths, q.lengths)
+    for name, none in (("positions", 0), ("slots", -1), ("requests", -1), ("masks", 0)):
+        x, y = getattr(p, name), getattr(q, name)
+        if x is not None:
+            assert bool((x[:first] == none).all()), name
+            assert torch.equal(x[first:], y), name
+
+
+@pytest.mark.gpu
 def test_new_workspace_is_clear_on_any_stream(tk):
     """Its counters are cleared on the legacy stream; torch's side streams do not wait for that one."""
     L, bs = 20000, 64
