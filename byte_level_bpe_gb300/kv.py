@@ -8,6 +8,11 @@
 offsets of drafted trees); nothing here copies to the host or waits for the
 device. Every step runs in libtk's kernels (include/tk.h, tk_kv_*): the calls
 raise without a GPU.
+
+A call queues its work on the current stream, or on the one given as `stream`: then
+it is as if that one were current (outputs are its own, the caller orders it
+after what wrote the inputs), and the inputs' memory is not handed out again
+before its work is done.
 """
 from typing import NamedTuple
 
@@ -48,8 +53,14 @@ def _need_current(index):
         raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
 
 
-def _stream(stream, index):
-    return stream.cuda_stream if stream is not None else _raw_stream(index)
+def _on(stream, call, *used):
+    """The call with `stream` as the current one; `used` are the tensors its work touches."""
+    with _torch().cuda.stream(stream):
+        result = call()
+    for x in used:
+        if x is not None:
+            x.record_stream(stream)
+    return result
 
 
 def _vector(x, name, dtype, n, index):
@@ -96,6 +107,9 @@ def kv_plan(offsets, context, table, free, block_size, n_tokens, parents=None, c
     the rest is padding; with
     fewer, requests that end past it are not placed), parents int32[T] for drafted trees, cursor: one
     int64 on the device, e.g. an earlier plan's info[:1]."""
+    if stream is not None:
+        return _on(stream, lambda: kv_plan(offsets, context, table, free, block_size, n_tokens, parents, cursor),
+                   offsets, context, table, free, parents, cursor)
     torch = _torch()
     index = table.get_device()
     i32, i64 = torch.int32, torch.int64
@@ -119,7 +133,7 @@ def kv_plan(offsets, context, table, free, block_size, n_tokens, parents=None, c
         p_mask = masks.data_ptr()
     rc = native.load().tk_kv_plan(p_off, p_ctx, R, T, block_size, p_table, stride, W, p_free, n_free, p_cur, p_par,
                                   positions.data_ptr(), slots.data_ptr(), requests.data_ptr(), lengths.data_ptr(), p_mask,
-                                  info.data_ptr(), _stream(stream, index))
+                                  info.data_ptr(), _raw_stream(index))
     if rc:
         native.check(rc, "tk_kv_plan")
     return KVPlan(positions, slots, requests, lengths, info, masks)
@@ -146,7 +160,7 @@ class KVWorkspace:
         """Waits for the stream; raises TkError for the first request that an
         attend on this workspace could not take (tk_kv_status)."""
         _need_current(self._index)
-        native.tk_kv_status(self._h, _stream(stream, self._index))
+        native.tk_kv_status(self._h, stream.cuda_stream if stream is not None else _raw_stream(self._index))
 
     def close(self):
         if self._h is not None:
@@ -190,6 +204,9 @@ class KVCache:
         head_dim], normed and rotated; keys (normed, rotated) and values are
         stored at `slots` (tk_kv_append). gains float32[head_dim], rope
         float32[n, rot_dim / 2, 2] (`rope_table`)."""
+        if stream is not None:
+            return _on(stream, lambda: self.append(qkv, positions, slots, q_heads, q_gain, k_gain, rope, eps, neighbours, out),
+                       qkv, positions, slots, q_gain, k_gain, rope, out, self.k, self.v)
         torch = _torch()
         index, d = self._index, self.head_dim
         T, width = qkv.shape  # a ValueError if there are not two dimensions
@@ -216,7 +233,7 @@ class KVCache:
             raise ValueError("out must be a contiguous tensor [T, q_heads, head_dim] of the cache's type")
         rc = native.load().tk_kv_append(self._h, qkv.data_ptr(), _row_stride(row, T, width, "qkv"), T, q_heads, p_qg,
                                         p_kg, eps, p_rope, n_rope, rot, 1 if neighbours else 0, p_pos, p_slot,
-                                        out.data_ptr(), _stream(stream, index))
+                                        out.data_ptr(), _raw_stream(index))
         if rc:
             native.check(rc, "tk_kv_append")
         return out
@@ -228,6 +245,9 @@ class KVCache:
         them for drafted trees, None = each token sees those before it. scale
         defaults to head_dim^-0.5; max_new: no request has more new tokens
         (T if not given). lse=True also returns float32[T, q_heads]."""
+        if stream is not None:
+            return _on(stream, lambda: self.attend(q, offsets, lengths, table, workspace, masks, scale, max_new, lse, out),
+                       q, offsets, lengths, table, masks, out, self.k, self.v)
         torch = _torch()
         index, d = self._index, self.head_dim
         T, hq, width = q.shape  # a ValueError if there are not three dimensions
@@ -248,7 +268,7 @@ class KVCache:
         rc = native.load().tk_kv_attend(self._h, workspace._h, q.data_ptr(), _row_stride(step, T, hq * d, "q"), hq, p_off, R, T,
                                         T if max_new is None else max_new, p_len, p_table, stride, W, p_mask,
                                         d ** -0.5 if scale is None else scale, out.data_ptr(),
-                                        sums.data_ptr() if lse else None, _stream(stream, index))
+                                        sums.data_ptr() if lse else None, _raw_stream(index))
         if rc:
             native.check(rc, "tk_kv_attend")
         return (out, sums) if lse else out

@@ -17,12 +17,22 @@ class OnCuda(torch.Tensor):
     """A tensor of the host that says it is on cuda:0: for what the calls check before they reach the library."""
     is_cuda = property(lambda self: True)
 
+    used = []
+
     def get_device(self):
         return 0
+
+    def record_stream(self, stream):
+        self.used.append((self.data_ptr(), stream))
 
 
 def on_cuda(x):
     return x.as_subclass(OnCuda)
+
+
+class Stream:
+    """A side stream, for calls without a GPU."""
+    cuda_stream = 4096
 
 
 class Library:
@@ -99,6 +109,87 @@ def test_rows_that_overlap_are_refused(tk, host):
     tk.kv_plan(x["off"][:2], x["ctx"][:1], one, x["free"], 16, x["T"])
     tk.kv_plan(x["off"], x["ctx"], wide[:, :0], x["free"], 16, x["T"])
     assert [args[6:8] for _, args in host.calls[seen:]] == [(9, 4), (4, 4), (0, 0)]
+
+
+def test_stream_argument_owns_the_outputs_and_keeps_the_inputs(tk, host, monkeypatch):
+    """Without a GPU: outputs are allocated with the stream current, and every tensor touched is recorded on it."""
+    x, side = host_inputs(), Stream()
+    cache, ws = tk.KVCache(x["k"], x["v"]), tk.KVWorkspace()
+    current, allocated, empty = [None], [], torch.empty
+
+    class use:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *e):
+            current.pop()
+
+    from byte_level_bpe_gb300 import kv
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(kv, "_raw_stream", lambda index: getattr(current[-1], "cuda_stream", 0))
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: (allocated.append(current[-1]), empty(*a, **k))[1])
+    gain, rope = on_cuda(torch.ones(64)), on_cuda(torch.ones(5, 32, 2))
+    par, masks, cur = on_cuda(torch.zeros(6, dtype=torch.int32)), x["slots"], x["slots"][:1]
+    out = on_cuda(torch.zeros_like(x["q"]))
+    for call, inputs in (
+            (lambda s: tk.kv_plan(x["off"], x["ctx"], x["table"], x["free"], 16, 6, parents=par, cursor=cur, stream=s),
+             (x["off"], x["ctx"], x["table"], x["free"], par, cur)),
+            (lambda s: cache.append(x["qkv"], x["pos"], x["slots"], 4, q_gain=gain, k_gain=gain, rope=rope, stream=s),
+             (x["qkv"], x["pos"], x["slots"], gain, rope, x["k"], x["v"])),
+            (lambda s: cache.append(x["qkv"], x["pos"], x["slots"], 4, out=out, stream=s), (x["qkv"], x["slots"], out)),
+            (lambda s: cache.attend(x["q"], x["off"], x["ctx"], x["table"], ws, masks=masks, lse=True, stream=s),
+             (x["q"], x["off"], x["ctx"], x["table"], masks, x["k"], x["v"])),
+            (lambda s: cache.attend(x["q"], x["off"], x["ctx"], x["table"], ws, out=out, stream=s), (x["q"], out))):
+        for stream in (None, side):
+            OnCuda.used.clear()
+            allocated.clear()
+            call(stream)
+            assert all(a is stream for a in allocated)
+            assert host.calls[-1][1][-1] == (4096 if stream else 0)  # where the kernel goes
+            for i in inputs:
+                assert ((i.data_ptr(), side) in OnCuda.used) == (stream is side)
+
+
+@pytest.mark.gpu
+def test_stream_argument(tk):
+    """The calls on a side stream give the same results; their outputs are that stream's, and inputs that are
+    let go meanwhile are not handed out again before it is done."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    z = torch.zeros
+    off, ctx = torch.tensor([0, 3, 9], device="cuda"), torch.tensor([20, 0], dtype=torch.int32, device="cuda")
+    qkv = torch.randn(9, 8 * 64, generator=gen, device="cuda").bfloat16()
+    free, rope, side = torch.arange(2, 30, dtype=torch.int32, device="cuda"), tk.rope_table(64, 64), torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device="cuda").bfloat16()
+
+    def step(stream):
+        table = z(2, 4, dtype=torch.int32, device="cuda")
+        table[0, 1] = 1
+        cache, ws = tk.KVCache(*z(2, 30, 2, 16, 64, dtype=torch.bfloat16, device="cuda")), tk.KVWorkspace()
+        rows = qkv.clone()
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                for _ in range(200):  # some 20 ms
+                    busy.matmul(busy)
+        p = tk.kv_plan(off, ctx, table, free, 16, 9, stream=stream)
+        q = cache.append(rows, p.positions, p.slots, 4, rope=rope, stream=stream)
+        at, size = rows.data_ptr(), rows.shape
+        del rows
+        if stream is not None:
+            again = torch.empty(size, dtype=torch.bfloat16, device="cuda")
+            assert not side.query() and again.data_ptr() != at
+        o = cache.attend(q, off, p.lengths, table, ws, stream=stream)
+        ws.status(stream)
+        return [p.positions, p.slots, p.info, q, o]
+
+    want, got = step(None), step(side)
+    for w, g in zip(want, got):
+        assert torch.equal(w, g)
+    owner = {b["address"]: s["stream"] for s in torch.cuda.memory_snapshot() for b in s["blocks"]}
+    assert [owner[g.data_ptr()] for g in got] == [side.cuda_stream] * 5
 
 
 def guarded_plan(tk, off, ctx, T, bs=16, W=3, parents=None, free=20):
