@@ -58,20 +58,20 @@ struct AttendArgs {
 // A request as the schedule sees it.
 struct Request {
   int t0;  // its first row of q
-  int n, ctx, len;
+  int n, ctx, len;  // n < 0: the offsets decrease
   bool good;
 };
 
 __device__ __forceinline__ Request load_request(const AttendArgs& a, int64_t r) {
   Request q;
-  int64_t t0 = a.off[r];
-  const int64_t n = a.off[r + 1] - t0, len = a.len[r];
-  q.good = n >= 0 && n <= a.max_new && (!a.mask || n <= KV_TREE_MAX) && len >= n && len <= a.table_width << a.log2_bs &&
-           t0 >= 0 && t0 + n <= a.T;
-  // rows that cannot be taken are written as zeros, inside the output whatever the offsets say
-  t0 = max((int64_t)0, min(t0, a.T));
+  const int64_t o = a.off[r], e = a.off[r + 1], len = a.len[r];
+  // rows that cannot be taken are written as zeros: inside the output whatever the offsets say,
+  // and, as long as these do not decrease, outside the other requests' rows
+  const int64_t t0 = max((int64_t)0, min(o, a.T)), n = max((int64_t)0, min(e, a.T)) - t0;
+  q.good = o >= 0 && e <= a.T && n >= 0 && n <= a.max_new && (!a.mask || n <= KV_TREE_MAX) && len >= n &&
+           len <= a.table_width << a.log2_bs;
   q.t0 = (int)t0;
-  q.n = (int)max((int64_t)0, min(n, a.T - t0));
+  q.n = (int)n;
   q.len = q.good ? (int)len : 0;
   q.ctx = q.good ? (int)(len - n) : 0;
   return q;
@@ -371,6 +371,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     int mine = 0, units = 0, longest = 0, before, coarse = 0;
     for (int r = r0; r < r1; r++) {
       const Request q = load_request(a, r);
+      if (q.n < 0) {  // requests over each other: any amount of work, and of rows with two answers
+        coarse = 1 << 21;
+        break;
+      }
       if (!q.good && blockIdx.x == 0 && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = r;
       const UnitSum w = request_work<ROWS>(a, q, plan);
       mine += w.length;
@@ -414,8 +418,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       longest = max(longest, s_longest[w]);
       coarse += s_coarse[w];
     }
-    // more than the line's 32 bits hold (offsets that run over each other may ask for any amount):
-    // nothing is done then
+    // more than the line's 32 bits hold, or offsets that decrease: nothing is done then
     const bool much = coarse >= 1 << 21;
     if (much) {
       if (blockIdx.x == 0 && tid == 0 && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = -1;

@@ -402,9 +402,9 @@ void tk_kv_workspace_free(tk_kv_workspace* ws);
  *
  * Found on the device: a request with more than max_new new tokens, with more
  * than 64 under a mask, with d_len below its new tokens, or past table_width
- * blocks.  Its rows are 0 (lse -infinity), and tk_kv_status tells of it.  A
+ * blocks, or with offsets outside [0, T].  Its rows are 0 (lse -infinity), and tk_kv_status tells of it.  A
  * block id outside the cache reads as zeros.  Tokens of no request are not written.
- * A call of 2^31 tiles of keys (of all row tiles and heads) or more does nothing.
+ * A call whose offsets decrease, or one of 2^31 tiles of keys (of all row tiles and heads) or more does nothing.
  * tk_kv_status waits for cuda_stream and gives what the workspace's calls
  * since the last tk_kv_status met first: TK_OK, TK_E_LIMIT (h_request: the
  * request; -1 if the call did nothing) or TK_E_TIMEOUT (a wait

@@ -4,7 +4,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_kv import U, _close  # noqa: E402
+from test_kv import U, _attend_case, _close  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -264,6 +264,50 @@ def test_plan_tokens_before_the_first_request(tk, first, tree):
         if x is not None:
             assert bool((x[:first] == none).all()), name
             assert torch.equal(x[first:], y), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first,last", [(-5, 9), (-(1 << 63), 9), (0, 12), (0, (1 << 63) - 1), (-1, 1 << 40)])
+def test_attend_offsets_past_the_tokens(tk, first, last):
+    """A request that reaches outside the tokens gives zeros; it writes no other one's rows."""
+    gen = torch.Generator().manual_seed(5)
+    new, ctx = [3, 2, 1, 3], [20, 30, 10, 300]
+    q, k, v, off, lens, table = _attend_case(gen, new, ctx, 4, 2, 64, 16, torch.bfloat16)
+    q, k, v, off, lens, table = (x.cuda() for x in (q, k, v, off, lens, table))
+    cache, ws = tk.KVCache(k, v), tk.KVWorkspace()
+    want = cache.attend(q, off, lens, table, ws)
+    ws.status()
+    bad = off.clone()
+    bad[0], bad[-1] = first, last
+    got, lse = cache.attend(q, bad, lens, table, ws, lse=True)
+    with pytest.raises(tk.TkError) as e:
+        ws.status()
+    assert e.value.code == tk.native.TK_E_LIMIT
+    for r, (a, b) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
+        if (r == 0 and first < 0) or (r == 3 and last > 9):
+            assert bool((got[a:b] == 0).all()) and bool(torch.isneginf(lse[a:b]).all())
+        else:
+            assert torch.equal(got[a:b], want[a:b])
+
+
+@pytest.mark.gpu
+def test_attend_offsets_that_decrease(tk):
+    """Many requests over the same tokens ask for work without end: none of it is done."""
+    R, T, bs = 4001, 1 << 20, 128
+    W = T // bs
+    z = torch.zeros
+    cache, ws = tk.KVCache(*z(2, 4, 1, bs, 64, dtype=torch.bfloat16, device="cuda")), tk.KVWorkspace()
+    q = z(T, 1, 64, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, T] * ((R + 1) // 2), device="cuda")
+    lens, table = torch.full((R,), T, dtype=torch.int32, device="cuda"), z(R, W, dtype=torch.int32, device="cuda")
+    cache.attend(q, off, lens, table, ws)
+    with pytest.raises(tk.TkError) as e:
+        ws.status()
+    assert e.value.code == tk.native.TK_E_LIMIT
+    off = torch.cat([torch.arange(200, device="cuda"), torch.arange(R - 199, device="cuda")])  # one step back, far on
+    cache.attend(q, off, lens, table, ws)
+    with pytest.raises(tk.TkError) as e:
+        ws.status()
 
 
 @pytest.mark.gpu
