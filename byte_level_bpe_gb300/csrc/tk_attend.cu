@@ -369,6 +369,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     const int R = (int)a.R, per = (R + AT_THREADS - 1) / AT_THREADS;
     const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
     int mine = 0, units = 0, longest = 0, before, coarse = 0;
+    const int64_t head = R ? a.off[0] : 0, tail = R ? a.off[R] : 0;
     for (int r = r0; r < r1; r++) {
       const Request q = load_request(a, r);
       if (q.n < 0) {  // requests over each other: any amount of work, and of rows with two answers
@@ -423,6 +424,19 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     if (much) {
       if (blockIdx.x == 0 && tid == 0 && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = -1;
       total = mine = units = 0;
+    }
+    // rows of no request are zeros, so that padding carries nothing on; after the last and before the first
+    auto nobody = [&](int64_t from, int64_t to) {
+      const int64_t me = (int64_t)blockIdx.x * AT_THREADS + tid, all = (int64_t)gridDim.x * AT_THREADS;
+      for (int64_t i = from * a.hq * (D / 8) + me; i < to * a.hq * (D / 8); i += all)
+        static_cast<uint4*>(a.out)[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int64_t i = from * a.hq + me; i < to * a.hq; i += all) a.lse[i] = -INFINITY;
+    };
+    if (much) nobody(0, a.T);
+    else if (head > 0 || tail < a.T) {
+      nobody(0, min(head, a.T));
+      nobody(max(tail, (int64_t)0), a.T);
     }
     const int workers = gridDim.x * WORKERS;
     auto over = [](int x, int y) { return (int)((unsigned)(x + y - 1) / (unsigned)y); };
@@ -1152,8 +1166,8 @@ extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const
   if (T * n_q_heads > INT32_MAX) return attend_arg(where, "T times n_q_heads is above 2^31");
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev != cache->device) return attend_arg(where, "the current device is not the cache's");
-  if (T == 0 || R == 0) return TK_OK;
-  if (!d_q || !d_off || !d_len || !d_out || (table_width > 0 && !d_table)) return attend_arg(where, "null pointer");
+  if (T == 0) return TK_OK;
+  if (!d_q || !d_out || (R > 0 && (!d_off || !d_len || (table_width > 0 && !d_table)))) return attend_arg(where, "null pointer");
   if ((((uintptr_t)d_q | (uintptr_t)d_out) & 15) != 0) return attend_arg(where, "a buffer is not 16-byte aligned");
   const int group = n_q_heads / cache->n_heads;
   AttendArgs a = {d_q, q_stride, n_q_heads, cache->n_heads, group, d_off, R, T, max_new, d_len, d_table, table_stride,

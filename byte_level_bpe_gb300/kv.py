@@ -244,7 +244,8 @@ class KVCache:
         tokens over its cache (tk_kv_attend). masks int64[T] as `kv_plan` makes
         them for drafted trees, None = each token sees those before it. scale
         defaults to head_dim^-0.5; max_new: no request has more new tokens
-        (T if not given). lse=True also returns float32[T, q_heads]."""
+        (T if not given). lse=True also returns float32[T, q_heads]. Tokens of
+        no request, and rows that see nothing, give 0 and an lse of -inf."""
         if stream is not None:
             return _on(stream, lambda: self.attend(q, offsets, lengths, table, workspace, masks, scale, max_new, lse, out),
                        q, offsets, lengths, table, masks, out, self.k, self.v)

@@ -403,11 +403,12 @@ void tk_kv_workspace_free(tk_kv_workspace* ws);
  * Found on the device: a request with more than max_new new tokens, with more
  * than 64 under a mask, with d_len below its new tokens, or past table_width
  * blocks, or with offsets outside [0, T].  Its rows are 0 (lse -infinity), and tk_kv_status tells of it.  A
- * block id outside the cache reads as zeros.  Tokens of no request are not written.
- * A call whose offsets decrease, or one of 2^31 tiles of keys (of all row tiles and heads) or more does nothing.
+ * block id outside the cache reads as zeros.  Tokens of no request (before d_off[0], from
+ * d_off[R] on) give 0 and -infinity.
+ * A call whose offsets decrease, or one of 2^31 tiles of keys (of all row tiles and heads) or more gives them for every token.
  * tk_kv_status waits for cuda_stream and gives what the workspace's calls
  * since the last tk_kv_status met first: TK_OK, TK_E_LIMIT (h_request: the
- * request; -1 if the call did nothing) or TK_E_TIMEOUT (a wait
+ * request; -1 if nothing was done) or TK_E_TIMEOUT (a wait
  * on the device gave up, never expected; the outputs are unspecified).
  */
 int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const void* d_q, int64_t q_stride,

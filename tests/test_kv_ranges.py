@@ -291,6 +291,34 @@ def test_attend_offsets_past_the_tokens(tk, first, last):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("first,behind", [(0, 1), (2, 0), (3, 500), (700, 0)])
+@pytest.mark.parametrize("d,dtype,max_new", [(64, torch.bfloat16, 3), (128, torch.float16, 40), (128, torch.bfloat16, None)])
+def test_attend_padding_is_zero(tk, first, behind, d, dtype, max_new):
+    """Tokens before the first and after the last request, as padded batches have them; a batch of them alone."""
+    gen = torch.Generator().manual_seed(6)
+    q, k, v, off, lens, table = (x.cuda() for x in _attend_case(gen, [3, 0, 2], [20, 30, 500], 4, 2, d, 16, dtype))
+    cache, ws = tk.KVCache(k, v), tk.KVWorkspace()
+    # as many tokens: the variants, chosen by the bound on a request's, sum in other orders
+    same = torch.cat([q, torch.zeros(first + behind, 4, d, dtype=dtype, device="cuda")])
+    want, want_lse = (x[:5] for x in cache.attend(same, off, lens, table, ws, max_new=max_new, lse=True))
+    none = float("nan")
+    wide = torch.full((first + 5 + behind, 4, d), none, dtype=dtype, device="cuda")
+    wide[first:first + 5] = q
+    got, lse = cache.attend(wide, off + first, lens, table, ws, max_new=max_new, lse=True, out=torch.full_like(wide, none))
+    ws.status()
+    assert torch.equal(got[first:first + 5], want) and torch.equal(lse[first:first + 5], want_lse)
+    for a, b in ((0, first), (first + 5, first + 5 + behind)):
+        assert bool((got[a:b] == 0).all()) and bool(torch.isneginf(lse[a:b]).all())
+    got, lse = cache.attend(wide, off[:1], lens[:0], table[:0], ws, max_new=max_new, lse=True, out=torch.full_like(wide, none))
+    ws.status()
+    assert bool((got == 0).all()) and bool(torch.isneginf(lse).all())
+    got, lse = cache.attend(wide, off.flip(0), lens, table, ws, max_new=max_new, lse=True, out=torch.full_like(wide, none))
+    with pytest.raises(tk.TkError):
+        ws.status()
+    assert bool((got == 0).all()) and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.gpu
 def test_attend_offsets_that_decrease(tk):
     """Many requests over the same tokens ask for work without end: none of it is done."""
     R, T, bs = 4001, 1 << 20, 128
