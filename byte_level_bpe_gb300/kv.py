@@ -53,6 +53,13 @@ def _need_current(index):
         raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
 
 
+def _no_gradient(name, *tensors):
+    """There is no backward pass: a result without a gradient must not pass for one that has it."""
+    for x in tensors:
+        if x is not None and x.requires_grad and _T.is_grad_enabled():
+            raise ValueError(f"{name} has no gradient: call it under torch.no_grad(), or detach its inputs")
+
+
 def _on(stream, call, *used):
     """The call with `stream` as the current one; `used` are the tensors its work touches."""
     with _torch().cuda.stream(stream):
@@ -215,6 +222,7 @@ class KVCache:
                 or unit != 1):
             raise ValueError(f"qkv must be {self.dtype}[T, (q_heads + 2 kv_heads) * head_dim] on cuda:{index}, "
                              "rows contiguous")
+        _no_gradient("append", qkv, q_gain, k_gain, rope)
         f32 = torch.float32
         p_qg = _vector(q_gain, "q_gain", f32, d, index) if q_gain is not None else None
         p_kg = _vector(k_gain, "k_gain", f32, d, index) if k_gain is not None else None
@@ -256,6 +264,7 @@ class KVCache:
         if (width != d or q.dtype is not self.dtype or q.get_device() != index or unit != 1
                 or (head != d and hq > 1)):
             raise ValueError(f"q must be {self.dtype}[T, q_heads, head_dim] on cuda:{index}, the heads of a token contiguous")
+        _no_gradient("attend", q, self.k, self.v)
         R = lengths.numel()
         p_table, stride, W = _table(table, R, torch.int32, index)
         p_off = _vector(offsets, "offsets", torch.int64, R + 1, index)

@@ -111,6 +111,26 @@ def test_rows_that_overlap_are_refused(tk, host):
     assert [args[6:8] for _, args in host.calls[seen:]] == [(9, 4), (4, 4), (0, 0)]
 
 
+def test_inputs_that_require_a_gradient_are_refused(tk, host):
+    """A loss over the outputs would train nothing, without a word."""
+    x = host_inputs()
+    cache, ws = tk.KVCache(x["k"], x["v"]), tk.KVWorkspace()
+    seen = len(host.calls)
+    qkv, q = (on_cuda(x[name].clone().requires_grad_()) for name in ("qkv", "q"))
+    gain = on_cuda(torch.ones(64).requires_grad_())
+    calls = (lambda: cache.append(qkv, x["pos"], x["slots"], 4), lambda: cache.append(x["qkv"], x["pos"], x["slots"], 4, q_gain=gain),
+             lambda: cache.append(x["qkv"], x["pos"], x["slots"], 4, k_gain=gain),
+             lambda: cache.attend(q, x["off"], x["ctx"], x["table"], ws))
+    for bad in calls:
+        with pytest.raises(ValueError):
+            bad()
+    assert len(host.calls) == seen
+    with torch.no_grad():
+        for fine in calls:
+            fine()
+    assert len(host.calls) == seen + 4
+
+
 def test_stream_argument_owns_the_outputs_and_keeps_the_inputs(tk, host, monkeypatch):
     """Without a GPU: outputs are allocated with the stream current, and every tensor touched is recorded on it."""
     x, side = host_inputs(), Stream()
