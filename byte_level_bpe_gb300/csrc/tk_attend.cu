@@ -97,7 +97,7 @@ __device__ __forceinline__ int key_tiles(int keys) {
 // gathered in one; a cut within AT_SNAP of a unit's start or end moves there.
 // Padded: there are fewer units than workers; a unit's length is rounded up to
 // whole shares and divided evenly over its workers, each of which has that one piece.
-// (A line of 2^31 and more is refused.)
+// (A line of 2^31 and more is refused; from 2^30 on one may be: a request counts as up to 1,024 more.)
 struct Plan {
   int share;
   bool padded;
@@ -441,7 +441,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     const int workers = gridDim.x * WORKERS;
     auto over = [](int x, int y) { return (int)((unsigned)(x + y - 1) / (unsigned)y); };
     plan.share = max(AT_MIN_SHARE, over(total, workers));
-    if (units > 0 && units < workers) {
+    // (a padded line is at most a quarter longer and 8 * workers: it fits 31 bits with what it is below here)
+    if (units > 0 && units < workers && total <= 1 << 30) {
       // shares that give the units no more workers than there are
       const int share = max(AT_MIN_SHARE, min(over(longest, workers / units), over(total, workers - units)));
       // What a worker may do more if it has a single piece for that.  Up to 128 rows memory is the

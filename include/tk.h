@@ -405,7 +405,10 @@ void tk_kv_workspace_free(tk_kv_workspace* ws);
  * blocks, or with offsets outside [0, T].  Its rows are 0 (lse -infinity), and tk_kv_status tells of it.  A
  * block id outside the cache reads as zeros.  Tokens of no request (before d_off[0], from
  * d_off[R] on) give 0 and -infinity.
- * A call whose offsets decrease, or one of 2^31 tiles of keys (of all row tiles and heads) or more gives them for every token.
+ * A call whose offsets decrease gives them for every token, and so may one of too much
+ * work: 2^30 tiles of keys or more, over all key heads and tiles of query rows, three
+ * tiles more for each of these (64 keys and 32 or 128 rows a tile; 128 and 256 from
+ * 129 rows a key head on; from 2^31 on it always does).
  * tk_kv_status waits for cuda_stream and gives what the workspace's calls
  * since the last tk_kv_status met first: TK_OK, TK_E_LIMIT (h_request: the
  * request; -1 if nothing was done) or TK_E_TIMEOUT (a wait
