@@ -525,6 +525,16 @@ extern "C" int tk_kv_plan(const int64_t* d_off, const int32_t* d_ctx, int64_t R,
     return kv_arg("tk_kv_plan", "null pointer");
   if (!aligned16(d_pos) || !aligned16(d_slot) || !aligned16(d_req) || !aligned16(d_mask))
     return kv_arg("tk_kv_plan", "an output is not 16-byte aligned");
+  // one CTA writes what another has yet to read
+  const struct {
+    const void* p;
+    int64_t bytes;
+  } ins[] = {{d_off, 8 * (R + 1)}, {d_ctx, 4 * R}, {d_free, 4 * n_free}, {d_cursor, 8}, {d_parent, 4 * T}},
+    outs[] = {{d_pos, 4 * T}, {d_slot, 8 * T}, {d_req, 4 * T}, {d_len, 4 * R}, {d_mask, 8 * T}, {d_info, 32}};
+  for (const auto& x : ins)
+    for (const auto& y : outs)
+      if (x.p && y.p && (uintptr_t)x.p < (uintptr_t)y.p + y.bytes && (uintptr_t)y.p < (uintptr_t)x.p + x.bytes)
+        return kv_arg("tk_kv_plan", "an output overlaps an input");
   int dev = 0, sms = 1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -318,6 +318,8 @@ enum { TK_BF16 = 1, TK_F16 = 2 };
  *   d_info[4]: cursor after the call, free blocks asked for by all requests,
  *       status of the first request not placed (TK_E_LIMIT, TK_E_CAPACITY; 0
  *       if all were), that request (-1).
+ *
+ * No output overlaps an input (d_len is not d_ctx, d_info not where d_cursor is): TK_E_ARG.
  */
 int tk_kv_plan(const int64_t* d_off, const int32_t* d_ctx, int64_t R, int64_t T, int block_size,
                int32_t* d_table, int64_t table_stride, int64_t table_width, const int32_t* d_free,

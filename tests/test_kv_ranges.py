@@ -111,6 +111,21 @@ def test_rows_that_overlap_are_refused(tk, host):
     assert [args[6:8] for _, args in host.calls[seen:]] == [(9, 4), (4, 4), (0, 0)]
 
 
+@pytest.mark.parametrize("out,over", [("len", "ctx"), ("info", "cur"), ("pos", "par"), ("slot", "off"), ("req", "free"), ("mask", "off"),
+                                      ("len", "off")])
+@pytest.mark.parametrize("shift", [-16, 0, 16])
+def test_plan_outputs_over_inputs_are_refused(tk, out, over, shift):
+    """In place, one CTA would write the lengths or the cursor that another has yet to read."""
+    if (over, shift) == ("cur", 16):
+        shift = -24  # one value: behind the first of the four
+    names = ("off", "ctx", "table", "free", "cur", "par", "pos", "slot", "req", "len", "mask", "info")
+    at = {name: (i + 1) << 20 for i, name in enumerate(names)}
+    at[out] = at[over] + shift
+    rc = tk.native.load().tk_kv_plan(at["off"], at["ctx"], 9, 40, 16, at["table"], 4, 4, at["free"], 8, at["cur"], at["par"],
+                                     at["pos"], at["slot"], at["req"], at["len"], at["mask"], at["info"], None)
+    assert rc == tk.native.TK_E_ARG and b"overlaps" in tk.native.load().tk_last_error()
+
+
 def test_inputs_that_require_a_gradient_are_refused(tk, host):
     """A loss over the outputs would train nothing, without a word."""
     x = host_inputs()
