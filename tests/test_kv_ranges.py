@@ -197,7 +197,9 @@ def test_stream_argument(tk):
     off, ctx = torch.tensor([0, 3, 9], device="cuda"), torch.tensor([20, 0], dtype=torch.int32, device="cuda")
     qkv = torch.randn(9, 8 * 64, generator=gen, device="cuda").bfloat16()
     free, rope, side = torch.arange(2, 30, dtype=torch.int32, device="cuda"), tk.rope_table(64, 64), torch.cuda.Stream()
-    busy = torch.randn(4096, 4096, device="cuda").bfloat16()
+    busy = torch.randn(8192, 8192, device="cuda").bfloat16()
+
+    product = torch.empty_like(busy)
 
     def step(stream):
         table = z(2, 4, dtype=torch.int32, device="cuda")
@@ -207,8 +209,8 @@ def test_stream_argument(tk):
         torch.cuda.synchronize()
         if stream is not None:
             with torch.cuda.stream(stream):
-                for _ in range(200):  # some 20 ms
-                    busy.matmul(busy)
+                for _ in range(300):  # some 200 ms
+                    torch.mm(busy, busy, out=product)
         p = tk.kv_plan(off, ctx, table, free, 16, 9, stream=stream)
         q = cache.append(rows, p.positions, p.slots, 4, rope=rope, stream=stream)
         at, size = rows.data_ptr(), rows.shape
