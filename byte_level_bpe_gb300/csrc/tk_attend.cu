@@ -1036,7 +1036,11 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       }
     }
   }
-  if (*abort && lane == 0 && atomicCAS(&a.status->code, 0, TK_E_TIMEOUT) == 0) a.status->request = -1;
+  // over whatever was met before: tk_kv_status clears the counters for this one only
+  if (*abort && lane == 0) {
+    atomicExch(&a.status->code, TK_E_TIMEOUT);
+    a.status->request = -1;
+  }
   tmem_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -412,7 +412,7 @@ void tk_kv_workspace_free(tk_kv_workspace* ws);
  * tiles more for each of these (64 keys and 32 or 128 rows a tile; 128 and 256 from
  * 129 rows a key head on; from 2^31 on it always does).
  * tk_kv_status waits for cuda_stream and gives what the workspace's calls
- * since the last tk_kv_status met first: TK_OK, TK_E_LIMIT (h_request: the
+ * since the last tk_kv_status met first (a timeout before others): TK_OK, TK_E_LIMIT (h_request: the
  * request; -1 if nothing was done) or TK_E_TIMEOUT (a wait
  * on the device gave up, never expected; the outputs are unspecified).
  */
