@@ -256,13 +256,6 @@ def tk_last_cache_stats(ws):
     return a.value, b.value
 
 
-def tk_kv_plan(d_off, d_ctx, R, T, block_size, d_table, table_stride, table_width, d_free, n_free, d_cursor,
-               d_parent, d_pos, d_slot, d_req, d_len, d_mask, d_info, stream):
-    """Device pointers (ints)."""
-    check(load().tk_kv_plan(d_off, d_ctx, R, T, block_size, d_table, table_stride, table_width, d_free, n_free,
-                            d_cursor, d_parent, d_pos, d_slot, d_req, d_len, d_mask, d_info, stream), "tk_kv_plan")
-
-
 def tk_kv_cache_create(d_k, d_v, type, n_blocks, n_heads, block_size, head_dim, stride=None):
     """stride: three ints (block, head, token, in elements) or None. Returns the handle."""
     h = _P()
@@ -277,13 +270,6 @@ def tk_kv_cache_free(cache):
         load().tk_kv_cache_free(cache)
 
 
-def tk_kv_append(cache, d_qkv, row_stride, T, n_q_heads, d_q_gain, d_k_gain, eps, d_rope, rope_len, rot_dim,
-                 neighbours, d_pos, d_slot, d_q, stream):
-    """Device pointers (ints)."""
-    check(load().tk_kv_append(cache, d_qkv, row_stride, T, n_q_heads, d_q_gain, d_k_gain, eps, d_rope, rope_len,
-                              rot_dim, 1 if neighbours else 0, d_pos, d_slot, d_q, stream), "tk_kv_append")
-
-
 def tk_kv_workspace_create():
     h = _P()
     check(load().tk_kv_workspace_create(ctypes.byref(h)), "tk_kv_workspace_create")
@@ -293,13 +279,6 @@ def tk_kv_workspace_create():
 def tk_kv_workspace_free(ws):
     if ws:
         load().tk_kv_workspace_free(ws)
-
-
-def tk_kv_attend(cache, ws, d_q, q_stride, n_q_heads, d_off, R, T, max_new, d_len, d_table, table_stride,
-                 table_width, d_mask, scale, d_out, d_lse, stream):
-    """Device pointers (ints)."""
-    check(load().tk_kv_attend(cache, ws, d_q, q_stride, n_q_heads, d_off, R, T, max_new, d_len, d_table,
-                              table_stride, table_width, d_mask, scale, d_out, d_lse, stream), "tk_kv_attend")
 
 
 def tk_kv_status(ws, stream, raise_on_error=True):
