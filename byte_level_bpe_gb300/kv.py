@@ -4,8 +4,11 @@
     q = cache.append(qkv, plan.positions, plan.slots, q_heads, ...)       # norm, rotate, store
     out = cache.attend(q, offsets, plan.lengths, table, workspace)        # read the cache
 
-`offsets` is what `encode_device` / `encode_segments` returned (or the
-offsets of drafted trees); nothing here copies to the host or waits for the
+`offsets` has an entry where each request's tokens begin, and the end: what
+`encode_device` / `encode_segments` returned if a request is one segment. The
+encode counts segments, so for requests of several it is `offsets[first]`, with
+first = the number of each request's first segment and, last, of all segments
+(an index tensor on the device). For drafted trees it is theirs. Nothing here copies to the host or waits for the
 device. Every step runs in libtk's kernels (include/tk.h, tk_kv_*): the calls
 raise without a GPU.
 

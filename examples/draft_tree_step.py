@@ -79,8 +79,12 @@ def _offsets(counts):
 
 
 def prefill(model, tokenizer, prompts, width, n_blocks):
-    """Encodes and stores the prompts; returns the batch and each request's first new token."""
-    ids, offsets = tokenizer.encode_segments([(p, False) for p in prompts])
+    """Encodes and stores the prompts, each a text or a list of (text, allow_special) segments; returns the batch
+    and each request's first new token."""
+    prompts = [[(p, False)] if isinstance(p, str) else p for p in prompts]
+    ids, offsets = tokenizer.encode_segments([s for p in prompts for s in p])
+    # the encode's offsets are its segments'; a request begins with its first one
+    offsets = offsets[_offsets([len(p) for p in prompts])]
     batch = Batch(model, len(prompts), width, n_blocks)
     logits = batch.run(ids, offsets, ids.numel())
     return batch, logits[offsets[1:] - 1].argmax(-1).int()
@@ -134,7 +138,8 @@ def generate_plainly(batch, first, steps):
 def main():
     import workloads
     tokenizer = tk.Tokenizer(workloads.full_table(), workloads.SPECIALS)
-    prompts = ["Shard the request over four ranks.", "def add(a, b):\n    return a + b\n", "1, 2, 3,", "x" * 300]
+    prompts = ["Shard the request over four ranks.", "def add(a, b):\n    return a + b\n", "1, 2, 3,", "x" * 300,
+               [("What is a page?", False), ("<|endoftext|>", True), ("A block of", False)]]
     model = Model(tk.native.load().tk_max_id(tokenizer.handle) + 1, 256)
     batch, first = prefill(model, tokenizer, prompts, 40, 256)
     done, kept = generate_drafted(batch, first, 8)
@@ -143,7 +148,8 @@ def main():
     print(f"{tokens} tokens in 8 passes over {len(prompts)} requests, {kept} of them drafted")
     for prompt, ids in zip(prompts, done):
         stream = tokenizer.stream_decoder()
-        print(repr(prompt[:20]), "->", (stream.feed(ids) + stream.finish()).decode(errors="replace"))
+        text = prompt if isinstance(prompt, str) else "".join(t for t, _ in prompt)
+        print(repr(text[:20]), "->", (stream.feed(ids) + stream.finish()).decode(errors="replace"))
 
 
 if __name__ == "__main__":

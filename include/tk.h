@@ -269,7 +269,8 @@ int tk_last_cache_stats(const tk_workspace* ws, int64_t* hits, int64_t* inserts)
 /*
  * From device ids to a paged key/value cache.  The encode leaves a batch's
  * ids and their offsets on the device; the three calls below take those
- * offsets on: tk_kv_plan places every request's new tokens in the cache's
+ * offsets on, as they are where a request is one segment (of a request of several
+ * segments the offset of the first, and the last one's end: a gather on the device): tk_kv_plan places every request's new tokens in the cache's
  * blocks, tk_kv_append stores their keys and values there, tk_kv_attend reads
  * them back for the new tokens, which may be drafted trees.  The pages have
  * no counterpart: these are engineering entry points of this library.
@@ -288,7 +289,7 @@ enum { TK_BF16 = 1, TK_F16 = 2 };
  * tk_kv_plan -- block tables and slot maps from request lengths.
  *
  *   d_off[R+1]: request r's new tokens are d_off[r] .. d_off[r+1) (the encode's
- *       d_out_offsets); non-decreasing.  Tokens before d_off[0] and past
+ *       d_out_offsets at the requests' first segments); non-decreasing.  Tokens before d_off[0] and past
  *       d_off[R] are padding: position 0, slot -1, request -1, mask 0.
  *   d_ctx[R]: tokens of r already in the cache.  d_table[R][table_stride]: its
  *       blocks in order, the first ceil(ctx/block_size) of them filled in.

@@ -1,4 +1,7 @@
 """Ranges and misuse of the paged cache calls (tk_kv_*): what must hold past the ordinary cases."""
+import os
+import sys
+
 import numpy as np
 import pytest
 
@@ -444,3 +447,23 @@ def test_attend_one_strong_key(tk, dtype, hq, hk, n, below, at, R):
         tol = tol + L * 2.0 ** -32 * vv.max() + 2.0 ** -25
     _close(got, o.cpu(), tol.cpu())
     assert bool(((got_lse.double() - torch.logsumexp(s, 2)).abs() <= 2.0 ** -16 * (1 + big[..., 0])).all())
+
+
+@pytest.mark.gpu
+def test_requests_of_several_segments(tk, full_table):
+    """A prompt of typed segments is one request: the encode's offsets are gathered at the requests' first segments."""
+    import workloads
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import draft_tree_step as ex
+    tokenizer = tk.Tokenizer(full_table, workloads.SPECIALS)
+    prompts = [[("What is a page?", False), ("<|endoftext|>", True), ("A block of", False)], "1, 2, 3,",
+               [("x" * 700, False), ("", False), (" and so on", False)]]
+    model = ex.Model(100277, 512)
+    batch, first = ex.prefill(model, tokenizer, prompts, 64, 512)
+    model.workspace.status()
+    sizes = [sum(tokenizer.encode(t, a).numel() for t, a in ([(p, False)] if isinstance(p, str) else p)) for p in prompts]
+    assert batch.lengths.tolist() == sizes and batch.lengths.shape == (3,)
+    for p, want in zip(prompts, first.tolist()):
+        alone, got = ex.prefill(model, tokenizer, [p], 64, 512)
+        assert got.tolist() == [want]
+    tokenizer.close()
