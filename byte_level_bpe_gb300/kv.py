@@ -56,11 +56,10 @@ def _need_current(index):
         raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
 
 
-def _no_gradient(name, *tensors):
+def _no_gradient(name):
     """There is no backward pass: a result without a gradient must not pass for one that has it."""
-    for x in tensors:
-        if x is not None and x.requires_grad and _T.is_grad_enabled():
-            raise ValueError(f"{name} has no gradient: call it under torch.no_grad(), or detach its inputs")
+    if _T.is_grad_enabled():
+        raise ValueError(f"{name} has no gradient: call it under torch.no_grad(), or detach its inputs")
 
 
 def _on(stream, call, *used):
@@ -225,7 +224,9 @@ class KVCache:
                 or unit != 1):
             raise ValueError(f"qkv must be {self.dtype}[T, (q_heads + 2 kv_heads) * head_dim] on cuda:{index}, "
                              "rows contiguous")
-        _no_gradient("append", qkv, q_gain, k_gain, rope)
+        if (qkv.requires_grad or (q_gain is not None and q_gain.requires_grad)
+                or (k_gain is not None and k_gain.requires_grad) or (rope is not None and rope.requires_grad)):
+            _no_gradient("append")
         f32 = torch.float32
         p_qg = _vector(q_gain, "q_gain", f32, d, index) if q_gain is not None else None
         p_kg = _vector(k_gain, "k_gain", f32, d, index) if k_gain is not None else None
@@ -267,7 +268,8 @@ class KVCache:
         if (width != d or q.dtype is not self.dtype or q.get_device() != index or unit != 1
                 or (head != d and hq > 1)):
             raise ValueError(f"q must be {self.dtype}[T, q_heads, head_dim] on cuda:{index}, the heads of a token contiguous")
-        _no_gradient("attend", q, self.k, self.v)
+        if q.requires_grad or self.k.requires_grad or self.v.requires_grad:
+            _no_gradient("attend")
         R = lengths.numel()
         p_table, stride, W = _table(table, R, torch.int32, index)
         p_off = _vector(offsets, "offsets", torch.int64, R + 1, index)
