@@ -1167,7 +1167,7 @@ extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const
     return attend_arg(where, "bad size");
   if (q_stride < (int64_t)n_q_heads * cache->head_dim || q_stride % 8)
     return attend_arg(where, "q_stride is below a token's elements or no multiple of 8");
-  if (!(scale > 0.f) || scale > 3e38f) return attend_arg(where, "scale is not a positive number");
+  if (!(scale > 0.f && scale < 1e38f)) return attend_arg(where, "scale is not a positive number below 1e38");
   if (T * n_q_heads > INT32_MAX) return attend_arg(where, "T times n_q_heads is above 2^31");
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev != cache->device) return attend_arg(where, "the current device is not the cache's");

@@ -390,7 +390,7 @@ void tk_kv_workspace_free(tk_kv_workspace* ws);
  *       itself.  Else it sees the context and those new tokens j whose bit j
  *       is set, itself included only if its own bit is (requests of at most
  *       64 new tokens).
- *   scale > 0: the factor on q.k before the softmax.
+ *   scale: the factor on q.k before the softmax, above 0 and below 1e38.
  *   d_out[T][n_q_heads][head_dim] (the cache's type), d_lse[T][n_q_heads]
  *       (fp32, NULL = not wanted): the natural log of the row's sum of
  *       exponentials.  A row that sees nothing gives 0 and -infinity.

@@ -379,6 +379,23 @@ def test_attend_offsets_that_decrease(tk):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scale,taken", [(1e-38, True), (9e37, True), (2.5e38, False), (float("inf"), False)])
+def test_attend_scales(tk, scale, taken):
+    """Scores of 0 have equal weights at any scale; one that is infinite in base 2 is refused."""
+    k = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    v = torch.ones_like(k)
+    cache, ws = tk.KVCache(k, v), tk.KVWorkspace()
+    off, lens = torch.tensor([0, 2], device="cuda"), torch.tensor([20], dtype=torch.int32, device="cuda")
+    table = torch.arange(2, dtype=torch.int32, device="cuda")[None]
+    q = torch.zeros(2, 1, 64, dtype=torch.bfloat16, device="cuda")
+    if taken:
+        assert bool((cache.attend(q, off, lens, table, ws, scale=scale) == 1).all())
+    else:
+        with pytest.raises(tk.TkError):
+            cache.attend(q, off, lens, table, ws, scale=scale)
+
+
+@pytest.mark.gpu
 def test_new_workspace_is_clear_on_any_stream(tk):
     """Its counters are cleared on the legacy stream; torch's side streams do not wait for that one."""
     L, bs = 20000, 64
