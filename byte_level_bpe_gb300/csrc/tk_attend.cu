@@ -14,12 +14,14 @@
 // S, m, l and O are fp32; P is rounded to the cache's type, which the tensor
 // cores ask for, and l sums what was rounded: an error of half an ulp in each weight, but
 // none in a weight that is nearly alone (summed before the rounding, the result's error
-// against 64 bits came to 1.6 times that of rounding it alone; so it is 1.1 to 1.4 times).
+// against 64 bits came to 1.6 times that of rounding it alone; so it is 1.1 to 1.4 times, for
+// 4% of the time of the second case below).
 //
 // Bounds, on one GB300: HBM up to 128 rows (one token of 128 requests over 6k,
-// 3.25 GB: 485 us, 6.7 TB/s); above, the tensor cores and the latency of the chain from one
-// tile's scores to the next one's (64 drafted tokens over 131k, 512 rows a head: 213 us,
-// 1.29 PFLOP/s); a short call its chain of first accesses (200 keys: 9 us).
+// 3.25 GB: 488 us, 6.7 TB/s); above, the tensor cores and the latency of the chain from one
+// tile's scores to the next one's (64 drafted tokens over 131k, 512 rows a head: 219 us,
+// 1.25 PFLOP/s; 202 with the keys in L2 from the call before); a short call its chain of
+// first accesses (200 keys: 12 us).
 #include <algorithm>
 #include <new>
 #include <type_traits>
@@ -30,9 +32,18 @@
 namespace tk {
 
 constexpr int AT_THREADS = 384;  // loads and products of two streams (4 warps), their softmax (2 x 4 warps)
-constexpr int AT_UNIT_COST = 3;  // what starting a unit costs, in tiles
-constexpr int AT_MIN_SHARE = 8;  // least share of a worker, in tiles
-constexpr int AT_SNAP = 4;       // a unit is not cut nearer to its ends than this, in tiles
+// How the work is divided, in tiles.  Times of one call in a replayed graph, in us.
+// What starting a unit costs: with 1, six prompts of 2,000 tokens take 484 instead of 365 and
+// one token of 32 requests over 3k (head_dim 64) 53 instead of 45; with 6, one token of 128
+// requests over 6k 490 instead of 481, the prompts 359.
+constexpr int AT_UNIT_COST = 3;
+// Least share of a worker: with 6 (and a snap of 3) one token over 200 takes 13.3 instead of 11.8;
+// with 16 one token of 8 requests over 2k 24.6 instead of 23.0.
+constexpr int AT_MIN_SHARE = 8;
+// A unit is not cut nearer to its ends than this: with 3, 24 trees of 9 over 1.5k (head_dim 64)
+// take 41.8 instead of 41.3; with 6 (and a least share of 12) 38.6, the others the same.
+constexpr int AT_SNAP = 4;
+static_assert(AT_SNAP >= AT_UNIT_COST && AT_MIN_SHARE >= 2 * AT_SNAP, "a piece has at least one tile");
 
 struct AttendArgs {
   const void* q;
@@ -263,7 +274,8 @@ __device__ __forceinline__ uint32_t nonfinite2<__half>(uint32_t w) {
 // scores of two, so that products run under the softmax of their own stream; with
 // 128-key tiles they run under the other stream's, and read the queries half as often
 // from shared memory (for 128 rows and 64 keys that is the products' bound: 48 cycles instead of 32 for
-// k = 16).  64 drafted tokens over 131k take 218 us with the former and 204 with the latter.
+// k = 16).  64 drafted tokens over 131k take 218 us with the former and 204 with the latter (both
+// before the sums of rounded weights).
 template <int D, int MODE>
 struct AttendShape {
   static constexpr int RINGS = MODE == 2 ? 1 : 2, ROWS = MODE == 0 ? 32 : MODE == 1 ? 128 : 256;
@@ -297,8 +309,8 @@ __device__ __forceinline__ float* part_at(float* part, int stream, int slot) {
 // were slower: 267 instead of 222 us for 64 drafted tokens over 131k).  Tensor memory of a
 // stream: scores (128 columns, the weights over the first half of a tile's) and O
 // (128), 256 columns from 256 * stream.
-// LSE: the log of the sum is wanted too, and summed before the rounding (without it 64 drafted
-// tokens over 131k take 213 us, with it 224; up to 128 rows the softmax is not the bound, and it is always there).
+// LSE: the log of the sum is wanted too, and summed before the rounding (64 drafted tokens over
+// 131k, replayed: 204 us without it, 221 with it; up to 128 rows the softmax is not the bound, and it is always there).
 // Rows of no request are zeros, so that padding carries nothing on.  Rarely run: in line it cost
 // 64 drafted tokens over 131k 1% (204 instead of 202 us).
 template <int D>
@@ -450,8 +462,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       // shares that give the units no more workers than there are
       const int share = max(AT_MIN_SHARE, min(over(longest, workers / units), over(total, workers - units)));
       // What a worker may do more if it has a single piece for that.  Up to 128 rows memory is the
-      // bound, which fewer workers reach too: 32 requests of 8k tokens, 256 units for 304
-      // workers, take 183 us padded (128 tiles each) and 206 us divided evenly (108).
+      // bound, which fewer workers reach too, so that may be a quarter: 32 trees of 16 over 8k, 256
+      // units for 304 workers, take 159 us padded (128 tiles each) and 189 us divided evenly (108),
+      // 30 trees of 8 over 3k 62 and 77, one token of 32 requests over 8k of head_dim 64 109 and 106.  The 8 tiles
+      // are for more rows: two trees of 64 over 30k take 67 us padded and 82 us not.
       if (share <= plan.share + 8 + (MODE == 2 ? 0 : plan.share / 4)) {
         plan.share = share;
         plan.padded = true;

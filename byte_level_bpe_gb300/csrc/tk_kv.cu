@@ -72,7 +72,7 @@ __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t* s_warp, int64_t
 // first place.  The last CTA writes the lengths and the totals.  The CTAs agree only if
 // the offsets do not decrease, so each looks at all of them and places nothing otherwise.  A thread has four
 // tokens and looks a block up where it begins: 5.3 M tokens of 4,096 prompts, bound by
-// instructions at first (37 us), take 23 us; the 85 MB of outputs alone take 13 us.
+// instructions at first (37 us), take 24 us; the 85 MB of outputs alone take 13 us.
 __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs a) {
   __shared__ int64_t s_warp[PLAN_THREADS / 32];
   __shared__ int s_off[PLAN_THREADS + 1];  // from t0 on

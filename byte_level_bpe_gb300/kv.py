@@ -115,7 +115,8 @@ def kv_plan(offsets, context, table, free, block_size, n_tokens, parents=None, c
     free int32[n] block ids, n_tokens = the new tokens (offsets[R], or more:
     the rest is padding; with
     fewer, requests that end past it are not placed), parents int32[T] for drafted trees, cursor: one
-    int64 on the device, e.g. an earlier plan's info[:1]."""
+    int64 on the device, e.g. an earlier plan's info[:1]. info tells whether all
+    were placed; the attention's rows of one that was not mean nothing."""
     if stream is not None:
         return _on(stream, lambda: kv_plan(offsets, context, table, free, block_size, n_tokens, parents, cursor),
                    offsets, context, table, free, parents, cursor)
@@ -256,7 +257,9 @@ class KVCache:
         tokens over its cache (tk_kv_attend). masks int64[T] as `kv_plan` makes
         them for drafted trees, None = each token sees those before it. scale
         defaults to head_dim^-0.5; max_new: no request has more new tokens
-        (T if not given). lse=True also returns float32[T, q_heads]. Tokens of
+        (T if not given; it chooses the kernel, so give it: a decode step with
+        max_new=1 can be a quarter faster). Requests outside the call's limits
+        give 0, and only workspace.status() tells. lse=True also returns float32[T, q_heads]. Tokens of
         no request, and rows that see nothing, give 0 and an lse of -inf."""
         if stream is not None:
             return _on(stream, lambda: self.attend(q, offsets, lengths, table, workspace, masks, scale, max_new, lse, out),

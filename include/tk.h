@@ -303,8 +303,10 @@ enum { TK_BF16 = 1, TK_F16 = 2 };
  *
  * In the order of the requests each takes the free blocks that its new tokens
  * need.  A request is placed if d_ctx[r] >= 0, d_off[r+1] <= T, its blocks fit table_width, a
- * tree holds at most 64 tokens, and the free list reaches; the others take no
- * part in what follows (slots -1, their table rows as they were).  R, T < 2^31.
+ * tree holds at most 64 tokens, and the free list reaches; the others get
+ * no slots and no blocks (slots -1, their table rows as they were).  d_info tells of them:
+ * tk_kv_attend cannot, it takes the last tokens of such a request's context for its new
+ * ones, so its rows mean nothing.  R, T < 2^31.
  * Offsets that start below 0 or decrease place nothing: every token counts as
  * padding, d_info[3] is the first such request, with TK_E_LIMIT.
  *
@@ -385,7 +387,9 @@ void tk_kv_workspace_free(tk_kv_workspace* ws);
  *       h / (n_q_heads / n_heads).
  *   d_off[R+1], d_len[R], d_table: as tk_kv_plan has them; d_len counts the
  *       new tokens, which are stored already.
- *   max_new: no request has more new tokens than this (T always holds).
+ *   max_new: no request has more new tokens than this (T always holds, but the rows of a
+ *       request and key head choose the kernel: one token of 64 requests over 1k, 4 query heads a
+ *       key head, takes 56 us with max_new = 1 and 73 with T).
  *   d_mask[T]: NULL = new token i sees the context and the new tokens up to
  *       itself.  Else it sees the context and those new tokens j whose bit j
  *       is set, itself included only if its own bit is (requests of at most
