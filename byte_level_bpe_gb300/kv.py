@@ -8,9 +8,9 @@
 `encode_device` / `encode_segments` returned if a request is one segment. The
 encode counts segments, so for requests of several it is `offsets[first]`, with
 first = the number of each request's first segment and, last, of all segments
-(an index tensor on the device). For drafted trees it is theirs. Nothing here copies to the host or waits for the
-device. Every step runs in libtk's kernels (include/tk.h, tk_kv_*): the calls
-raise without a GPU.
+(an index tensor on the device). For drafted trees it is theirs. Nothing here
+copies to the host or waits for the device. Every step runs in libtk's kernels
+(include/tk.h, tk_kv_*): the calls raise without a GPU.
 
 A call queues its work on the current stream, or on the one given as `stream`: then
 it is as if that one were current (outputs are its own, the caller orders it
@@ -113,10 +113,10 @@ def kv_plan(offsets, context, table, free, block_size, n_tokens, parents=None, c
     offsets int64[R+1], context int32[R] (tokens cached already), table
     int32[R, W] (filled in place behind ceil(context / block_size) blocks),
     free int32[n] block ids, n_tokens = the new tokens (offsets[R], or more:
-    the rest is padding; with
-    fewer, requests that end past it are not placed), parents int32[T] for drafted trees, cursor: one
-    int64 on the device, e.g. an earlier plan's info[:1]. info tells whether all
-    were placed; the attention's rows of one that was not mean nothing."""
+    the rest is padding; with fewer, requests that end past it are not placed),
+    parents int32[T] for drafted trees, cursor: one int64 on the device, e.g. an
+    earlier plan's info[:1]. info tells whether all were placed; the attention's
+    rows of one that was not mean nothing."""
     if stream is not None:
         return _on(stream, lambda: kv_plan(offsets, context, table, free, block_size, n_tokens, parents, cursor),
                    offsets, context, table, free, parents, cursor)
@@ -258,9 +258,10 @@ class KVCache:
         them for drafted trees, None = each token sees those before it. scale
         defaults to head_dim^-0.5; max_new: no request has more new tokens
         (T if not given; it chooses the kernel, so give it: a decode step with
-        max_new=1 can be a quarter faster). Requests outside the call's limits
-        give 0, and only workspace.status() tells. lse=True also returns float32[T, q_heads]. Tokens of
-        no request, and rows that see nothing, give 0 and an lse of -inf."""
+        max_new=1 can be a quarter faster). lse=True also returns
+        float32[T, q_heads]. Tokens of no request, and rows that see nothing, give
+        0 and an lse of -inf; so do requests outside the call's limits, of which
+        only workspace.status() tells."""
         if stream is not None:
             return _on(stream, lambda: self.attend(q, offsets, lengths, table, workspace, masks, scale, max_new, lse, out),
                        q, offsets, lengths, table, masks, out, self.k, self.v)

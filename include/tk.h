@@ -269,11 +269,11 @@ int tk_last_cache_stats(const tk_workspace* ws, int64_t* hits, int64_t* inserts)
 /*
  * From device ids to a paged key/value cache.  The encode leaves a batch's
  * ids and their offsets on the device; the three calls below take those
- * offsets on, as they are where a request is one segment (of a request of several
- * segments the offset of the first, and the last one's end: a gather on the device): tk_kv_plan places every request's new tokens in the cache's
- * blocks, tk_kv_append stores their keys and values there, tk_kv_attend reads
- * them back for the new tokens, which may be drafted trees.  The pages have
- * no counterpart: these are engineering entry points of this library.
+ * offsets on (as they are where a request is one segment; of requests of several,
+ * gathered on the device at each one's first): tk_kv_plan places every
+ * request's new tokens in the cache's blocks, tk_kv_append stores their keys and
+ * values there, tk_kv_attend reads them back for the new tokens, which may be
+ * drafted trees.  The pages have no counterpart: these are engineering entry points of this library.
  *
  * All buffers, handles and the stream belong to the current device (a handle is refused
  * where another one is current; of plain pointers the caller has to see to it).
@@ -289,8 +289,8 @@ enum { TK_BF16 = 1, TK_F16 = 2 };
  * tk_kv_plan -- block tables and slot maps from request lengths.
  *
  *   d_off[R+1]: request r's new tokens are d_off[r] .. d_off[r+1) (the encode's
- *       d_out_offsets at the requests' first segments); non-decreasing.  Tokens before d_off[0] and past
- *       d_off[R] are padding: position 0, slot -1, request -1, mask 0.
+ *       d_out_offsets at the requests' first segments); non-decreasing.  Tokens
+ *       before d_off[0] and past d_off[R] are padding: position 0, slot -1, request -1, mask 0.
  *   d_ctx[R]: tokens of r already in the cache.  d_table[R][table_stride]: its
  *       blocks in order, the first ceil(ctx/block_size) of them filled in.
  *   d_free[n_free]: ids of free blocks; d_cursor: the first unused entry (one
@@ -399,8 +399,8 @@ void tk_kv_workspace_free(tk_kv_workspace* ws);
  *       (fp32, NULL = not wanted): the natural log of the row's sum of
  *       exponentials.  A row that sees nothing gives 0 and -infinity.
  *       Scores, softmax and sums are fp32; the weights are rounded to the
- *       cache's type for the product with the values (fp16: a weight below about 2^-32 of the
- *       row's largest counts as 0).  Tokens that the mask
+ *       cache's type for the product with the values (fp16: a weight below
+ *       about 2^-32 of the row's largest counts as 0).  Tokens that the mask
  *       hides, and cache places past d_len, have no influence, whatever they hold.
  *
  * R <= 2^20, T <= 2^26, T * n_q_heads < 2^31.  The launch is cooperative (one CTA
@@ -409,16 +409,16 @@ void tk_kv_workspace_free(tk_kv_workspace* ws);
  *
  * Found on the device: a request with more than max_new new tokens, with more
  * than 64 under a mask, with d_len below its new tokens, or past table_width
- * blocks, or with offsets outside [0, T].  Its rows are 0 (lse -infinity), and tk_kv_status tells of it.  A
- * block id outside the cache reads as zeros.  Tokens of no request (before d_off[0], from
- * d_off[R] on) give 0 and -infinity.
+ * blocks, or with offsets outside [0, T].  Its rows are 0 (lse -infinity), and
+ * tk_kv_status tells of it.  A block id outside the cache reads as zeros.  Tokens of no
+ * request (before d_off[0], from d_off[R] on) give 0 and -infinity.
  * A call whose offsets decrease gives them for every token, and so may one of too much
  * work: 2^30 tiles of keys or more, over all key heads and tiles of query rows, three
  * tiles more for each of these (64 keys and 32 or 128 rows a tile; 128 and 256 from
  * 129 rows a key head on; from 2^31 on it always does).
  * tk_kv_status waits for cuda_stream and gives what the workspace's calls
- * since the last tk_kv_status met first (a timeout before others): TK_OK, TK_E_LIMIT (h_request: the
- * request; -1 if nothing was done) or TK_E_TIMEOUT (a wait
+ * since the last tk_kv_status met first (a timeout before others): TK_OK,
+ * TK_E_LIMIT (h_request: the request; -1 if nothing was done) or TK_E_TIMEOUT (a wait
  * on the device gave up, never expected; the outputs are unspecified).
  */
 int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const void* d_q, int64_t q_stride,
