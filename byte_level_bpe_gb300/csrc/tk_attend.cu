@@ -26,8 +26,7 @@
 #include <new>
 #include <type_traits>
 
-#include "tk_blackwell.cuh"
-#include "tk_kv.cuh"
+#include "tk_attend.cuh"
 
 namespace tk {
 
@@ -43,217 +42,8 @@ constexpr int AT_MIN_SHARE = 8;
 // A unit is not cut nearer to its ends than this: with 3, 24 trees of 9 over 1.5k (head_dim 64)
 // take 41.8 instead of 41.3; with 6 (and a least share of 12) 38.6, the others the same.
 constexpr int AT_SNAP = 4;
-static_assert(AT_SNAP >= AT_UNIT_COST && AT_MIN_SHARE >= 2 * AT_SNAP, "a piece has at least one tile");
-
-struct AttendArgs {
-  const void* q;
-  int64_t q_stride;
-  int hq, hk, group;
-  const int64_t* off;
-  int64_t R, T, max_new;
-  const int32_t* len;
-  const int32_t* table;
-  int64_t table_stride, table_width;
-  const int64_t* mask;
-  float scale_log2;
-  void* out;
-  float* lse;
-  KvStatus* status;
-  const void* v;
-  int64_t n_blocks, s_block, s_head, s_token;
-  int log2_bs;
-  float* part;         // partial outputs, see part_at
-  unsigned* counters;  // [2 gridDim.x][2] of a divided unit, by its first stream: pieces that are done, joined
-};
-
-// A request as the schedule sees it.
-struct Request {
-  int t0;  // its first row of q
-  int n, ctx, len;  // n < 0: the offsets decrease
-  bool good;
-};
-
-__device__ __forceinline__ Request load_request(const AttendArgs& a, int64_t r) {
-  Request q;
-  const int64_t o = a.off[r], e = a.off[r + 1], len = a.len[r];
-  // rows that cannot be taken are written as zeros: inside the output whatever the offsets say,
-  // and, as long as these do not decrease, outside the other requests' rows
-  const int64_t t0 = max((int64_t)0, min(o, a.T)), n = max((int64_t)0, min(e, a.T)) - t0;
-  q.good = o >= 0 && e <= a.T && n >= 0 && n <= a.max_new && (!a.mask || n <= KV_TREE_MAX) && len >= n &&
-           len <= a.table_width << a.log2_bs;
-  q.t0 = (int)t0;
-  q.n = (int)n;
-  q.len = q.good ? (int)len : 0;
-  q.ctx = q.good ? (int)(len - n) : 0;
-  return q;
-}
-
-// Keys that the rows [row0, row0 + ROWS) of a request read, and their tiles (at
-// least one: it writes the rows).
-template <int ROWS>
-__device__ __forceinline__ int unit_keys(const AttendArgs& a, const Request& q, int row0) {
-  if (a.mask || !q.good) return q.len;
-  return q.ctx + (min(q.n * a.group, row0 + ROWS) - 1) / a.group + 1;
-}
-// Tiles of a 256-row unit have 128 keys, the others' 64 (see AttendShape).
-template <int ROWS>
-__device__ __forceinline__ int key_tiles(int keys) {
-  constexpr int KEYS = ROWS == 256 ? 128 : 64;
-  return max(1, (keys + KEYS - 1) / KEYS);
-}
-
-// How the work is divided.  It is one line of units (request, row tile, key
-// head), each AT_UNIT_COST + its key tiles long; worker w has it from w * share to
-// (w + 1) * share.  Long caches are so divided over workers and short ones
-// gathered in one; a cut within AT_SNAP of a unit's start or end moves there.
-// Padded: there are fewer units than workers; a unit's length is rounded up to
-// whole shares and divided evenly over its workers, each of which has that one piece.
-// (A line of 2^31 and more is refused; from 2^30 on one may be: a request counts as up to 1,024 more.)
-struct Plan {
-  int share;
-  bool padded;
-};
-
-struct UnitSum {
-  int length, units, longest;
-};
-template <int ROWS>
-__device__ __forceinline__ UnitSum request_work(const AttendArgs& a, const Request& q, const Plan& plan) {
-  UnitSum w = {0, 0, 0};
-  int64_t length = 0;
-  const int rows = q.n * a.group;
-  const bool same = a.mask || !q.good || rows <= ROWS;  // every row tile has the request's keys
-  for (int row0 = 0; row0 < rows; row0 += ROWS) {
-    const int cost = key_tiles<ROWS>(unit_keys<ROWS>(a, q, row0)) + AT_UNIT_COST;
-    const int tiles = same ? (rows + ROWS - 1) / ROWS : 1;
-    length += (int64_t)(plan.padded ? ((unsigned)(cost + plan.share - 1) / (unsigned)plan.share) * plan.share : cost) * tiles;
-    w.units += tiles;
-    w.longest = max(w.longest, cost);
-    if (same) break;
-  }
-  w.length = (int)min(length * a.hk, (int64_t)INT32_MAX);
-  w.units *= a.hk;
-  return w;
-}
-
-struct Piece {
-  int t0, r, h;       // first row of q, request, key head
-  int row0, rows;     // rows of the unit among the request's tokens x group
-  int n, ctx, len;    // of the request; ctx = len = 0 if it cannot be taken
-  int open;           // keys that every row of the unit sees
-  int keys, lo, hi;   // keys of the unit; tiles of this piece
-  int first, pieces;  // the worker with the unit's tile 0; workers it is divided over
-  int valid;          // 0 = no more, 1 = a request that cannot be taken
-};
 constexpr int AT_PIECES = 4;  // handed over ahead
 
-template <int ROWS>
-struct Walk {
-  Plan plan;
-  int from, to;  // the worker's part of the line
-  int u, r;      // where the next unit starts, and its request
-  Request q;
-  int row0, h;                         // the unit's row tile and head
-  int keys, cost, pieces, size, length;  // of the row tile's units; padded: what they are divided into
-  bool loaded;
-
-  __device__ __forceinline__ void row_tile(const AttendArgs& a) {
-    keys = unit_keys<ROWS>(a, q, row0);
-    cost = length = key_tiles<ROWS>(keys) + AT_UNIT_COST;
-    if (plan.padded) {
-      pieces = (unsigned)(cost + plan.share - 1) / (unsigned)plan.share;
-      size = (unsigned)(cost + pieces - 1) / (unsigned)pieces;
-      length = pieces * plan.share;
-    }
-  }
-  __device__ __forceinline__ bool next(const AttendArgs& a, Piece& x) {
-    for (;;) {
-      if (u >= to || r >= a.R) break;
-      if (!loaded) {
-        q = load_request(a, r);
-        if (q.n <= 0) {
-          r++;
-          continue;
-        }
-        row0 = h = 0;
-        loaded = true;
-        row_tile(a);
-      }
-      if (u + length <= from) {  // heads before this worker
-        const int skip = min(a.hk - h, (int)((unsigned)(from - u) / (unsigned)length));
-        u += skip * length;
-        h += skip;
-      }
-      if (h == a.hk) {
-        h = 0;
-        row0 += ROWS;
-        loaded = row0 < q.n * a.group;
-        if (loaded) row_tile(a);
-        else r++;
-        continue;
-      }
-      const int lo = cut(from - u), hi = cut(to - u), at = u;
-      u += length;
-      h++;
-      if (hi <= lo) continue;
-      x.t0 = q.t0;
-      x.r = r;
-      x.h = h - 1;
-      x.row0 = row0;
-      x.rows = min(ROWS, q.n * a.group - row0);
-      x.n = q.n;
-      x.ctx = q.ctx;
-      x.len = q.len;
-      x.open = !q.good ? 0 : a.mask ? q.ctx : q.ctx + row0 / a.group + 1;
-      x.keys = keys;
-      x.lo = max(0, lo - AT_UNIT_COST);
-      x.hi = hi - AT_UNIT_COST;
-      x.first = 0;
-      x.pieces = 1;
-      if (lo > 0 || hi < cost) {
-        x.first = (unsigned)(at + (plan.padded ? 0 : AT_SNAP)) / (unsigned)plan.share;
-        x.pieces = plan.padded ? pieces : (int)((unsigned)(at + cost - AT_SNAP - 1) / (unsigned)plan.share) - x.first + 1;
-      }
-      x.valid = 1 + q.good;
-      return true;
-    }
-    x.valid = 0;
-    return false;
-  }
-  // a worker's end `in` after the unit's start, as a cut of the unit
-  __device__ __forceinline__ int cut(int in) const {
-    if (in <= 0) return 0;
-    if (in >= length) return cost;
-    if (plan.padded) return min(cost, (int)((unsigned)in / (unsigned)plan.share) * size);
-    return in <= AT_SNAP ? 0 : in >= cost - AT_SNAP ? cost : in;
-  }
-};
-
-// The keys of a row among 32 from `first` on, as bits.
-struct Seen {
-  int ctx, last;     // chain: keys up to `last`
-  uint64_t mask;     // tree: drafted tokens
-  bool tree;
-  __device__ __forceinline__ uint32_t bits(int first) const {
-    if (!tree) {
-      const int n = last + 1 - first;
-      return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1;
-    }
-    const int sh = first - ctx;
-    if (sh <= -32) return 0xffffffffu;
-    if (sh >= 64) return 0u;
-    return sh >= 0 ? (uint32_t)(mask >> sh) : ((uint32_t)mask << -sh) | ((1u << -sh) - 1);
-  }
-  __device__ __forceinline__ bool has(int j) const {
-    return tree ? j < ctx || (j - ctx < 64 && ((mask >> (j - ctx)) & 1)) : j <= last;
-  }
-};
-
-template <class T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const typename Pair<T>::type p = Pair<T>::down(a, b);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
 // 16-bit halves with all exponent bits set (infinities and NaN): 0x8000 each.
 template <class T>
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w);
@@ -281,6 +71,12 @@ struct AttendShape {
   static constexpr int RINGS = MODE == 2 ? 1 : 2, ROWS = MODE == 0 ? 32 : MODE == 1 ? 128 : 256;
   static constexpr int Q_ROWS = MODE == 0 ? 32 : 128;  // of a stream
   static constexpr int KEYS = MODE == 2 ? 128 : 64, BUFS = 128 / KEYS;  // keys of a tile; tiles' scores in tensor memory
+  // Up to 128 rows memory is the bound, which fewer workers reach too, so a worker with a single piece may have a
+  // quarter more: 32 trees of 16 over 8k, 256 units for 304 workers, take 159 us padded (128 tiles each) and 189 us
+  // divided evenly (108), 30 trees of 8 over 3k 62 and 77, one token of 32 requests over 8k of head_dim 64 109 and
+  // 106.  The 8 tiles are for more rows: two trees of 64 over 30k take 67 us padded and 82 us not.
+  template <bool WIN>
+  using Tiles = Tiling<ROWS, KEYS, 1, WIN, AT_UNIT_COST, AT_MIN_SHARE, AT_SNAP, 8, MODE != 2>;
   static constexpr int Q = Q_ROWS * D * 2, STAGE = KEYS * D * 2;
   static constexpr int STAGES = (RINGS == 1 ? 160 : MODE == 0 ? 96 : 80) * 1024 / STAGE;  // of a ring
   static constexpr int RING = 2 * Q;
@@ -311,21 +107,16 @@ __device__ __forceinline__ float* part_at(float* part, int stream, int slot) {
 // (128), 256 columns from 256 * stream.
 // LSE: the log of the sum is wanted too, and summed before the rounding (64 drafted tokens over
 // 131k, replayed: 204 us without it, 221 with it; up to 128 rows the softmax is not the bound, and it is always there).
-// Rows of no request are zeros, so that padding carries nothing on.  Rarely run: in line it cost
-// 64 drafted tokens over 131k 1% (204 instead of 202 us).
-template <int D>
-__device__ __noinline__ void zero_rows(void* out, float* lse, int hq, int64_t from, int64_t to) {
-  const int64_t me = (int64_t)blockIdx.x * AT_THREADS + threadIdx.x, all = (int64_t)gridDim.x * AT_THREADS;
-  for (int64_t i = from * hq * (D / 8) + me; i < to * hq * (D / 8); i += all) static_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
-  if (lse)
-    for (int64_t i = from * hq + me; i < to * hq; i += all) lse[i] = -INFINITY;
-}
-
-template <class T, int D, int MODE, bool LSE>
+//
+// WIN: the call has a window.  A unit then reads the tiles of the first places and those from its first
+// token's window on; a tile that only some of its rows see all of is masked, its values made finite,
+// like one at the unit's end.
+template <class T, int D, int MODE, bool LSE, bool WIN>
 __global__ void __launch_bounds__(AT_THREADS, 1)
 k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   using L = AttendShape<D, MODE>;
-  constexpr int ROWS = L::ROWS, KEYS = L::KEYS, BUFS = L::BUFS, HALVES = D / 64, NST = L::STAGES;
+  constexpr int KEYS = L::KEYS, BUFS = L::BUFS, HALVES = D / 64, NST = L::STAGES;
+  using S = typename L::template Tiles<WIN>;
   constexpr bool BF = Pair<T>::BF;
   // fp16 weights have their range below 2^15: with m's weight at 2^7 those 2^8 above it (before O is
   // rescaled) still fit, and one is lost at 2^-32 of m's instead of 2^-25: a million keys that
@@ -344,10 +135,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
   Piece* s_piece = reinterpret_cast<Piece*>(smem + L::PIECES) + ring * AT_PIECES;
   int* s_walk = reinterpret_cast<int*>(smem + L::SMALL);  // of each worker: first request, where it starts
   int* s_sum = s_walk + 4;
-  int* s_units = s_sum + AT_THREADS / 32;
-  int* s_longest = s_units + AT_THREADS / 32;
-  int* s_coarse = s_longest + AT_THREADS / 32;
-  volatile int* s_int = reinterpret_cast<volatile int*>(s_coarse + AT_THREADS / 32);
+  volatile int* s_int = reinterpret_cast<volatile int*>(s_sum + 4 * AT_THREADS / 32);
   volatile int* abort = s_int + 1;
   volatile int* s_bad = s_int + 2 + 8 * ring;  // by piece
 
@@ -382,112 +170,9 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     const int64_t at = ((int64_t)blockIdx.x * AT_THREADS + tid) * 32;
     if (at < (a.R - 1) * a.table_stride + a.table_width) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.table + at));
   }
-  // the plan, and where the workers start on its line: the requests' lengths added up, each
-  // thread a run of them
   constexpr int WORKERS = MODE == 2 ? 1 : 2;  // of a CTA
-  Plan plan = {1, false};
-  int total;
-  {
-    const int R = (int)a.R, per = (R + AT_THREADS - 1) / AT_THREADS;
-    const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
-    int mine = 0, units = 0, longest = 0, before, coarse = 0;
-    const int64_t head = R ? a.off[0] : 0, tail = R ? a.off[R] : 0;
-    for (int r = r0; r < r1; r++) {
-      const Request q = load_request(a, r);
-      if (q.n < 0) {  // requests over each other: any amount of work, and of rows with two answers
-        coarse = 1 << 21;
-        break;
-      }
-      if (!q.good && blockIdx.x == 0 && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = r;
-      const UnitSum w = request_work<ROWS>(a, q, plan);
-      mine += w.length;
-      units += w.units;
-      longest = max(longest, w.longest);
-      coarse = min(coarse + (w.length >> 10) + 1, 1 << 21);
-    }
-    // the sum over the threads before this one, and over all
-    auto scan = [&](int x, int& all) {
-      int incl = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (lane == 31) s_sum[warp] = incl;
-      __syncthreads();
-      int b = incl - x;
-      all = 0;
-#pragma unroll
-      for (int w = 0; w < AT_THREADS / 32; w++) {
-        const int y = s_sum[w];
-        if (w < warp) b += y;
-        all += y;
-      }
-      return b;
-    };
-    units = __reduce_add_sync(0xffffffffu, units);
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    coarse = __reduce_add_sync(0xffffffffu, coarse);
-    if (lane == 0) {
-      s_units[warp] = units;
-      s_longest[warp] = longest;
-      s_coarse[warp] = coarse;
-    }
-    before = scan(mine, total);
-    units = coarse = 0;
-#pragma unroll
-    for (int w = 0; w < AT_THREADS / 32; w++) {
-      units += s_units[w];
-      longest = max(longest, s_longest[w]);
-      coarse += s_coarse[w];
-    }
-    // more than the line's 32 bits hold, or offsets that decrease: nothing is done then
-    const bool much = coarse >= 1 << 21;
-    if (much) {
-      if (blockIdx.x == 0 && tid == 0 && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = -1;
-      total = mine = units = 0;
-    }
-    // rows of no request are zeros, so that padding carries nothing on; after the last and before the first
-    if (much) {
-      zero_rows<D>(a.out, a.lse, a.hq, 0, a.T);
-    } else if (head > 0 || tail < a.T) {
-      zero_rows<D>(a.out, a.lse, a.hq, 0, min(head, a.T));
-      zero_rows<D>(a.out, a.lse, a.hq, max(tail, (int64_t)0), a.T);
-    }
-    const int workers = gridDim.x * WORKERS;
-    auto over = [](int x, int y) { return (int)((unsigned)(x + y - 1) / (unsigned)y); };
-    plan.share = max(AT_MIN_SHARE, over(total, workers));
-    // (a padded line is at most a quarter longer and 8 * workers: it fits 31 bits with what it is below here)
-    if (units > 0 && units < workers && total <= 1 << 30) {
-      // shares that give the units no more workers than there are
-      const int share = max(AT_MIN_SHARE, min(over(longest, workers / units), over(total, workers - units)));
-      // What a worker may do more if it has a single piece for that.  Up to 128 rows memory is the
-      // bound, which fewer workers reach too, so that may be a quarter: 32 trees of 16 over 8k, 256
-      // units for 304 workers, take 159 us padded (128 tiles each) and 189 us divided evenly (108),
-      // 30 trees of 8 over 3k 62 and 77, one token of 32 requests over 8k of head_dim 64 109 and 106.  The 8 tiles
-      // are for more rows: two trees of 64 over 30k take 67 us padded and 82 us not.
-      if (share <= plan.share + 8 + (MODE == 2 ? 0 : plan.share / 4)) {
-        plan.share = share;
-        plan.padded = true;
-        mine = 0;
-        for (int r = r0; r < r1; r++) mine += request_work<ROWS>(a, load_request(a, r), plan).length;
-        __syncthreads();  // s_sum has been read
-        before = scan(mine, total);
-      }
-    }
-    for (int w = 0; w < WORKERS; w++) {
-      const int x = (blockIdx.x * WORKERS + w) * plan.share;
-      if (x < before || x >= before + mine) continue;
-      int r = r0, at = before;
-      for (; r < r1 - 1; r++) {
-        const int c = request_work<ROWS>(a, load_request(a, r), plan).length;
-        if (x < at + c) break;
-        at += c;
-      }
-      s_walk[2 * w] = r;
-      s_walk[2 * w + 1] = at;
-    }
-  }
+  Plan plan;
+  const int total = make_plan<S, AT_THREADS, WORKERS, D>(a, plan, s_sum, s_walk);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -511,7 +196,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     if (MODE == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 0 || (warp == 3 && MODE != 2)) {
       // ---- loads, in the order of their use: K0 K1 V0 K2 V1 K3 ... with two tiles' scores, K0 V0 K1 V1 ... with one
-      Walk<ROWS> walk;
+      Walk<S> walk;
       walk.plan = plan;
       walk.from = (blockIdx.x * WORKERS + ring) * plan.share;
       walk.to = min(total, walk.from + plan.share);
@@ -539,14 +224,20 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       struct Ids {
         int window, now, then;
       };
-      int boxes = 0, h = 0;
+      int boxes = 0, h = 0, head = 0, skip = 0;
       const int32_t* row = nullptr;
+      auto at_key = [&](int tile) { return WIN && tile >= head ? tile + skip : tile; };  // in tiles from key 0 on
       auto id_of = [&](int b) { return b < boxes ? __ldg(row + (b >> per_page)) : 0; };
       auto load = [&](const CUtensorMap* map, Ids& ids, int tile) {
-        const int box0 = tile * ppt;
+        const int box0 = at_key(tile) * ppt;
         if (box0 >= ids.window + 32) {
-          ids.window += 32;
-          ids.now = ids.then;
+          if (WIN && box0 >= ids.window + 64) {
+            ids.window = box0 & ~31;
+            ids.now = id_of(ids.window + lane);
+          } else {
+            ids.window += 32;
+            ids.now = ids.then;
+          }
           ids.then = id_of(ids.window + 32 + lane);
         }
         const int nb = max(0, min(ppt, boxes - box0));
@@ -569,10 +260,14 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       while (ok && nx.valid) {
         const int lo = nx.lo, hi = nx.hi;
         h = nx.h;
+        if (WIN) {
+          head = nx.head;
+          skip = nx.skip;
+        }
         boxes = (nx.keys + (1 << log2_box) - 1) >> log2_box;
         row = a.table + (int64_t)nx.r * a.table_stride;
         Ids k, v;
-        k.window = (lo * ppt) & ~31;
+        k.window = (at_key(lo) * ppt) & ~31;
         k.now = id_of(k.window + lane);
         k.then = id_of(k.window + 32 + lane);
         v = k;
@@ -734,24 +429,23 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       }
       const bool live = row < rows, active = wq * 32 < rows;  // the row's, the warp's
       const int gr = p.row0 + skip + row, tok = live ? gr / a.group : 0;
-      Seen seen;
-      seen.tree = a.mask != nullptr;
-      seen.ctx = p.ctx;
-      seen.last = p.valid == 2 ? p.ctx + tok : -1;
-      seen.mask = 0;
-      if (seen.tree && live && p.valid == 2) {
-        seen.mask = (uint64_t)a.mask[p.t0 + tok];
-        if (p.n < 64) seen.mask &= (1ull << p.n) - 1;
-      }
+      Seen<WIN> seen;
+      seen.set(a, p, live, tok);
       float m = -INFINITY, mc = 0.f, l = 0.f, l_full = 0.f;  // mc = m c - UP, or 0 while the row has seen nothing
       const int lo = p.lo;
       const uint64_t c2 = pair64(c, c);
 
+      const int head = p.head, jump = WIN ? p.skip : 0, shut = p.shut;
+      auto at_key = [&](int tile) { return (WIN && tile >= head ? tile + jump : tile) * KEYS; };
+      // a tile, a key
+      auto seen_by_all = [&](int k0) { return k0 + KEYS <= open && (!WIN || k0 >= shut || k0 + KEYS <= a.sinks); };
+      auto seen_by_some = [&](int key) { return key >= open || (WIN && key < shut && key >= a.sinks); };
+
       // One tile.  Nearly all are seen by every row; where the softmax is the bound (MODE 2) those have a
       // body of their own.
       auto tile = [&](int t, auto some_hidden) {
-        const int k0 = (lo + t) * KEYS;
-        const bool hidden = decltype(some_hidden)::value && (MODE == 2 || k0 + KEYS > open);
+        const int k0 = at_key(lo + t);
+        const bool hidden = decltype(some_hidden)::value && (MODE == 2 || !seen_by_all(k0));
         if (hidden) {
           // Values of keys past the request's end become 0; so do infinities and NaN of
           // keys that only some rows see: 0 * inf in a product would reach the others.
@@ -761,7 +455,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
             wait(b_full + 8 * (at % NST), (at / NST) & 1);
             constexpr int PARTS = 128 / KEYS;  // threads of a row
             const int kr = row % KEYS, part = row / KEYS, key = k0 + kr;
-            if (key >= open) {
+            if (seen_by_some(key)) {
               uint8_t* v = smem + (s_ring - base) + (at % NST) * L::STAGE + kr * 128;
               bool bad = false;
 #pragma unroll 4
@@ -867,13 +561,16 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         nt++;
       };
       int clear = 0;
-      if constexpr (MODE == 2) {
+      if constexpr (MODE == 2 && !WIN) {
         clear = max(0, min(n, open / KEYS - lo));
 #pragma unroll 1
         for (int t = 0; t < clear; t++) tile(t, std::false_type());
       }
 #pragma unroll 1
-      for (int t = clear; t < n; t++) tile(t, std::true_type());
+      for (int t = clear; t < n; t++) {
+        if (MODE == 2 && WIN && seen_by_all(at_key(lo + t))) tile(t, std::false_type());
+        else tile(t, std::true_type());
+      }
       // the queries have been read for the last time: the next ones come in under the last products
       more = coming(taken + 1);
       if (more && has_rows(taken + 1)) {
@@ -929,8 +626,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       if (row == 0 && (MODE != 2 || stream == 0)) s_bad[(taken + 2) & 7] = 0;
       if (bad && live) {
         // the values taken out above, for the rows that see them: any weight makes them infinite or NaN
-        const int to = min(p.len, p.hi * KEYS);
-        for (int j = max(open, p.lo * KEYS); j < to; j++) {
+        const int to = WIN ? n * KEYS : min(p.len, p.hi * KEYS);
+        for (int i = WIN ? 0 : max(open, p.lo * KEYS); i < to; i++) {
+          const int j = WIN ? at_key(lo + i / KEYS) + i % KEYS : i;
+          if (WIN && (!seen_by_some(j) || j >= p.len)) continue;
           const int64_t id = a.table[(int64_t)p.r * a.table_stride + (j >> a.log2_bs)];
           if (!seen.has(j) || id < 0 || id >= a.n_blocks) continue;
           const T* v = static_cast<const T*>(a.v) + id * a.s_block + p.h * a.s_head + (j & ((1 << a.log2_bs) - 1)) * a.s_token;
@@ -1067,12 +766,12 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
   }
 }
 
-template <class T, int D, int MODE, bool LSE>
+template <class T, int D, int MODE, bool LSE, bool WIN>
 static cudaError_t attend_launch(const AttendArgs& a, const tk_kv_cache* cache, int grid, cudaStream_t st) {
   constexpr int bytes = AttendShape<D, MODE>::TOTAL;
   static bool set[64];  // by device
   if (cache->device >= 64 || !set[cache->device]) {
-    const cudaError_t e = cudaFuncSetAttribute(k_kv_attend<T, D, MODE, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = cudaFuncSetAttribute(k_kv_attend<T, D, MODE, LSE, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     if (cache->device < 64) set[cache->device] = true;
   }
@@ -1086,14 +785,19 @@ static cudaError_t attend_launch(const AttendArgs& a, const tk_kv_cache* cache, 
   cfg.stream = st;
   cfg.attrs = &coop;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_kv_attend<T, D, MODE, LSE>, a, cache->map_k, cache->map_v);
+  return cudaLaunchKernelEx(&cfg, k_kv_attend<T, D, MODE, LSE, WIN>, a, cache->map_k, cache->map_v);
+}
+
+template <class T, int D, bool WIN>
+static cudaError_t attend_pick(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, int grid, cudaStream_t st) {
+  if (rows <= 32) return attend_launch<T, D, 0, true, WIN>(a, cache, grid, st);
+  if (rows <= 128) return attend_launch<T, D, 1, true, WIN>(a, cache, grid, st);
+  return a.lse ? attend_launch<T, D, 2, true, WIN>(a, cache, grid, st) : attend_launch<T, D, 2, false, WIN>(a, cache, grid, st);
 }
 
 template <class T, int D>
 static cudaError_t attend_pick(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, int grid, cudaStream_t st) {
-  if (rows <= 32) return attend_launch<T, D, 0, true>(a, cache, grid, st);
-  if (rows <= 128) return attend_launch<T, D, 1, true>(a, cache, grid, st);
-  return a.lse ? attend_launch<T, D, 2, true>(a, cache, grid, st) : attend_launch<T, D, 2, false>(a, cache, grid, st);
+  return a.window < INT32_MAX ? attend_pick<T, D, true>(a, cache, rows, grid, st) : attend_pick<T, D, false>(a, cache, rows, grid, st);
 }
 
 }  // namespace tk
@@ -1170,12 +874,12 @@ extern "C" int tk_kv_status(tk_kv_workspace* ws, int64_t* h_request, void* cuda_
   return s.code;
 }
 
-extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const void* d_q, int64_t q_stride,
-                            int n_q_heads, const int64_t* d_off, int64_t R, int64_t T, int64_t max_new,
-                            const int32_t* d_len, const int32_t* d_table, int64_t table_stride, int64_t table_width,
-                            const int64_t* d_mask, float scale, void* d_out, float* d_lse, void* cuda_stream) {
+// window: INT32_MAX for none
+static int kv_attend(const char* where, const tk_kv_cache* cache, tk_kv_workspace* ws, const void* d_q, int64_t q_stride,
+                     int n_q_heads, const int64_t* d_off, int64_t R, int64_t T, int64_t max_new, const int32_t* d_len,
+                     const int32_t* d_table, int64_t table_stride, int64_t table_width, const int64_t* d_mask, int window,
+                     int sinks, float scale, void* d_out, float* d_lse, void* cuda_stream) {
   using namespace tk;
-  const char* where = "tk_kv_attend";
   if (!cache || !ws) return attend_arg(where, "null cache or workspace");
   if (ws->device != cache->device) return attend_arg(where, "cache and workspace are on different devices");
   if (cache->head_dim != 64 && cache->head_dim != 128) return attend_arg(where, "head_dim is neither 64 nor 128");
@@ -1196,11 +900,13 @@ extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const
   AttendArgs a = {d_q, q_stride, n_q_heads, cache->n_heads, group, d_off, R, T, max_new, d_len, d_table, table_stride,
                   table_width, d_mask, scale * 1.4426950408889634f, d_out, d_lse, ws->status,
                   cache->v, cache->n_blocks, cache->stride[0], cache->stride[1],
-                  cache->stride[2], cache->log2_block, ws->part, ws->counters};
+                  cache->stride[2], cache->log2_block, ws->part, ws->counters, window, sinks, cache->k_scale, cache->v_scale};
   cudaStream_t st = (cudaStream_t)cuda_stream;
   const int64_t rows = std::min(max_new, T) * group;  // of a request and key head
   cudaError_t e;
-  if (cache->type == TK_BF16)
+  if (cache->k_scale)
+    e = attend8(a, cache, rows, st);
+  else if (cache->type == TK_BF16)
     e = cache->head_dim == 64 ? attend_pick<__nv_bfloat16, 64>(a, cache, rows, ws->sms, st)
                               : attend_pick<__nv_bfloat16, 128>(a, cache, rows, ws->sms, st);
   else
@@ -1211,4 +917,27 @@ extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const
     return TK_E_CUDA;
   }
   return TK_OK;
+}
+
+extern "C" int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const void* d_q, int64_t q_stride,
+                            int n_q_heads, const int64_t* d_off, int64_t R, int64_t T, int64_t max_new,
+                            const int32_t* d_len, const int32_t* d_table, int64_t table_stride, int64_t table_width,
+                            const int64_t* d_mask, float scale, void* d_out, float* d_lse, void* cuda_stream) {
+  return kv_attend("tk_kv_attend", cache, ws, d_q, q_stride, n_q_heads, d_off, R, T, max_new, d_len, d_table, table_stride,
+                   table_width, d_mask, INT32_MAX, 0, scale, d_out, d_lse, cuda_stream);
+}
+
+extern "C" int tk_kv_attend_window(const tk_kv_cache* cache, tk_kv_workspace* ws, const void* d_q, int64_t q_stride,
+                                   int n_q_heads, const int64_t* d_off, int64_t R, int64_t T, int64_t max_new,
+                                   const int32_t* d_len, const int32_t* d_table, int64_t table_stride, int64_t table_width,
+                                   const int64_t* d_mask, int64_t window, int64_t sinks, float scale, void* d_out,
+                                   float* d_lse, void* cuda_stream) {
+  using namespace tk;
+  const char* where = "tk_kv_attend_window";
+  if (window < 1 || sinks < 0) return attend_arg(where, "window is below 1 or sinks below 0");
+  if (d_mask && window < KV_TREE_MAX) return attend_arg(where, "a window under masks is below 64, the most tokens of a tree");
+  // a request has less than 2^31 places
+  const int w = (int)std::min<int64_t>(window, INT32_MAX), s = (int)std::min<int64_t>(sinks, INT32_MAX - 128);
+  return kv_attend(where, cache, ws, d_q, q_stride, n_q_heads, d_off, R, T, max_new, d_len, d_table, table_stride, table_width,
+                   d_mask, w, s, scale, d_out, d_lse, cuda_stream);
 }

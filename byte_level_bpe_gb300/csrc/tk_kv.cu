@@ -3,6 +3,8 @@
 #include <algorithm>
 #include <new>
 
+#include <cuda_fp8.h>
+
 #include "tk_blackwell.cuh"
 #include "tk_kv.cuh"
 
@@ -330,13 +332,12 @@ struct AppendArgs {
 // the passes of a warp arrive ahead in shared memory, each lane's elements in its own place
 // (in registers, two passes ahead, 32,768 rows of 48 heads took 163 us instead of 140).
 template <class T, int LANES, bool NEIGHBOURS>
-__global__ void __launch_bounds__(APPEND_THREADS, 5) k_kv_append(AppendArgs a) {
+__device__ __forceinline__ void append_rows(const AppendArgs& a, uint4 (*s_x)[APPEND_FLIGHT][2][32], int64_t cta) {
   using P = Pair<T>;
   using T2 = typename P::type;
   constexpr int HEADS = 32 / LANES;
-  __shared__ uint4 s_x[APPEND_THREADS / 32][APPEND_FLIGHT][2][32];
   const int lane = threadIdx.x & 31, l = lane % LANES, g = lane / LANES;
-  const int64_t w = ((int64_t)blockIdx.x * APPEND_THREADS + threadIdx.x) >> 5;
+  const int64_t w = (cta * APPEND_THREADS + threadIdx.x) >> 5;
   const int64_t t = w / a.chunks;
   if (t >= a.T) return;
   // the lane's two runs of 8 elements: pairs are (e0 + i, e1 + i), or neighbours in each
@@ -480,8 +481,236 @@ __global__ void __launch_bounds__(APPEND_THREADS, 5) k_kv_append(AppendArgs a) {
   }
 }
 
+template <class T, int LANES, bool NEIGHBOURS>
+__global__ void __launch_bounds__(APPEND_THREADS, 5) k_kv_append(AppendArgs a) {
+  __shared__ uint4 s_x[APPEND_THREADS / 32][APPEND_FLIGHT][2][32];
+  append_rows<T, LANES, NEIGHBOURS>(a, s_x, blockIdx.x);
+}
+
+// Into 8-bit blocks: a value stands for e4m3 * scale of its block and head, for keys and values apart.
+//   need = the least 2^e with max |y| <= 448 2^e over the call's rows of the block
+//   scale' = need if the call stores the block's first place, else max(need, scale)
+//   stored = rn(y / scale'), older rows of a block whose scale grows: rn(e4m3 * scale / scale')
+// A power of two costs e4m3, which floats itself, no precision, and an older value that is scaled
+// down stays what it was unless it gets under e4m3's least normal one.
+// The rows of a block follow one another (tk_kv_plan's do): they are one run, and a run is one
+// CTA's for each head, keys and values, so that nothing is added up over CTAs and the
+// result does not go by their order. A CTA takes the runs that begin among `chunk` tokens. The rows are
+// read once more for the second pass unless one pass has them all (16 rows of up to 128
+// elements); they are then in L1 or L2, and a third of the heads at 4 query heads a key head.
+struct Store8Args {
+  AppendArgs a;  // its hk is 0: its heads are the queries
+  int hk;
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int chunk;       // tokens of a CTA
+  int store_ctas;  // the CTAs after these have the queries
+};
+constexpr int STORE8_CHUNK = 64;  // most tokens of a CTA: its run starts are two words
+constexpr float STORE8_LEAST = 7.888609052210118e-31f;  // 2^-100, the scale of zeros
+
+// 8 elements -> e4m3, infinities as NaN (e4m3 has none)
+__device__ __forceinline__ uint2 to_e4m3(const float* y, float scale, float inv, bool pow2) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    float u = pow2 ? y[2 * i] * inv : __fdiv_rn(y[2 * i], scale), v = pow2 ? y[2 * i + 1] * inv : __fdiv_rn(y[2 * i + 1], scale);
+    if (!(fabsf(u) < INFINITY)) u = __int_as_float(0x7fffffff);
+    if (!(fabsf(v) < INFINITY)) v = __int_as_float(0x7fffffff);
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(u, v), __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+__device__ __forceinline__ uint32_t rescale_e4m3(uint32_t w, float ratio) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const __half2 h(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3));
+    const float2 f = __half22float2(h);
+    out |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f.x * ratio, f.y * ratio), __NV_SATFINITE, __NV_E4M3) << (16 * i);
+  }
+  return out;
+}
+
+template <class T, int LANES, bool NEIGHBOURS>
+__device__ __forceinline__ void store8_runs(const Store8Args& s) {
+  using P = Pair<T>;
+  using T2 = typename P::type;
+  constexpr int G = 32 / LANES, WARPS = APPEND_THREADS / 32, STEP = G * WARPS;  // rows of a pass
+  __shared__ uint32_t s_starts[STORE8_CHUNK / 32], s_placed[4], s_top;
+  __shared__ int s_rows;
+  const AppendArgs& a = s.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % LANES, g = lane / LANES;
+  const int part = blockIdx.x % (2 * s.hk), h = part % s.hk;
+  const bool key = part < s.hk;
+  uint8_t* pool = (key ? s.k : s.v) + h * a.s_head;
+  float* scales = (key ? s.k_scale : s.v_scale) + h;
+  const int within = (1 << a.log2_bs) - 1;
+  const int64_t t_first = (int64_t)(blockIdx.x / (2 * s.hk)) * s.chunk;
+  auto block_of = [&](int64_t t) {  // -1: none
+    if (t < 0 || t >= a.T) return (int64_t)-1;
+    const int64_t x = a.slot[t];
+    return x >= 0 && x < a.n_slots ? x >> a.log2_bs : (int64_t)-1;
+  };
+  if (tid < STORE8_CHUNK) {
+    const int64_t t = t_first + tid, b = tid < s.chunk ? block_of(t) : -1;
+    const uint32_t starts = __ballot_sync(0xffffffffu, b >= 0 && block_of(t - 1) != b);
+    if (lane == 0) s_starts[warp] = starts;
+  }
+
+  // the lane's elements, as append_rows has them
+  const bool turns = key && a.rot > 0, normed = key && a.k_gain;
+  const int half = a.rot >> 1;
+  const bool rotated = key && l * 16 < a.rot, in_dim = l * 16 < a.dim;
+  const bool apart = !NEIGHBOURS && rotated;
+  const int e0 = apart ? l * 8 : l * 16, e1 = apart ? e0 + half : e0 + 8;
+  const T* src = static_cast<const T*>(a.qkv) + (int64_t)(a.hq + part) * a.dim;
+  float g0[8], g1[8];
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    g0[j] = normed && in_dim ? __ldg(a.k_gain + e0 + j) : 1.f;
+    g1[j] = normed && in_dim ? __ldg(a.k_gain + e1 + j) : 1.f;
+  }
+  // normed and rotated elements of token t, of which there is one if `in`
+  auto row = [&](int64_t t, bool in, float* y0, float* y1) {
+    union Vec {
+      uint4 u;
+      T2 p[4];
+    } x0, x1;
+    x0.u = x1.u = make_uint4(0, 0, 0, 0);
+    if (in && in_dim) {
+      x0.u = __ldg(reinterpret_cast<const uint4*>(src + t * a.row_stride + e0));
+      x1.u = __ldg(reinterpret_cast<const uint4*>(src + t * a.row_stride + e1));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const float2 u = P::up(x0.p[j]), v = P::up(x1.p[j]);
+      y0[2 * j] = u.x; y0[2 * j + 1] = u.y;
+      y1[2 * j] = v.x; y1[2 * j + 1] = v.y;
+    }
+    if (normed) {
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; j++) ss = fmaf(y0[j], y0[j], fmaf(y1[j], y1[j], ss));
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float inv = rsqrtf(ss / (float)a.dim + a.eps);
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        y0[j] *= inv * g0[j];
+        y1[j] *= inv * g1[j];
+      }
+    }
+    if (turns && rotated && in) {
+      const int64_t p = a.pos[t];
+      const bool known = p >= 0 && p < a.rope_len;
+      const float4* rope = reinterpret_cast<const float4*>(a.rope + ((known ? p : 0) * half + l * 8) * 2);
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        float4 f = __ldg(rope + j);
+        if (!known) f.x = f.y = f.z = f.w = __int_as_float(0x7fffffff);
+        auto turn = [](float& u, float& v, float c, float sn) {
+          const float x = u;
+          u = u * c - v * sn;
+          v = v * c + x * sn;
+        };
+        if (NEIGHBOURS) {
+          float* y = j < 2 ? y0 : y1;
+          turn(y[4 * (j & 1)], y[4 * (j & 1) + 1], f.x, f.y);
+          turn(y[4 * (j & 1) + 2], y[4 * (j & 1) + 3], f.z, f.w);
+        } else {
+          turn(y0[2 * j], y1[2 * j], f.x, f.y);
+          turn(y0[2 * j + 1], y1[2 * j + 1], f.z, f.w);
+        }
+      }
+    }
+  };
+  auto top_of = [&](const float* y0, const float* y1) {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const float u = fabsf(y0[j]), v = fabsf(y1[j]);
+      if (u < INFINITY) m = fmaxf(m, u);
+      if (v < INFINITY) m = fmaxf(m, v);
+    }
+    return m;
+  };
+
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < s.chunk; i++) {
+    if (!((s_starts[i >> 5] >> (i & 31)) & 1)) continue;
+    const int64_t t0 = t_first + i, b = a.slot[t0] >> a.log2_bs;
+    const float old = scales[b * s.hk];
+    __syncthreads();  // the last run's shared words have been read
+    if (tid < 4) s_placed[tid] = 0;
+    if (tid == 0) {
+      s_top = 0;
+      s_rows = INT32_MAX;
+    }
+    __syncthreads();
+    // the run's rows and places
+    for (int64_t n = 0;; n += APPEND_THREADS) {
+      const bool in = block_of(t0 + n + tid) == b;
+      const uint32_t out = __ballot_sync(0xffffffffu, !in);
+      if (out && lane == 0) atomicMin(&s_rows, (int)min(n + warp * 32 + __ffs(out) - 1, (int64_t)INT32_MAX - 1));
+      if (__syncthreads_or(out != 0)) break;
+    }
+    const int rows = s_rows;
+    for (int r = tid; r < rows; r += APPEND_THREADS) {
+      const int place = (int)(a.slot[t0 + r] & within);
+      atomicOr(&s_placed[place >> 5], 1u << (place & 31));
+    }
+    float y0[8], y1[8], m = 0.f;
+    for (int r = warp * G; r < rows; r += STEP) {
+      row(t0 + r + g, r + g < rows, y0, y1);
+      m = fmaxf(m, top_of(y0, y1));
+    }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    if (lane == 0 && top) atomicMax(&s_top, top);
+    __syncthreads();
+    const bool begun = s_placed[0] & 1;
+    // 448 = 1.75 2^8
+    const int e = (int)(s_top >> 23) - 8 + ((s_top & 0x7fffff) > 0x600000);
+    const float need = e < 27 ? STORE8_LEAST : __uint_as_float((uint32_t)e << 23);
+    const float scale = begun ? need : fmaxf(need, old);
+    const bool pow2 = (__float_as_uint(scale) & 0x7fffff) == 0;
+    const float inv = 1.f / scale;
+    uint8_t* to = pool + b * a.s_block;
+    for (int r = warp * G; r < rows; r += STEP) {
+      if (rows > STEP) row(t0 + r + g, r + g < rows, y0, y1);
+      if (r + g < rows && in_dim) {
+        uint8_t* dst = to + (a.slot[t0 + r + g] & within) * a.s_token;
+        *reinterpret_cast<uint2*>(dst + e0) = to_e4m3(y0, scale, inv, pow2);
+        *reinterpret_cast<uint2*>(dst + e1) = to_e4m3(y1, scale, inv, pow2);
+      }
+    }
+    if (!begun && scale != old) {
+      const float ratio = old / scale;
+      const int chunks = a.dim / 16;
+      for (int x = tid; x < (within + 1) * chunks; x += APPEND_THREADS) {
+        const int place = x / chunks;
+        if ((s_placed[place >> 5] >> (place & 31)) & 1) continue;
+        uint4* at = reinterpret_cast<uint4*>(to + place * a.s_token + (x - place * chunks) * 16);
+        const uint4 w = *at;
+        *at = make_uint4(rescale_e4m3(w.x, ratio), rescale_e4m3(w.y, ratio), rescale_e4m3(w.z, ratio), rescale_e4m3(w.w, ratio));
+      }
+    }
+    if (tid == 0) scales[b * s.hk] = scale;  // all have read the old one
+  }
+}
+
+template <class T, int LANES, bool NEIGHBOURS>
+__global__ void __launch_bounds__(APPEND_THREADS, 5) k_kv_append8(Store8Args s) {
+  __shared__ uint4 s_x[APPEND_THREADS / 32][APPEND_FLIGHT][2][32];
+  if (blockIdx.x < s.store_ctas) store8_runs<T, LANES, NEIGHBOURS>(s);
+  else append_rows<T, LANES, NEIGHBOURS>(s.a, s_x, blockIdx.x - s.store_ctas);
+}
+
 template <class T, int LANES>
-static void append_launch(AppendArgs& a, bool neighbours, int sms, cudaStream_t st) {
+static unsigned append_split(AppendArgs& a, int sms) {
   constexpr int HEADS = 32 / LANES;
   const int all = (a.hq + 2 * a.hk + HEADS - 1) / HEADS;
   // a warp takes a token, or less of it while that fills the GPU's SMs with 16 warps each
@@ -489,7 +718,29 @@ static void append_launch(AppendArgs& a, bool neighbours, int sms, cudaStream_t 
   a.chunks = (int)std::min<int64_t>(all, std::max<int64_t>(1, enough / std::max<int64_t>(a.T, 1)));
   a.passes = (all + a.chunks - 1) / a.chunks;
   a.chunks = (all + a.passes - 1) / a.passes;
-  const unsigned grid = (unsigned)((a.T * a.chunks * 32 + APPEND_THREADS - 1) / APPEND_THREADS);
+  return (unsigned)((a.T * a.chunks * 32 + APPEND_THREADS - 1) / APPEND_THREADS);
+}
+
+template <class T, int LANES>
+static void append8_launch(Store8Args& s, bool neighbours, int sms, cudaStream_t st) {
+  const unsigned grid = append_split<T, LANES>(s.a, sms);
+  // a CTA for every token while that is no more than 16 for each SM
+  s.chunk = (int)std::max<int64_t>(1, std::min<int64_t>(STORE8_CHUNK, s.a.T * 2 * s.hk / ((int64_t)sms * 16)));
+  s.store_ctas = (int)((s.a.T + s.chunk - 1) / s.chunk) * 2 * s.hk;
+  if (neighbours) k_kv_append8<T, LANES, true><<<s.store_ctas + grid, APPEND_THREADS, 0, st>>>(s);
+  else k_kv_append8<T, LANES, false><<<s.store_ctas + grid, APPEND_THREADS, 0, st>>>(s);
+}
+
+template <class T>
+static void append8_lanes(Store8Args& s, bool neighbours, int sms, cudaStream_t st) {
+  if (s.a.dim <= 64) append8_launch<T, 4>(s, neighbours, sms, st);
+  else if (s.a.dim <= 128) append8_launch<T, 8>(s, neighbours, sms, st);
+  else append8_launch<T, 16>(s, neighbours, sms, st);
+}
+
+template <class T, int LANES>
+static void append_launch(AppendArgs& a, bool neighbours, int sms, cudaStream_t st) {
+  const unsigned grid = append_split<T, LANES>(a, sms);
   if (neighbours) k_kv_append<T, LANES, true><<<grid, APPEND_THREADS, 0, st>>>(a);
   else k_kv_append<T, LANES, false><<<grid, APPEND_THREADS, 0, st>>>(a);
 }
@@ -557,8 +808,9 @@ extern "C" int tk_kv_plan(const int64_t* d_off, const int32_t* d_ctx, int64_t R,
   return TK_OK;
 }
 
-// The cache as a tensor (element, token, head, block) whose box is 64
-// elements of one head's block, or of half of one of 128 tokens: 128-byte rows, swizzled as the tensor cores read them.
+// The cache as a tensor (element, token, head, block).  16 bits: its box is 64 elements of one head's
+// block, or of half of one of 128 tokens: 128-byte rows, swizzled as the tensor cores read them.  8 bits: 16
+// tokens of all elements, swizzled so that eight lanes that read 16 bytes of eight rows meet no bank twice.
 static bool kv_map(const tk_kv_cache* c, void* mem, CUtensorMap* map) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -568,19 +820,24 @@ static bool kv_map(const tk_kv_cache* c, void* mem, CUtensorMap* map) {
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
       found != cudaDriverEntryPointSuccess)
     return false;
+  const bool e8 = c->k_scale != nullptr;
+  const cuuint64_t size = e8 ? 1 : 2;
   const cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->block_size, (cuuint64_t)c->n_heads, (cuuint64_t)c->n_blocks};
-  const cuuint64_t strides[3] = {(cuuint64_t)c->stride[2] * 2, (cuuint64_t)c->stride[1] * 2, (cuuint64_t)c->stride[0] * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)std::min(c->block_size, 64), 1, 1}, step[4] = {1, 1, 1, 1};
-  return reinterpret_cast<Encode>(fn)(map, c->type == TK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+  const cuuint64_t strides[3] = {(cuuint64_t)c->stride[2] * size, (cuuint64_t)c->stride[1] * size, (cuuint64_t)c->stride[0] * size};
+  const cuuint32_t box[4] = {e8 ? (cuuint32_t)c->head_dim : 64u, e8 ? 16u : (cuuint32_t)std::min(c->block_size, 64), 1, 1},
+                   step[4] = {1, 1, 1, 1};
+  return reinterpret_cast<Encode>(fn)(map,
+                                      e8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                         : c->type == TK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                                       4, mem, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                                      e8 && c->head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-extern "C" int tk_kv_cache_create(void* d_k, void* d_v, int type, int64_t n_blocks, int n_heads, int block_size,
-                                  int head_dim, const int64_t* stride, tk_kv_cache** out) {
+static int kv_create(const char* where, void* d_k, void* d_v, float* d_k_scale, float* d_v_scale, int type, int64_t n_blocks,
+                     int n_heads, int block_size, int head_dim, const int64_t* stride, tk_kv_cache** out) {
   using namespace tk;
-  const char* where = "tk_kv_cache_create";
+  const int unit = d_k_scale ? 16 : 8;  // elements of 16 bytes
   if (!out || !d_k || !d_v) return kv_arg(where, "null pointer");
   *out = nullptr;
   if (type != TK_BF16 && type != TK_F16) return kv_arg(where, "type is neither TK_BF16 nor TK_F16");
@@ -590,8 +847,8 @@ extern "C" int tk_kv_cache_create(void* d_k, void* d_v, int type, int64_t n_bloc
   int64_t st[3] = {(int64_t)n_heads * block_size * head_dim, (int64_t)block_size * head_dim, head_dim};
   for (int i = 0; i < 3 && stride; i++) {
     st[i] = stride[i];
-    if (st[i] < head_dim || st[i] % 8 || st[i] >= (int64_t)1 << 38)
-      return kv_arg(where, "a stride is below head_dim, no multiple of 8 elements, or 2^38 and more");
+    if (st[i] < head_dim || st[i] % unit || st[i] >= (int64_t)1 << 38)
+      return kv_arg(where, "a stride is below head_dim, no multiple of 16 bytes, or 2^38 and more");
   }
   if (!aligned16(d_k) || !aligned16(d_v)) return kv_arg(where, "keys or values are not 16-byte aligned");
   int dev = 0, sms = 1;
@@ -617,6 +874,8 @@ extern "C" int tk_kv_cache_create(void* d_k, void* d_v, int type, int64_t n_bloc
   for (int i = 0; i < 3; i++) c->stride[i] = st[i];
   c->k = d_k;
   c->v = d_v;
+  c->k_scale = d_k_scale;
+  c->v_scale = d_v_scale;
   if (head_dim == 64 || head_dim == 128) {
     if (!kv_map(c, d_k, &c->map_k) || !kv_map(c, d_v, &c->map_v)) {
       delete c;
@@ -626,6 +885,19 @@ extern "C" int tk_kv_cache_create(void* d_k, void* d_v, int type, int64_t n_bloc
   }
   *out = c;
   return TK_OK;
+}
+
+extern "C" int tk_kv_cache_create(void* d_k, void* d_v, int type, int64_t n_blocks, int n_heads, int block_size,
+                                  int head_dim, const int64_t* stride, tk_kv_cache** out) {
+  return kv_create("tk_kv_cache_create", d_k, d_v, nullptr, nullptr, type, n_blocks, n_heads, block_size, head_dim, stride, out);
+}
+
+extern "C" int tk_kv_cache_create8(void* d_k, void* d_v, float* d_k_scale, float* d_v_scale, int type, int64_t n_blocks,
+                                   int n_heads, int block_size, int head_dim, const int64_t* stride, tk_kv_cache** out) {
+  const char* where = "tk_kv_cache_create8";
+  if (!d_k_scale || !d_v_scale) return kv_arg(where, "null pointer");
+  if ((((uintptr_t)d_k_scale | (uintptr_t)d_v_scale) & 3) != 0) return kv_arg(where, "scales are not 4-byte aligned");
+  return kv_create(where, d_k, d_v, d_k_scale, d_v_scale, type, n_blocks, n_heads, block_size, head_dim, stride, out);
 }
 
 extern "C" void tk_kv_cache_free(tk_kv_cache* cache) { delete cache; }
@@ -652,7 +924,16 @@ extern "C" int tk_kv_append(const tk_kv_cache* cache, const void* d_qkv, int64_t
   AppendArgs a = {d_qkv, row_stride, T, n_q_heads, cache->n_heads, cache->head_dim, d_q_gain, d_k_gain, eps, d_rope,
                   rope_len, rot_dim, d_pos, d_slot, d_q, cache->k, cache->v, cache->stride[0], cache->stride[1],
                   cache->stride[2], cache->n_blocks << cache->log2_block, cache->log2_block, 0, 0};
-  if (cache->type == TK_BF16) append_lanes<__nv_bfloat16>(a, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);
+  if (cache->k_scale) {
+    // its CTAs are counted in 32 bits, with room for the queries'
+    if (T / STORE8_CHUNK * 2 * cache->n_heads > 1 << 29) return kv_arg(where, "more rows and heads than one call takes");
+    a.hk = 0;
+    a.k = a.v = nullptr;
+    Store8Args s = {a, cache->n_heads, static_cast<uint8_t*>(cache->k), static_cast<uint8_t*>(cache->v), cache->k_scale,
+                    cache->v_scale, 0, 0};
+    if (cache->type == TK_BF16) append8_lanes<__nv_bfloat16>(s, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);
+    else append8_lanes<__half>(s, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);
+  } else if (cache->type == TK_BF16) append_lanes<__nv_bfloat16>(a, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);
   else append_lanes<__half>(a, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {

@@ -51,6 +51,8 @@ struct tk_kv_cache {
   int64_t stride[3];  // block, head, token, in elements
   void* k;
   void* v;
+  float* k_scale;  // [n_blocks][n_heads] of a cache in 8 bits, else null
+  float* v_scale;
   CUtensorMap map_k, map_v;  // for tk_kv_attend; head_dim 64 and 128 only
 };
 

@@ -187,17 +187,35 @@ class KVWorkspace:
 class KVCache:
     """The paged cache of one layer over caller-owned tensors k, v
     [n_blocks, kv_heads, block_size, head_dim] (bfloat16 or float16; any
-    strides that are multiples of 8 elements, the last dimension contiguous)."""
+    strides that are multiples of 8 elements, the last dimension contiguous).
 
-    def __init__(self, k, v):
+    In 8 bits k and v are float8_e4m3fn (strides multiples of 16 elements) and stand for multiples of k_scale and
+    v_scale, contiguous float32[n_blocks, kv_heads]; dtype is then the type of rows, queries and outputs
+    (tk_kv_cache_create8). Blocks that hold nothing yet need no scale."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None, dtype=None):
         torch = _torch()
         types = {torch.bfloat16: native.TK_BF16, torch.float16: native.TK_F16}
-        _need(k.is_cuda and k.dim() == 4 and k.dtype in types, "k must be a 4-dimensional bf16 or fp16 GPU tensor")
+        in_8 = k.dtype is torch.float8_e4m3fn
+        _need(k.is_cuda and k.dim() == 4 and (in_8 or k.dtype in types),
+              "k must be a 4-dimensional bf16, fp16 or float8_e4m3fn GPU tensor")
         _need(v.device == k.device and v.shape == k.shape and v.dtype == k.dtype and v.stride() == k.stride(),
               "v must have k's device, shape, type and strides")
         _need(k.stride(3) == 1, "the last dimension must be contiguous")
         self._h = None
-        self.k, self.v, self.device, self.dtype = k, v, k.device, k.dtype
+        if in_8:
+            dtype = torch.bfloat16 if dtype is None else dtype
+            _need(dtype in types, "dtype must be bf16 or fp16")
+            for x in (k_scale, v_scale):
+                _need(x is not None and x.dtype is torch.float32 and x.shape == k.shape[:2] and x.is_contiguous()
+                      and x.get_device() == k.get_device(),
+                      "k_scale and v_scale must be contiguous float32[n_blocks, kv_heads] tensors on k's device")
+        else:
+            _need(k_scale is None and v_scale is None and dtype in (None, k.dtype),
+                  "scales and a type of their own go with float8_e4m3fn keys and values only")
+            dtype = k.dtype
+        self.k, self.v, self.device, self.dtype = k, v, k.device, dtype
+        self.k_scale, self.v_scale = k_scale, v_scale
         self._index = k.get_device()
         _need_current(self._index)
         self.n_blocks, self.kv_heads, self.block_size, self.head_dim = k.shape
@@ -205,18 +223,22 @@ class KVCache:
         d = self.head_dim
         packed = (self.kv_heads * self.block_size * d, self.block_size * d, d)
         stride = [s if n > 1 else p for s, n, p in zip(k.stride(), k.shape, packed)]
-        self._h = native.tk_kv_cache_create(k.data_ptr(), v.data_ptr(), types[k.dtype], self.n_blocks, self.kv_heads,
-                                            self.block_size, d, stride)
+        geometry = types[dtype], self.n_blocks, self.kv_heads, self.block_size, d, stride
+        if in_8:
+            self._h = native.tk_kv_cache_create8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *geometry)
+        else:
+            self._h = native.tk_kv_cache_create(k.data_ptr(), v.data_ptr(), *geometry)
 
     def append(self, qkv, positions, slots, q_heads, q_gain=None, k_gain=None, rope=None, eps=1e-6,
                neighbours=False, out=None, stream=None):
         """qkv [T, (q_heads + 2 kv_heads) * head_dim] -> queries [T, q_heads,
         head_dim], normed and rotated; keys (normed, rotated) and values are
-        stored at `slots` (tk_kv_append). gains float32[head_dim], rope
+        stored at `slots` (tk_kv_append; in 8 bits with a scale for each block and head, the rows of a block
+        next to one another, as `kv_plan` places them). gains float32[head_dim], rope
         float32[n, rot_dim / 2, 2] (`rope_table`)."""
         if stream is not None:
             return _on(stream, lambda: self.append(qkv, positions, slots, q_heads, q_gain, k_gain, rope, eps, neighbours, out),
-                       qkv, positions, slots, q_gain, k_gain, rope, out, self.k, self.v)
+                       qkv, positions, slots, q_gain, k_gain, rope, out, self.k, self.v, self.k_scale, self.v_scale)
         torch = _torch()
         index, d = self._index, self.head_dim
         T, width = qkv.shape  # a ValueError if there are not two dimensions
@@ -252,7 +274,7 @@ class KVCache:
         return out
 
     def attend(self, q, offsets, lengths, table, workspace, masks=None, scale=None, max_new=None, lse=False,
-               out=None, stream=None):
+               out=None, stream=None, window=None, sinks=0):
         """q [T, q_heads, head_dim] -> out of the same shape: each request's new
         tokens over its cache (tk_kv_attend). masks int64[T] as `kv_plan` makes
         them for drafted trees, None = each token sees those before it. scale
@@ -261,10 +283,15 @@ class KVCache:
         max_new=1 can be a quarter faster). lse=True also returns
         float32[T, q_heads]. Tokens of no request, and rows that see nothing, give
         0 and an lse of -inf; so do requests outside the call's limits, of which
-        only workspace.status() tells."""
+        only workspace.status() tells.
+
+        window: a token sees the `window` places up to its own, itself among them, and the first `sinks` of its
+        request (tk_kv_attend_window). Under masks, where it is 64 at least, it is the context
+        that they limit, and a token's own place comes after those of the drafted tokens it sees."""
         if stream is not None:
-            return _on(stream, lambda: self.attend(q, offsets, lengths, table, workspace, masks, scale, max_new, lse, out),
-                       q, offsets, lengths, table, masks, out, self.k, self.v)
+            return _on(stream, lambda: self.attend(q, offsets, lengths, table, workspace, masks, scale, max_new, lse, out, None,
+                                                   window, sinks),
+                       q, offsets, lengths, table, masks, out, self.k, self.v, self.k_scale, self.v_scale)
         torch = _torch()
         index, d = self._index, self.head_dim
         T, hq, width = q.shape  # a ValueError if there are not three dimensions
@@ -284,12 +311,17 @@ class KVCache:
         elif out.shape != q.shape or out.dtype is not self.dtype or not out.is_contiguous() or out.get_device() != index:
             raise ValueError("out must be a contiguous tensor of q's shape and type")
         sums = torch.empty((T, hq), dtype=torch.float32, device=self.device) if lse else None
-        rc = native.load().tk_kv_attend(self._h, workspace._h, q.data_ptr(), _row_stride(step, T, hq * d, "q"), hq, p_off, R, T,
-                                        T if max_new is None else max_new, p_len, p_table, stride, W, p_mask,
-                                        d ** -0.5 if scale is None else scale, out.data_ptr(),
-                                        sums.data_ptr() if lse else None, _raw_stream(index))
+        common = (self._h, workspace._h, q.data_ptr(), _row_stride(step, T, hq * d, "q"), hq, p_off, R, T,
+                  T if max_new is None else max_new, p_len, p_table, stride, W, p_mask)
+        rest = (d ** -0.5 if scale is None else scale, out.data_ptr(), sums.data_ptr() if lse else None, _raw_stream(index))
+        if window is None:
+            if sinks:
+                raise ValueError("sinks go with a window")
+            rc = native.load().tk_kv_attend(*common, *rest)
+        else:
+            rc = native.load().tk_kv_attend_window(*common, window, sinks, *rest)
         if rc:
-            native.check(rc, "tk_kv_attend")
+            native.check(rc, "tk_kv_attend" if window is None else "tk_kv_attend_window")
         return (out, sums) if lse else out
 
     def close(self):

@@ -59,11 +59,14 @@ SIGNATURES = {
     "tk_last_cache_stats": (_INT, [_P, ctypes.POINTER(_I64), ctypes.POINTER(_I64)]),
     "tk_kv_plan": (_INT, [_P, _P, _I64, _I64, _INT, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "tk_kv_cache_create": (_INT, [_P, _P, _INT, _I64, _INT, _INT, _INT, ctypes.POINTER(_I64), ctypes.POINTER(_P)]),
+    "tk_kv_cache_create8": (_INT, [_P, _P, _P, _P, _INT, _I64, _INT, _INT, _INT, ctypes.POINTER(_I64), ctypes.POINTER(_P)]),
     "tk_kv_cache_free": (None, [_P]),
     "tk_kv_append": (_INT, [_P, _P, _I64, _I64, _INT, _P, _P, _F32, _P, _I64, _INT, _INT, _P, _P, _P, _P]),
     "tk_kv_workspace_create": (_INT, [ctypes.POINTER(_P)]),
     "tk_kv_workspace_free": (None, [_P]),
     "tk_kv_attend": (_INT, [_P, _P, _P, _I64, _INT, _P, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _F32, _P, _P, _P]),
+    "tk_kv_attend_window": (_INT, [_P, _P, _P, _I64, _INT, _P, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I64, _F32, _P, _P,
+                                   _P]),
     "tk_kv_status": (_INT, [_P, ctypes.POINTER(_I64), _P]),
     "tk_status_string": (ctypes.c_char_p, [_INT]),
     "tk_last_error": (ctypes.c_char_p, []),
@@ -262,6 +265,15 @@ def tk_kv_cache_create(d_k, d_v, type, n_blocks, n_heads, block_size, head_dim, 
     st = (_I64 * 3)(*stride) if stride is not None else None
     check(load().tk_kv_cache_create(d_k, d_v, type, n_blocks, n_heads, block_size, head_dim, st, ctypes.byref(h)),
           "tk_kv_cache_create")
+    return h
+
+
+def tk_kv_cache_create8(d_k, d_v, d_k_scale, d_v_scale, type, n_blocks, n_heads, block_size, head_dim, stride=None):
+    """A cache in 8 bits; as tk_kv_cache_create, with the addresses of the scales."""
+    h = _P()
+    st = (_I64 * 3)(*stride) if stride is not None else None
+    check(load().tk_kv_cache_create8(d_k, d_v, d_k_scale, d_v_scale, type, n_blocks, n_heads, block_size, head_dim, st,
+                                     ctypes.byref(h)), "tk_kv_cache_create8")
     return h
 
 

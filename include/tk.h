@@ -350,6 +350,18 @@ int tk_kv_cache_create(void* d_k, void* d_v, int type, int64_t n_blocks, int n_h
 void tk_kv_cache_free(tk_kv_cache* cache);
 
 /*
+ * The same in 8 bits: e4m3 values (the OCP format without infinities) with an fp32 scale for each
+ * block and head, for keys and values apart: the element stands for e4m3 * scale.
+ *
+ *   d_k, d_v: as above with one byte an element; strides multiples of 16 elements.
+ *   d_k_scale, d_v_scale [n_blocks][n_heads]: finite, 0 or above (tk_kv_append writes powers of two; of
+ *       blocks that hold nothing yet they need not be set).
+ *   type: of the rows, queries and outputs of the calls (TK_BF16 or TK_F16).
+ */
+int tk_kv_cache_create8(void* d_k, void* d_v, float* d_k_scale, float* d_v_scale, int type, int64_t n_blocks,
+                        int n_heads, int block_size, int head_dim, const int64_t* stride, tk_kv_cache** out);
+
+/*
  * tk_kv_append -- norm of queries and keys for each head, rotation by
  * position, and the store into the cache, in one pass over the projection.
  *
@@ -366,6 +378,14 @@ void tk_kv_cache_free(tk_kv_cache* cache);
  *       is negative or past the cache stores nothing.  A position outside
  *       [0, rope_len) gives NaN in the rotated elements.
  *   d_q[T][n_q_heads][head_dim]: the queries, packed.
+ *
+ * Into a cache in 8 bits the rows go from fp32 to e4m3 in one rounding, as multiples of their block's scale.
+ * For each head, keys and values apart, a call that stores a block's first place gives the block a new scale, the
+ * least power of two (2^-100 at least) that its largest new element fits 448 times; any other call raises the
+ * scale to that if it is less, and rounds the block's older elements once more.  Infinities
+ * and NaN are stored as NaN and do not count for the scale.  The rows of one block follow one another
+ * in the call, as tk_kv_plan places them; of blocks whose rows do not, the scale and the elements are unspecified, and
+ * so are those of a place that two rows name.
  */
 int tk_kv_append(const tk_kv_cache* cache, const void* d_qkv, int64_t row_stride, int64_t T,
                  int n_q_heads, const float* d_q_gain, const float* d_k_gain, float eps,
@@ -427,6 +447,23 @@ int tk_kv_attend(const tk_kv_cache* cache, tk_kv_workspace* ws, const void* d_q,
                  int64_t table_width, const int64_t* d_mask, float scale, void* d_out, float* d_lse,
                  void* cuda_stream);
 int tk_kv_status(tk_kv_workspace* ws, int64_t* h_request, void* cuda_stream);
+
+/*
+ * tk_kv_attend_window -- tk_kv_attend of a layer whose tokens see a window of the cache and its first
+ * tokens; only their tiles are read.
+ *
+ *   window: a token sees the places from window - 1 before its own on, 1 or above.
+ *   sinks: and the first `sinks` places of its request, 0 or above.
+ *
+ * With d_mask NULL that holds for every place up to the token's own.  With masks it holds for the
+ * context, the mask alone decides on new tokens, and a token's own place is d_len - new + the number of
+ * other new tokens that it sees (its d_pos, for the masks of tk_kv_plan); window is 64 or above then.
+ */
+int tk_kv_attend_window(const tk_kv_cache* cache, tk_kv_workspace* ws, const void* d_q, int64_t q_stride,
+                        int n_q_heads, const int64_t* d_off, int64_t R, int64_t T, int64_t max_new,
+                        const int32_t* d_len, const int32_t* d_table, int64_t table_stride,
+                        int64_t table_width, const int64_t* d_mask, int64_t window, int64_t sinks,
+                        float scale, void* d_out, float* d_lse, void* cuda_stream);
 
 /*
  * Per-kernel timing of encodes on a workspace, for benchmarks.  With
