@@ -13,8 +13,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD_DIR, "libtk.so")
-SOURCES = ["tk_encode.cu", "tk_scan.cu", "tk_tokenizer.cu", "tk_noalloc.cu", "tk_kv.cu", "tk_attend.cu", "tk_attend8.cu"]
-HEADERS = ["tk_internal.cuh", "tk_kv.cuh", "tk_attend.cuh", "tk_blackwell.cuh", "tk_unicode_table.h"]
+SOURCES = ["tk_encode.cu", "tk_scan.cu", "tk_tokenizer.cu", "tk_noalloc.cu", "tk_kv.cu", "tk_attend.cu",
+           "tk_attend_window.cu", "tk_attend8.cu", "tk_attend8_mma.cu"]
+HEADERS = ["tk_internal.cuh", "tk_kv.cuh", "tk_attend.cuh", "tk_attend_mma.cuh", "tk_blackwell.cuh", "tk_unicode_table.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

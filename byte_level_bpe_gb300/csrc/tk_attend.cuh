@@ -394,7 +394,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// Attention over a cache in 8 bits (tk_attend8.cu); rows: of a request and key head, at most.
-cudaError_t attend8(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, cudaStream_t st);
+// The kernels' launches; rows: of a request and key head, at most.  With a window over a cache in 16 bits
+// (tk_attend_window.cu), over a cache in 8 bits (tk_attend8.cu, of few rows), and of many rows (tk_attend8_mma.cu).
+cudaError_t attend_windowed(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, int grid, cudaStream_t st);
+cudaError_t attend8(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, int grid, cudaStream_t st);
+cudaError_t attend8_many(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, int grid, cudaStream_t st);
 
 }  // namespace tk

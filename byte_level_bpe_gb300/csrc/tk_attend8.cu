@@ -18,10 +18,6 @@
 // they are, four neighbouring elements being one thread's share of a product of 16, which may be any 16 as long as
 // the queries take the same; of the values a thread has four keys' 16 bytes, whose bytes it pairs up.
 // Nothing is written to shared memory but what TMA brings.
-#include <algorithm>
-
-#include <cuda_fp8.h>
-
 #include "tk_attend.cuh"
 
 namespace tk {
@@ -59,17 +55,6 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// two e4m3 -> two fp16; of the lower or upper half of a word
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
-  uint32_t d;
-  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %1;\ncvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(d) : "r"(w));
-  return d;
-}
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
-  uint32_t d;
-  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %1;\ncvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(d) : "r"(w));
-  return d;
 }
 // 0x80 in every byte that is a NaN
 __device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
@@ -585,14 +570,18 @@ static cudaError_t attend8_launch(const AttendArgs& a, const tk_kv_cache* cache,
   return cudaGetLastError();
 }
 
-template <class T, int D>
-static cudaError_t attend8_pick(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, cudaStream_t st) {
-  if (a.window < INT32_MAX)
-    return rows <= 16 ? attend8_launch<T, D, 1, true>(a, cache, st) : attend8_launch<T, D, 2, true>(a, cache, st);
-  return rows <= 16 ? attend8_launch<T, D, 1, false>(a, cache, st) : attend8_launch<T, D, 2, false>(a, cache, st);
+template <class T, int D, bool WIN>
+static cudaError_t attend8_rows(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, cudaStream_t st) {
+  return rows <= 16 ? attend8_launch<T, D, 1, WIN>(a, cache, st) : attend8_launch<T, D, 2, WIN>(a, cache, st);
 }
 
-cudaError_t attend8(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, cudaStream_t st) {
+template <class T, int D>
+static cudaError_t attend8_pick(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, cudaStream_t st) {
+  return a.window < INT32_MAX ? attend8_rows<T, D, true>(a, cache, rows, st) : attend8_rows<T, D, false>(a, cache, rows, st);
+}
+
+cudaError_t attend8(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, int grid, cudaStream_t st) {
+  if (rows > 32) return attend8_many(a, cache, rows, grid, st);
   if (cache->type == TK_BF16)
     return cache->head_dim == 64 ? attend8_pick<__nv_bfloat16, 64>(a, cache, rows, st) : attend8_pick<__nv_bfloat16, 128>(a, cache, rows, st);
   return cache->head_dim == 64 ? attend8_pick<__half, 64>(a, cache, rows, st) : attend8_pick<__half, 128>(a, cache, rows, st);

@@ -174,4 +174,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// two e4m3 -> two fp16; of the lower or upper half of a word
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
+  uint32_t d;
+  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %1;\ncvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(d) : "r"(w));
+  return d;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
+  uint32_t d;
+  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %1;\ncvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(d) : "r"(w));
+  return d;
+}
+
 }  // namespace tk
