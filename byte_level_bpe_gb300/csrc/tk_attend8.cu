@@ -23,15 +23,17 @@
 namespace tk {
 
 constexpr int A8_WARPS = 8, A8_THREADS = A8_WARPS * 32;
-constexpr int A8_STEP = 16;  // keys of a step: one warp's
+constexpr int A8_SUB = 16;  // keys of a product: they lie in one block
 constexpr int A8_UNIT_COST = 1, A8_MIN_SHARE = 2, A8_SNAP = 1;
 constexpr float A8_UP = 7.f;
 
 // A warp has a ring of its own: STAGES steps of keys and values.
+// A step, one warp's, is SUBS times 16 keys.
 template <int D, int MT>
 struct Attend8Shape {
   static constexpr int ROWS = 16 * MT;
-  static constexpr int TILE = A8_STEP * D, STAGE = 2 * TILE, STAGES = 16 * 1024 / STAGE;  // 16 KB a warp
+  static constexpr int SUBS = MT == 1 ? 2 : 1, STEP = SUBS * A8_SUB;
+  static constexpr int TILE = STEP * D, STAGE = 2 * TILE, STAGES = 16 * 1024 / STAGE;  // 16 KB a warp
   static constexpr int DIMS = D / 4;                      // neighbouring columns that a thread has of an output
   static constexpr int O_GROUP = DIMS + 4, O_ROW = 4 * O_GROUP;  // floats; quarter-warps meet no bank twice
   static constexpr int O = A8_WARPS * STAGES * STAGE;     // [warp][16][O_ROW] outputs of the warps, for one 16 rows at a time
@@ -39,9 +41,10 @@ struct Attend8Shape {
   static constexpr int STATS = Q + (MT > 1 ? MT * (D / 16) * 512 : 0);  // [MT][warp][16] m, l; [warp] E
   static constexpr int BARS = STATS + (2 * MT * 16 + 2) * A8_WARPS * 4;
   static constexpr int SMALL = BARS + 8 * A8_WARPS * STAGES;
-  static constexpr int TOTAL = SMALL + 16 + 4 * A8_WARPS * 4 + 32;
+  static constexpr int PIECES = SMALL + 16 + 4 * A8_WARPS * 4 + 16;  // this one and the next one; the walk
+  static constexpr int TOTAL = PIECES + 2 * (int)sizeof(Piece) + 192;
   template <bool WIN>
-  using Tiles = Tiling<ROWS, A8_STEP, A8_WARPS, WIN, A8_UNIT_COST, A8_MIN_SHARE, A8_SNAP, 2, true>;
+  using Tiles = Tiling<ROWS, STEP, A8_WARPS, WIN, A8_UNIT_COST, A8_MIN_SHARE, A8_SNAP, 2, true>;
   static_assert(SMALL % 8 == 0 && TOTAL <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -52,7 +55,7 @@ __device__ __forceinline__ float* part8_at(float* part, int worker, int slot) {
 }
 
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -72,7 +75,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
 k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   using L = Attend8Shape<D, MT>;
   using S = typename L::template Tiles<WIN>;
-  constexpr int NST = L::STAGES, KS = D / 16, NT = D / 8, ROWS = L::ROWS, DIMS = L::DIMS;
+  constexpr int NST = L::STAGES, KS = D / 16, NT = D / 8, ROWS = L::ROWS, DIMS = L::DIMS, SUBS = L::SUBS, STEP = L::STEP;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle goes by address bits
   const uint32_t base = smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -102,56 +105,71 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
   __syncthreads();
 
   const int me = blockIdx.x;
-  Walk<S> walk;
-  walk.plan = plan;
-  walk.from = me * plan.share;
-  walk.to = min(total, walk.from + plan.share);
-  walk.r = walk.from < total ? s_walk[0] : (int)a.R;
-  walk.u = walk.from < total ? s_walk[1] : total;
-  walk.loaded = false;
+  // The walk and its pieces are in shared memory, where they cost no registers: the first thread goes on to
+  // the next piece as one begins, the other warps ask for it when they have done their steps.
+  Piece* s_piece = reinterpret_cast<Piece*>(smem + L::PIECES);
+  Walk<S>* walk = reinterpret_cast<Walk<S>*>(s_piece + 2);
+  static_assert(sizeof(Walk<S>) <= 192 && L::PIECES % 8 == 0, "room for the walk");
+  if (tid == 0) {
+    walk->plan = plan;
+    walk->from = me * plan.share;
+    walk->to = min(total, walk->from + plan.share);
+    walk->r = walk->from < total ? s_walk[0] : (int)a.R;
+    walk->u = walk->from < total ? s_walk[1] : total;
+    walk->loaded = false;
+    walk->next(a, s_piece[0]);
+  }
+  __syncthreads();
 
-  // ---- loads of the warp's steps: step i of a piece is its 16 keys number step0 + 8 i
+  // ---- loads of the warp's steps: step i of a piece is its step number step0 + 8 i
   uint32_t issued = 0, used = 0;  // stages of the ring, over all pieces
   bool ok = true;                 // no wait has given up: else the warp has no more steps
   int step0 = 0, n = 0, next = 0, window = 0;
-  int id0 = 0, id1 = 0, id2 = 0;  // block ids of steps `window`, + 32 and + 64 + lane
+  // lane: 16 keys each from step `window` on, their block ids and those of the next 32 and 32 times 16
+  constexpr int AHEAD = 32 / SUBS;  // steps of 32 lanes
+  int id0 = 0, id1 = 0, id2 = 0;
   float2 sc0 = {0.f, 0.f}, sc1 = {0.f, 0.f};  // (ks, vs) of the first two
-  Piece p;
   const int32_t* row = nullptr;
-  auto key_of = [&](const Piece& x, int step) { return (WIN && step >= x.head ? step + x.skip : step) * A8_STEP; };
-  auto id_of = [&](const Piece& x, int i) { return i < n ? __ldg(row + (key_of(x, step0 + A8_WARPS * i) >> a.log2_bs)) : 0; };
-  // (of a block outside the cache zeros are read)
-  auto scales_of = [&](const Piece& x, int id, bool in) {
-    if (!in || id < 0 || id >= a.n_blocks) return make_float2(0.f, 0.f);
+  auto key_of = [&](const Piece& x, int i) {
+    const int step = step0 + A8_WARPS * i;
+    return (WIN && step >= x.head ? step + x.skip : step) * STEP;
+  };
+  // (of a block outside the cache zeros are read, and of keys past the end)
+  auto id_of = [&](const Piece& x, int i) {
+    const int at = i + lane / SUBS, key = key_of(x, at) + lane % SUBS * A8_SUB;
+    return at < n && key < x.keys ? __ldg(row + (key >> a.log2_bs)) : -1;
+  };
+  auto scales_of = [&](const Piece& x, int id) {
+    if (id < 0 || id >= a.n_blocks) return make_float2(0.f, 0.f);
     const int64_t at = (int64_t)id * a.hk + x.h;
     return make_float2(__ldg(a.k_scale + at), __ldg(a.v_scale + at));
   };
   auto issue = [&](const Piece& x) {
-    const int i = next - window;
-    const int id = __shfl_sync(0xffffffffu, i < 32 ? id0 : id1, i & 31);
+    const int i = next - window, sub = lane % SUBS;
+    const int id = __shfl_sync(0xffffffffu, i < AHEAD ? id0 : id1, (i * SUBS + sub) & 31);
     const uint32_t st = issued % NST;
-    if (elect_one()) {
-      const int at = key_of(x, step0 + A8_WARPS * next) & ((1 << a.log2_bs) - 1);
-      bar_expect(bars + 8 * st, L::STAGE);
-      tma_load_4d(ring + st * L::STAGE, &map_k, bars + 8 * st, 0, at, x.h, id);
-      tma_load_4d(ring + st * L::STAGE + L::TILE, &map_v, bars + 8 * st, 0, at, x.h, id);
+    if (lane == 0) bar_expect(bars + 8 * st, L::STAGE);
+    __syncwarp();
+    if (lane < 2 * SUBS) {  // keys, then values
+      const int at = (key_of(x, next) + sub * A8_SUB) & ((1 << a.log2_bs) - 1);
+      tma_load_4d(ring + st * L::STAGE + lane * (A8_SUB * D), lane < SUBS ? &map_k : &map_v, bars + 8 * st, 0, at, x.h, id);
     }
     __syncwarp();
     issued++;
     next++;
   };
   auto start = [&](const Piece& x) {
-    const int steps = x.keys > 0 && ok ? min(x.hi * A8_WARPS, (x.keys + A8_STEP - 1) / A8_STEP - (WIN ? x.skip : 0)) : 0;
+    const int steps = x.keys > 0 && ok ? min(x.hi * A8_WARPS, (x.keys + STEP - 1) / STEP - (WIN ? x.skip : 0)) : 0;
     step0 = x.lo * A8_WARPS + warp;
     n = max(0, (steps - step0 + A8_WARPS - 1) / A8_WARPS);
     next = window = 0;
     row = a.table + (int64_t)x.r * a.table_stride;
-    id0 = id_of(x, lane);
-    id1 = id_of(x, 32 + lane);
-    id2 = id_of(x, 64 + lane);
+    id0 = id_of(x, 0);
+    id1 = id_of(x, AHEAD);
+    id2 = id_of(x, 2 * AHEAD);
     for (int i = 0; i < min(n, NST); i++) issue(x);
-    sc0 = scales_of(x, id0, lane < n);
-    sc1 = scales_of(x, id1, 32 + lane < n);
+    sc0 = scales_of(x, id0);
+    sc1 = scales_of(x, id1);
   };
 
   // ---- queries: rows g and g + 8 of each 16; of its DIMS neighbouring elements four are a thread's share of a product
@@ -200,13 +218,20 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
     }
   };
 
-  bool more = walk.next(a, p);
-  if (more) {
-    start(p);
-    fetch(p);
+  int cur = 0;
+  if (s_piece[0].valid) {
+    start(s_piece[0]);
+    fetch(s_piece[0]);
   }
   if (MT > 1) __syncthreads();
-  while (more) {
+  while (s_piece[cur].valid) {
+    const Piece& p = s_piece[cur];
+    const Piece& nx = s_piece[cur ^ 1];
+    if (warp == 0) {
+      if (lane == 0) walk->next(a, s_piece[cur ^ 1]);
+      __syncwarp();
+      asm volatile("bar.arrive 1, %0;" ::"n"(A8_THREADS) : "memory");
+    }
     float o[MT][NT][4];
     float m[MT][2], l[MT][2];
     int E = -1000;
@@ -217,14 +242,6 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
 #pragma unroll
       for (int j = 0; j < NT; j++) o[mt][j][0] = o[mt][j][1] = o[mt][j][2] = o[mt][j][3] = 0.f;
     }
-    Seen<WIN> seen[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-      for (int half = 0; half < 2; half++) {
-        const int rr = mt * 16 + half * 8 + g;
-        seen[mt][half].set(a, p, rr < p.rows, rr < p.rows ? (p.row0 + rr) / a.group : 0);
-      }
     float cr[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; mt++) {
@@ -234,31 +251,36 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
 
 #pragma unroll 1
     for (int i = 0; i < n && ok; i++) {
-      if (i == window + 32) {
-        window += 32;
+      if (i == window + AHEAD) {
+        window += AHEAD;
         id0 = id1;
         sc0 = sc1;
         id1 = id2;
-        sc1 = scales_of(p, id1, i + 32 + lane < n);
-        id2 = id_of(p, i + 64 + lane);
+        sc1 = scales_of(p, id1);
+        id2 = id_of(p, i + 2 * AHEAD);
       }
-      const float ks = __shfl_sync(0xffffffffu, sc0.x, i & 31), vs = __shfl_sync(0xffffffffu, sc0.y, i & 31);
-      const int k0 = key_of(p, step0 + A8_WARPS * i);
-      const bool hidden = !(k0 + A8_STEP <= p.open && (!WIN || k0 >= p.shut || k0 + A8_STEP <= a.sinks));
+      float ks[SUBS], vs[SUBS];
+#pragma unroll
+      for (int u = 0; u < SUBS; u++) {
+        ks[u] = __shfl_sync(0xffffffffu, sc0.x, (i * SUBS + u) & 31);
+        vs[u] = __shfl_sync(0xffffffffu, sc0.y, (i * SUBS + u) & 31);
+      }
+      const int k0 = key_of(p, i);
+      const bool hidden = !(k0 + STEP <= p.open && (!WIN || k0 >= p.shut || k0 + STEP <= a.sinks));
       const uint32_t st = used % NST, s_k = ring + st * L::STAGE, s_v = s_k + L::TILE;
       ok = __all_sync(0xffffffffu, bar_wait(bars + 8 * st, (used / NST) & 1, abort)) != 0;
       if (!ok) break;
       used++;
 
       // scores
-      float s[MT][2][4];
+      float s[MT][2 * SUBS][4];
 #pragma unroll
       for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-        for (int e = 0; e < 8; e++) s[mt][e >> 2][e & 3] = 0.f;
-      uint32_t kw[2][D / 16];
+        for (int e = 0; e < 8 * SUBS; e++) s[mt][e >> 2][e & 3] = 0.f;
+      uint32_t kw[2 * SUBS][D / 16];
 #pragma unroll
-      for (int j = 0; j < 2; j++) {
+      for (int j = 0; j < 2 * SUBS; j++) {
         const int key = j * 8 + g;
         if constexpr (D == 128) {
           lds<4>(kw[j], s_k + key * 128 + (((2 * t4) ^ (key & 7)) << 4));
@@ -269,42 +291,57 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
       }
 #pragma unroll
       for (int k = 0; k < KS; k++) {
-        const uint32_t b00 = e4m3_lo(kw[0][k]), b01 = e4m3_hi(kw[0][k]), b10 = e4m3_lo(kw[1][k]), b11 = e4m3_hi(kw[1][k]);
+        uint32_t q4[MT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
-          uint32_t q4[4];
           if constexpr (MT == 1) {
 #pragma unroll
-            for (int e = 0; e < 4; e++) q4[e] = qa[k][e];
+            for (int e = 0; e < 4; e++) q4[mt][e] = qa[k][e];
           } else {
-            lds<4>(q4, base + L::Q + ((mt * KS + k) * 32 + lane) * 16);
+            lds<4>(q4[mt], base + L::Q + ((mt * KS + k) * 32 + lane) * 16);
           }
-          mma16816(s[mt][0], q4, b00, b01);
-          mma16816(s[mt][1], q4, b10, b11);
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * SUBS; j++) {
+          const uint32_t b0 = e4m3_lo(kw[j][k]), b1 = e4m3_hi(kw[j][k]);
+#pragma unroll
+          for (int mt = 0; mt < MT; mt++) mma16816(s[mt][j], q4[mt], b0, b1);
         }
       }
-      // values: keys 2 t4, + 1, + 8, + 9; neighbouring columns g * NT ..
-      uint32_t vw[4][NT / 4];
+      // values: of each 16 keys 2 t4, + 1, + 8, + 9; neighbouring columns g * NT ..
+      uint32_t vw[SUBS][4][NT / 4];
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const int key = 2 * t4 + (e & 1) + (e >> 1) * 8;
-        if constexpr (D == 128) lds<4>(vw[e], s_v + key * 128 + ((g ^ (key & 7)) << 4));
-        else lds<2>(vw[e], s_v + key * 64 + (((g >> 1) ^ ((key >> 1) & 3)) << 4) + (g & 1) * 8);
-      }
+      for (int u = 0; u < SUBS; u++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const int key = u * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8;
+          if constexpr (D == 128) lds<4>(vw[u][e], s_v + key * 128 + ((g ^ (key & 7)) << 4));
+          else lds<2>(vw[u][e], s_v + key * 64 + (((g >> 1) ^ ((key >> 1) & 3)) << 4) + (g & 1) * 8);
+        }
       __syncwarp();  // the stage has been read
       if (next < n) issue(p);
 
-      const int ev = vs > 0.f ? (int)((__float_as_uint(vs) >> 23) & 255) - 126 : -1000;  // vs <= 2^ev
+      float largest = vs[0];
+      if (SUBS > 1) largest = fmaxf(vs[0], vs[SUBS - 1]);
+      const int ev = largest > 0.f ? (int)((__float_as_uint(largest) >> 23) & 255) - 126 : -1000;  // vs <= 2^ev
       const bool larger = ev > E;
-      const float shrink = larger ? (E < -500 ? 0.f : exp2f((float)(E - ev))) : 1.f;
-      if (larger) E = ev;
-      const float vn = vs > 0.f ? vs * __uint_as_float((uint32_t)(127 - E / 2) << 23) * __uint_as_float((uint32_t)(127 - (E - E / 2)) << 23) : 0.f;
-      uint32_t w4[MT][4], bits[MT][2];
+      float shrink = 1.f;
+      if (larger) {
+        shrink = E < -500 ? 0.f : exp2f((float)(E - ev));
+        E = ev;
+      }
+      // 2^-E in two factors: it may be below the least normal number
+      const float down = E < -500 ? 0.f : __uint_as_float((uint32_t)(127 - E / 2) << 23),
+                  down2 = E < -500 ? 0.f : __uint_as_float((uint32_t)(127 - (E - E / 2)) << 23);
+      float vn[SUBS];
+#pragma unroll
+      for (int u = 0; u < SUBS; u++) vn[u] = vs[u] * down * down2;
+      uint32_t w4[MT][SUBS][4], bits[MT][2];
 #pragma unroll
       for (int mt = 0; mt < MT; mt++) {
-        const float c0 = cr[mt][0] * ks, c1 = cr[mt][1] * ks;
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
+        for (int j = 0; j < 2 * SUBS; j++) {
+          const float c0 = cr[mt][0] * ks[j >> 1], c1 = cr[mt][1] * ks[j >> 1];
           s[mt][j][0] *= c0;
           s[mt][j][1] *= c0;
           s[mt][j][2] *= c1;
@@ -313,9 +350,12 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
         if (hidden) {
 #pragma unroll
           for (int half = 0; half < 2; half++) {
-            bits[mt][half] = seen[mt][half].bits(k0);
+            const int rr = mt * 16 + half * 8 + g;
+            Seen<WIN> seen;
+            seen.set(a, p, rr < p.rows, rr < p.rows ? (p.row0 + rr) / a.group : 0);
+            bits[mt][half] = seen.bits(k0);
 #pragma unroll
-            for (int j = 0; j < 2; j++)
+            for (int j = 0; j < 2 * SUBS; j++)
 #pragma unroll
               for (int e = 0; e < 2; e++)
                 if (!((bits[mt][half] >> (j * 8 + 2 * t4 + e)) & 1)) s[mt][j][half * 2 + e] = -INFINITY;
@@ -325,7 +365,9 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
         bool grow = false;
 #pragma unroll
         for (int half = 0; half < 2; half++) {
-          float x = fmaxf(fmaxf(s[mt][0][2 * half], s[mt][0][2 * half + 1]), fmaxf(s[mt][1][2 * half], s[mt][1][2 * half + 1]));
+          float x = fmaxf(s[mt][0][2 * half], s[mt][0][2 * half + 1]);
+#pragma unroll
+          for (int j = 1; j < 2 * SUBS; j++) x = max3(x, s[mt][j][2 * half], s[mt][j][2 * half + 1]);
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
           mx[half] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
           grow |= mx[half] > m[mt][half] && !(mx[half] - m[mt][half] <= 8.f);
@@ -349,15 +391,18 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
           }
         }
         const float m0 = m[mt][0] == -INFINITY ? 0.f : m[mt][0] - A8_UP, m1 = m[mt][1] == -INFINITY ? 0.f : m[mt][1] - A8_UP;
+        float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
+        for (int j = 0; j < 2 * SUBS; j++) {
           const float p0 = exp2_fast(s[mt][j][0] - m0), p1 = exp2_fast(s[mt][j][1] - m0), p2 = exp2_fast(s[mt][j][2] - m1),
                       p3 = exp2_fast(s[mt][j][3] - m1);
-          l[mt][0] += p0 + p1;
-          l[mt][1] += p2 + p3;
-          w4[mt][2 * j] = pack2<__half>(p0 * vn, p1 * vn);
-          w4[mt][2 * j + 1] = pack2<__half>(p2 * vn, p3 * vn);
+          l0 += p0 + p1;
+          l1 += p2 + p3;
+          w4[mt][j >> 1][2 * (j & 1)] = pack2<__half>(p0 * vn[j >> 1], p1 * vn[j >> 1]);
+          w4[mt][j >> 1][2 * (j & 1) + 1] = pack2<__half>(p2 * vn[j >> 1], p3 * vn[j >> 1]);
         }
+        l[mt][0] += l0;
+        l[mt][1] += l1;
       }
 
       // values of keys that a row does not see have no influence on it: NaN become 0, and come
@@ -365,56 +410,60 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
       uint32_t bad = 0;
       if (hidden) {
 #pragma unroll
-        for (int e = 0; e < 4; e++)
+        for (int u = 0; u < SUBS; u++)
 #pragma unroll
-          for (int j = 0; j < NT / 4; j++) bad |= e4m3_nan(vw[e][j]);
+          for (int e = 0; e < 4; e++)
+#pragma unroll
+            for (int j = 0; j < NT / 4; j++) bad |= e4m3_nan(vw[u][e][j]);
         bad = __any_sync(0xffffffffu, bad != 0);
       }
       if (bad) {
-#pragma unroll 1
-        for (int mt = 0; mt < MT; mt++) {
-          // rows x keys that are seen, as a matrix of ones, times keys x columns that are NaN
-          uint32_t one[4];
 #pragma unroll
-          for (int x = 0; x < 4; x++) {
-            const uint32_t b = (MT == 1 || mt == 0 ? bits[0][x & 1] : bits[MT - 1][x & 1]) >> ((x >> 1) * 8 + 2 * t4);
-            one[x] = (b & 1 ? 0x3c00u : 0u) | (b & 2 ? 0x3c000000u : 0u);
+        for (int u = 0; u < SUBS; u++) {
+#pragma unroll
+          for (int mt = 0; mt < MT; mt++) {
+            // rows x keys that are seen, as a matrix of ones, times keys x columns that are NaN
+            uint32_t one[4];
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+              const uint32_t b = bits[mt][x & 1] >> (u * 16 + (x >> 1) * 8 + 2 * t4);
+              one[x] = (b & 1 ? 0x3c00u : 0u) | (b & 2 ? 0x3c000000u : 0u);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+              auto ones = [&](uint32_t x, uint32_t y) {
+                return ((e4m3_nan(x) >> (8 * (j & 3) + 7)) & 1 ? 0x3c00u : 0u) | ((e4m3_nan(y) >> (8 * (j & 3) + 7)) & 1 ? 0x3c000000u : 0u);
+              };
+              float met[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816(met, one, ones(vw[u][0][j >> 2], vw[u][1][j >> 2]), ones(vw[u][2][j >> 2], vw[u][3][j >> 2]));
+#pragma unroll
+              for (int x = 0; x < 4; x++)
+                if (met[x] > 0.f) o[mt][j][x] = __int_as_float(0x7fffffff);
+            }
           }
 #pragma unroll
-          for (int j = 0; j < NT; j++) {
-            auto ones = [&](uint32_t x, uint32_t y) {
-              return ((e4m3_nan(x) >> (8 * (j & 3) + 7)) & 1 ? 0x3c00u : 0u) | ((e4m3_nan(y) >> (8 * (j & 3) + 7)) & 1 ? 0x3c000000u : 0u);
-            };
-            float met[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(met, one, ones(vw[0][j >> 2], vw[1][j >> 2]), ones(vw[2][j >> 2], vw[3][j >> 2]));
+          for (int e = 0; e < 4; e++)
 #pragma unroll
-            for (int x = 0; x < 4; x++)
-#pragma unroll
-              for (int y = 0; y < MT; y++)
-                if (met[x] > 0.f && y == mt) o[y][j][x] = __int_as_float(0x7fffffff);
-          }
+            for (int j = 0; j < NT / 4; j++) vw[u][e][j] &= ~((e4m3_nan(vw[u][e][j]) >> 7) * 255u);
         }
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-#pragma unroll
-          for (int j = 0; j < NT / 4; j++) vw[e][j] &= ~((e4m3_nan(vw[e][j]) >> 7) * 255u);
       }
 #pragma unroll
-      for (int j = 0; j < NT / 2; j++) {  // two columns: bytes 2 (j & 1), + 1 of word j / 2
-        const uint32_t pick = j & 1 ? 0x7362u : 0x5140u;
-        const uint32_t x = __byte_perm(vw[0][j >> 1], vw[1][j >> 1], pick), y = __byte_perm(vw[2][j >> 1], vw[3][j >> 1], pick);
-        const uint32_t b00 = e4m3_lo(x), b01 = e4m3_lo(y), b10 = e4m3_hi(x), b11 = e4m3_hi(y);
+      for (int u = 0; u < SUBS; u++) {
 #pragma unroll
-        for (int mt = 0; mt < MT; mt++) {
-          mma16816(o[mt][2 * j], w4[mt], b00, b01);
-          mma16816(o[mt][2 * j + 1], w4[mt], b10, b11);
+        for (int j = 0; j < NT / 2; j++) {  // two columns: bytes 2 (j & 1), + 1 of word j / 2
+          const uint32_t pick = j & 1 ? 0x7362u : 0x5140u;
+          const uint32_t x = __byte_perm(vw[u][0][j >> 1], vw[u][1][j >> 1], pick), y = __byte_perm(vw[u][2][j >> 1], vw[u][3][j >> 1], pick);
+          const uint32_t b00 = e4m3_lo(x), b01 = e4m3_lo(y), b10 = e4m3_hi(x), b11 = e4m3_hi(y);
+#pragma unroll
+          for (int mt = 0; mt < MT; mt++) {
+            mma16816(o[mt][2 * j], w4[mt][u], b00, b01);
+            mma16816(o[mt][2 * j + 1], w4[mt][u], b10, b11);
+          }
         }
       }
     }
 
     // ---- the warps' outputs become the piece's
-    const Piece done = p;
-    const int E_mine = E;
 #pragma unroll
     for (int mt = 0; mt < MT; mt++) {
 #pragma unroll
@@ -429,13 +478,13 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
         }
       }
     }
-    if (lane == 0) s_e[warp] = E_mine;
-    more = walk.next(a, p);
-    const bool whole = done.pieces == 1;
-    float* part = part8_at<D, ROWS>(a.part, me, done.lo == 0);
+    if (lane == 0) s_e[warp] = E;
+    if (warp != 0) asm volatile("bar.sync 1, %0;" ::"n"(A8_THREADS) : "memory");
+    const bool whole = p.pieces == 1;
+    float* part = part8_at<D, ROWS>(a.part, me, p.lo == 0);
 #pragma unroll
     for (int mt = 0; mt < MT; mt++) {
-      if (mt * 16 >= done.rows) break;
+      if (mt * 16 >= p.rows) break;
       // a thread has columns (2 t4) * NT .. and (2 t4 + 1) * NT .., which are neighbours
 #pragma unroll
       for (int half = 0; half < 2; half++) {
@@ -447,14 +496,14 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
             *reinterpret_cast<float4*>(dst + side * NT + j) =
                 make_float4(o[mt][j][2 * half + side], o[mt][j + 1][2 * half + side], o[mt][j + 2][2 * half + side], o[mt][j + 3][2 * half + side]);
       }
-      if (mt == 0 && more) start(p);
+      if (mt == 0 && nx.valid) start(nx);
       __syncthreads();
       int Emax = -1000;
 #pragma unroll
       for (int w = 0; w < A8_WARPS; w++) Emax = max(Emax, s_e[w]);
       for (int x = tid; x < 16 * (D / 4); x += A8_THREADS) {
         const int rr = x / (D / 4), col = (x % (D / 4)) * 4, all = mt * 16 + rr;
-        if (all >= done.rows) break;
+        if (all >= p.rows) break;
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < A8_WARPS; w++) top = fmaxf(top, s_m[all * A8_WARPS + w]);
@@ -478,8 +527,8 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
         y = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
         const float log2sum = none ? -INFINITY : (top == -INFINITY ? 0.f : top - A8_UP) + log2f(sum);
         if (whole) {
-          const int gr = done.row0 + all, tok = gr / a.group;
-          const int64_t at = (int64_t)(done.t0 + tok) * a.hq + done.h * a.group + (gr - tok * a.group);
+          const int gr = p.row0 + all, tok = gr / a.group;
+          const int64_t at = (int64_t)(p.t0 + tok) * a.hq + p.h * a.group + (gr - tok * a.group);
           *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * D + col) = make_uint2(pack2<T>(y.x, y.y), pack2<T>(y.z, y.w));
           if (a.lse && col == 0) a.lse[at] = log2sum * 0.69314718055994531f;
         } else {
@@ -489,32 +538,32 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
       }
       __syncthreads();  // the outputs have been read
     }
-    if (more) fetch(p);
+    if (nx.valid) fetch(nx);
     if (!whole) {
       // The last of a unit's pieces to be ready joins them, always in the same order.
       __threadfence();
       __syncthreads();
       if (tid == 0) {
-        const unsigned before = atomicAdd(a.counters + 2 * done.first, 1u);
-        *s_last = before == (unsigned)done.pieces - 1;
-        if (*s_last) a.counters[2 * done.first] = 0;  // all have come by
+        const unsigned before = atomicAdd(a.counters + 2 * p.first, 1u);
+        *s_last = before == (unsigned)p.pieces - 1;
+        if (*s_last) a.counters[2 * p.first] = 0;  // all have come by
         __threadfence();
       }
       __syncthreads();
       if (*s_last && !*abort) {
-        for (int x = tid; x < done.rows * (D / 4); x += A8_THREADS) {
+        for (int x = tid; x < p.rows * (D / 4); x += A8_THREADS) {
           const int rr = x / (D / 4), col = (x % (D / 4)) * 4;
           float top = -INFINITY, sum = 0.f;
           float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int j0 = 0; j0 < done.pieces; j0 += 8) {
+          for (int j0 = 0; j0 < p.pieces; j0 += 8) {
             float e[8];
             float4 z[8];
 #pragma unroll
             for (int j = 0; j < 8; j++) {
               const int pc = j0 + j;
-              const float* src = part8_at<D, ROWS>(a.part, done.first + pc, pc == 0);
-              e[j] = pc < done.pieces ? __ldcg(src + ROWS * D + rr) : -INFINITY;
-              z[j] = pc < done.pieces ? __ldcg(reinterpret_cast<const float4*>(src + rr * D + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
+              const float* src = part8_at<D, ROWS>(a.part, p.first + pc, pc == 0);
+              e[j] = pc < p.pieces ? __ldcg(src + ROWS * D + rr) : -INFINITY;
+              z[j] = pc < p.pieces ? __ldcg(reinterpret_cast<const float4*>(src + rr * D + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float up = top;
 #pragma unroll
@@ -535,8 +584,8 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
             }
           }
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          const int gr = done.row0 + rr, tok = gr / a.group;
-          const int64_t at = (int64_t)(done.t0 + tok) * a.hq + done.h * a.group + (gr - tok * a.group);
+          const int gr = p.row0 + rr, tok = gr / a.group;
+          const int64_t at = (int64_t)(p.t0 + tok) * a.hq + p.h * a.group + (gr - tok * a.group);
           *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * D + col) =
               make_uint2(pack2<T>(y.x * inv, y.y * inv), pack2<T>(y.z * inv, y.w * inv));
           if (a.lse && col == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
@@ -546,6 +595,7 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
     } else if (MT > 1) {
       __syncthreads();  // the queries are there
     }
+    cur ^= 1;
   }
   // given up: the copies in flight land before the CTA ends
   if (!ok)
