@@ -493,11 +493,11 @@ __global__ void __launch_bounds__(APPEND_THREADS, 5) k_kv_append(AppendArgs a) {
 //   stored = rn(y / scale'), older rows of a block whose scale grows: rn(e4m3 * scale / scale')
 // A power of two costs e4m3, which floats itself, no precision, and an older value that is scaled
 // down stays what it was unless it gets under e4m3's least normal one.
-// The rows of a block follow one another (tk_kv_plan's do): they are one run, and a run is one
-// CTA's for each head, keys and values, so that nothing is added up over CTAs and the
-// result does not go by their order. A CTA takes the runs that begin among `chunk` tokens. The rows are
-// read once more for the second pass unless one pass has them all (16 rows of up to 128
-// elements); they are then in L1 or L2, and a third of the heads at 4 query heads a key head.
+// The rows of a block follow one another (tk_kv_plan's do): they are one run, and a run is W warps' for each
+// head, keys and values, so that the result does not go by any order.  W = 4, a CTA: chunks of
+// prompts; 64 rows of up to 128 elements stay in registers between the search for the largest and the store, more are
+// read again.  W = 1: a decode step's few rows, each of which is a block's only one.  The runs of a warp or CTA
+// are those that begin among `chunk` tokens.
 struct Store8Args {
   AppendArgs a;  // its hk is 0: its heads are the queries
   int hk;
@@ -505,20 +505,113 @@ struct Store8Args {
   uint8_t* v;
   float* k_scale;
   float* v_scale;
-  int chunk;       // tokens of a CTA
-  int store_ctas;  // the CTAs after these have the queries
+  float per_dim;          // 1 / head_dim
+  int chunk;              // tokens
+  int store_ctas, every;  // CTAs 0, every, 2 every, .. store; the others have the queries
 };
-constexpr int STORE8_CHUNK = 64;  // most tokens of a CTA: its run starts are two words
+constexpr int STORE8_CHUNK = 32;  // most tokens: their starts are a word
 constexpr float STORE8_LEAST = 7.888609052210118e-31f;  // 2^-100, the scale of zeros
 
-// 8 elements -> e4m3, infinities as NaN (e4m3 has none)
-__device__ __forceinline__ uint2 to_e4m3(const float* y, float scale, float inv, bool pow2) {
+// What turns a lane's 16 elements, two runs of 8 of a head: z0 = x0 f00 + x1 f01, z1 = x1 f11 + x0 f10, or with the
+// neighbour in each run.  Gain and rotation of one token.
+template <bool NEIGHBOURS>
+struct Turn8 {
+  uint64_t f00[4], f01[4], f10[4], f11[4];
+  // gain: of the lane's elements e0.., e1.., or null; rope: the lane's 8 pairs, or null if it does not rotate
+  __device__ __forceinline__ void set(const float* gain, int e0, int e1, const float4* rope, bool known) {
+    float g0[8], g1[8];
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      const float4 x = gain ? __ldg(reinterpret_cast<const float4*>(gain + e0) + j) : make_float4(1.f, 1.f, 1.f, 1.f);
+      const float4 y = gain ? __ldg(reinterpret_cast<const float4*>(gain + e1) + j) : make_float4(1.f, 1.f, 1.f, 1.f);
+      g0[4 * j] = x.x; g0[4 * j + 1] = x.y; g0[4 * j + 2] = x.z; g0[4 * j + 3] = x.w;
+      g1[4 * j] = y.x; g1[4 * j + 1] = y.y; g1[4 * j + 2] = y.z; g1[4 * j + 3] = y.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      f00[j] = pair64(g0[2 * j], g0[2 * j + 1]);
+      f11[j] = pair64(g1[2 * j], g1[2 * j + 1]);
+    }
+    if (rope) {
+      float cs[8], sn[8];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        float4 f = __ldg(rope + j);
+        if (!known) f.x = f.y = f.z = f.w = __int_as_float(0x7fffffff);
+        cs[2 * j] = f.x; sn[2 * j] = f.y;
+        cs[2 * j + 1] = f.z; sn[2 * j + 1] = f.w;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        if (NEIGHBOURS) {  // run 0 has pairs 0-3, run 1 pairs 4-7
+          f00[j] = pair64(g0[2 * j] * cs[j], g0[2 * j + 1] * cs[j]);
+          f01[j] = pair64(-g0[2 * j + 1] * sn[j], g0[2 * j] * sn[j]);
+          f11[j] = pair64(g1[2 * j] * cs[4 + j], g1[2 * j + 1] * cs[4 + j]);
+          f10[j] = pair64(-g1[2 * j + 1] * sn[4 + j], g1[2 * j] * sn[4 + j]);
+        } else {
+          f00[j] = pair64(g0[2 * j] * cs[2 * j], g0[2 * j + 1] * cs[2 * j + 1]);
+          f01[j] = pair64(-g1[2 * j] * sn[2 * j], -g1[2 * j + 1] * sn[2 * j + 1]);
+          f11[j] = pair64(g1[2 * j] * cs[2 * j], g1[2 * j + 1] * cs[2 * j + 1]);
+          f10[j] = pair64(g0[2 * j] * sn[2 * j], g0[2 * j + 1] * sn[2 * j + 1]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void apply(uint64_t* x0, uint64_t* x1, bool rotated) const {
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      uint64_t z0 = mul2(x0[j], f00[j]), z1 = mul2(x1[j], f11[j]);
+      if (rotated) {
+        if (NEIGHBOURS) {
+          const float2 u = unpair64(x0[j]), v = unpair64(x1[j]);
+          z0 = fma2(pair64(u.y, u.x), f01[j], z0);
+          z1 = fma2(pair64(v.y, v.x), f10[j], z1);
+        } else {
+          z0 = fma2(x1[j], f01[j], z0);
+          z1 = fma2(x0[j], f10[j], z1);
+        }
+      }
+      x0[j] = z0;
+      x1[j] = z1;
+    }
+  }
+};
+// 16 bytes -> 8 elements
+template <class T>
+__device__ __forceinline__ void unpack8(uint4 w, uint64_t* x) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    const float2 f = Pair<T>::up(*reinterpret_cast<const typename Pair<T>::type*>(v + j));
+    x[j] = pair64(f.x, f.y);
+  }
+}
+// 1 / sqrt(mean square + eps) of the head that LANES lanes hold
+template <int LANES>
+__device__ __forceinline__ float norm8(const uint64_t* x0, const uint64_t* x1, bool in_dim, float per_dim, float eps) {
+  uint64_t ss = 0, ss2 = 0;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    ss = fma2(x0[j], x0[j], ss);
+    ss2 = fma2(x1[j], x1[j], ss2);
+  }
+  const float2 s2 = unpair64(add2(ss, ss2));
+  float s = in_dim ? s2.x + s2.y : 0.f;
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return rsqrtf(fmaf(s, per_dim, eps));
+}
+// 8 elements -> e4m3 of y * by; PLAIN: none is infinite (e4m3 has none: NaN) and 1 / scale is exact.
+template <bool PLAIN>
+__device__ __forceinline__ uint2 to_e4m3(const float* y, float by, float scale) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    float u = pow2 ? y[2 * i] * inv : __fdiv_rn(y[2 * i], scale), v = pow2 ? y[2 * i + 1] * inv : __fdiv_rn(y[2 * i + 1], scale);
-    if (!(fabsf(u) < INFINITY)) u = __int_as_float(0x7fffffff);
-    if (!(fabsf(v) < INFINITY)) v = __int_as_float(0x7fffffff);
+    float u = y[2 * i] * by, v = y[2 * i + 1] * by;
+    if (!PLAIN) {
+      u = fabsf(u) < INFINITY ? __fdiv_rn(u, scale) : __int_as_float(0x7fffffff);
+      v = fabsf(v) < INFINITY ? __fdiv_rn(v, scale) : __int_as_float(0x7fffffff);
+    }
     w[i] = __nv_cvt_float2_to_fp8x2(make_float2(u, v), __NV_SATFINITE, __NV_E4M3);
   }
   return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
@@ -534,179 +627,270 @@ __device__ __forceinline__ uint32_t rescale_e4m3(uint32_t w, float ratio) {
   return out;
 }
 
-template <class T, int LANES, bool NEIGHBOURS>
-__device__ __forceinline__ void store8_runs(const Store8Args& s) {
-  using P = Pair<T>;
-  using T2 = typename P::type;
-  constexpr int G = 32 / LANES, WARPS = APPEND_THREADS / 32, STEP = G * WARPS;  // rows of a pass
-  __shared__ uint32_t s_starts[STORE8_CHUNK / 32], s_placed[4], s_top;
-  __shared__ int s_rows;
+template <class T, int LANES, bool NEIGHBOURS, int W>
+__device__ __forceinline__ void store8_runs(const Store8Args& s, int cta) {
+  constexpr int G = 32 / LANES, STEP = W * G, BATCH = W == 1 ? 2 : 4, WARPS = APPEND_THREADS / 32;  // rows of a pass; passes held
+  constexpr uint32_t ALL = 0xffffffffu;
+  static_assert(W == 1 || W == WARPS, "a run is a warp's or a CTA's");
+  __shared__ float s_top[W];
   const AppendArgs& a = s.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % LANES, g = lane / LANES;
-  const int part = blockIdx.x % (2 * s.hk), h = part % s.hk;
-  const bool key = part < s.hk;
-  uint8_t* pool = (key ? s.k : s.v) + h * a.s_head;
-  float* scales = (key ? s.k_scale : s.v_scale) + h;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LANES, g = lane / LANES, sub = W == 1 ? 0 : warp;
+  const int item = W == 1 ? cta * WARPS + warp : cta, part = item % (2 * s.hk), h = part % s.hk;
+  const int64_t t_first = (int64_t)(item / (2 * s.hk)) * s.chunk;
+  if (t_first >= a.T) return;
   const int within = (1 << a.log2_bs) - 1;
-  const int64_t t_first = (int64_t)(blockIdx.x / (2 * s.hk)) * s.chunk;
-  auto block_of = [&](int64_t t) {  // -1: none
+  auto slot_of = [&](int64_t t) {  // -1: none
     if (t < 0 || t >= a.T) return (int64_t)-1;
     const int64_t x = a.slot[t];
-    return x >= 0 && x < a.n_slots ? x >> a.log2_bs : (int64_t)-1;
+    return x >= 0 && x < a.n_slots ? x : (int64_t)-1;
   };
-  if (tid < STORE8_CHUNK) {
-    const int64_t t = t_first + tid, b = tid < s.chunk ? block_of(t) : -1;
-    const uint32_t starts = __ballot_sync(0xffffffffu, b >= 0 && block_of(t - 1) != b);
-    if (lane == 0) s_starts[warp] = starts;
-  }
+  const int64_t mine = slot_of(t_first + lane), before = slot_of(t_first + lane - 1);
+  uint32_t starts = __ballot_sync(ALL, lane < s.chunk && mine >= 0 && mine >> a.log2_bs != before >> a.log2_bs);
 
   // the lane's elements, as append_rows has them
-  const bool turns = key && a.rot > 0, normed = key && a.k_gain;
+  const bool key = part < s.hk, normed = key && a.k_gain;
+  uint8_t* pool = (key ? s.k : s.v) + h * a.s_head;
+  float* scales = (key ? s.k_scale : s.v_scale) + h;
   const int half = a.rot >> 1;
-  const bool rotated = key && l * 16 < a.rot, in_dim = l * 16 < a.dim;
-  const bool apart = !NEIGHBOURS && rotated;
+  const bool in_dim = l * 16 < a.dim, turned = key && l * 16 < a.rot, apart = !NEIGHBOURS && turned;
   const int e0 = apart ? l * 8 : l * 16, e1 = apart ? e0 + half : e0 + 8;
   const T* src = static_cast<const T*>(a.qkv) + (int64_t)(a.hq + part) * a.dim;
-  float g0[8], g1[8];
+  uint4 raw[BATCH][2];
+  int32_t pos[BATCH];
+  float y[BATCH][16], inv[BATCH];
+  auto load = [&](int64_t t0, int r0, int rows) {
 #pragma unroll
-  for (int j = 0; j < 8; j++) {
-    g0[j] = normed && in_dim ? __ldg(a.k_gain + e0 + j) : 1.f;
-    g1[j] = normed && in_dim ? __ldg(a.k_gain + e1 + j) : 1.f;
-  }
-  // normed and rotated elements of token t, of which there is one if `in`
-  auto row = [&](int64_t t, bool in, float* y0, float* y1) {
-    union Vec {
-      uint4 u;
-      T2 p[4];
-    } x0, x1;
-    x0.u = x1.u = make_uint4(0, 0, 0, 0);
-    if (in && in_dim) {
-      x0.u = __ldg(reinterpret_cast<const uint4*>(src + t * a.row_stride + e0));
-      x1.u = __ldg(reinterpret_cast<const uint4*>(src + t * a.row_stride + e1));
-    }
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const float2 u = P::up(x0.p[j]), v = P::up(x1.p[j]);
-      y0[2 * j] = u.x; y0[2 * j + 1] = u.y;
-      y1[2 * j] = v.x; y1[2 * j + 1] = v.y;
-    }
-    if (normed) {
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; j++) ss = fmaf(y0[j], y0[j], fmaf(y1[j], y1[j], ss));
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float inv = rsqrtf(ss / (float)a.dim + a.eps);
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        y0[j] *= inv * g0[j];
-        y1[j] *= inv * g1[j];
+    for (int k = 0; k < BATCH; k++) {
+      const int r = r0 + k * STEP + sub * G + g;
+      raw[k][0] = raw[k][1] = make_uint4(0, 0, 0, 0);
+      pos[k] = -1;
+      if (r < rows && in_dim) {
+        if (turned) pos[k] = a.pos[t0 + r];
+        raw[k][0] = __ldg(reinterpret_cast<const uint4*>(src + (t0 + r) * a.row_stride + e0));
+        raw[k][1] = __ldg(reinterpret_cast<const uint4*>(src + (t0 + r) * a.row_stride + e1));
       }
     }
-    if (turns && rotated && in) {
-      const int64_t p = a.pos[t];
-      const bool known = p >= 0 && p < a.rope_len;
-      const float4* rope = reinterpret_cast<const float4*>(a.rope + ((known ? p : 0) * half + l * 8) * 2);
+  };
+  // the rows that were loaded, normed but for the factor inv, and rotated
+  auto turn = [&](int r0, int rows) {
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        float4 f = __ldg(rope + j);
-        if (!known) f.x = f.y = f.z = f.w = __int_as_float(0x7fffffff);
-        auto turn = [](float& u, float& v, float c, float sn) {
-          const float x = u;
-          u = u * c - v * sn;
-          v = v * c + x * sn;
-        };
-        if (NEIGHBOURS) {
-          float* y = j < 2 ? y0 : y1;
-          turn(y[4 * (j & 1)], y[4 * (j & 1) + 1], f.x, f.y);
-          turn(y[4 * (j & 1) + 2], y[4 * (j & 1) + 3], f.z, f.w);
-        } else {
-          turn(y0[2 * j], y1[2 * j], f.x, f.y);
-          turn(y0[2 * j + 1], y1[2 * j + 1], f.z, f.w);
+    for (int k = 0; k < BATCH; k++) {
+      if (r0 + k * STEP >= rows) break;
+      uint64_t x[8];
+      unpack8<T>(raw[k][0], x);
+      unpack8<T>(raw[k][1], x + 4);
+      inv[k] = normed ? norm8<LANES>(x, x + 4, in_dim, s.per_dim, a.eps) : 1.f;
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const float2 u = unpair64(x[j]);
+        y[k][2 * j] = u.x;
+        y[k][2 * j + 1] = u.y;
+      }
+      if (normed && in_dim) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const float4 u = __ldg(reinterpret_cast<const float4*>(a.k_gain + (j < 2 ? e0 : e1)) + (j & 1));
+          y[k][4 * j] *= u.x; y[k][4 * j + 1] *= u.y; y[k][4 * j + 2] *= u.z; y[k][4 * j + 3] *= u.w;
+        }
+      }
+      if (turned) {
+        const bool known = pos[k] >= 0 && pos[k] < a.rope_len;
+        const float4* rope = reinterpret_cast<const float4*>(a.rope + ((int64_t)(known ? pos[k] : 0) * half + l * 8) * 2);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          float4 f = __ldg(rope + j);
+          if (!known) f.x = f.y = f.z = f.w = __int_as_float(0x7fffffff);
+          auto by = [](float& u, float& v, float c, float sn) {
+            const float z = u;
+            u = u * c - v * sn;
+            v = v * c + z * sn;
+          };
+          float* z = y[k];
+          if (NEIGHBOURS) {
+            by(z[4 * j], z[4 * j + 1], f.x, f.y);
+            by(z[4 * j + 2], z[4 * j + 3], f.z, f.w);
+          } else {
+            by(z[2 * j], z[8 + 2 * j], f.x, f.y);
+            by(z[2 * j + 1], z[8 + 2 * j + 1], f.z, f.w);
+          }
         }
       }
     }
   };
-  auto top_of = [&](const float* y0, const float* y1) {
+  auto largest = [](const float* z) {  // NaN do not count
     float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-      const float u = fabsf(y0[j]), v = fabsf(y1[j]);
-      if (u < INFINITY) m = fmaxf(m, u);
-      if (v < INFINITY) m = fmaxf(m, v);
-    }
+    for (int j = 0; j < 16; j += 2) m = max3(m, fabsf(z[j]), fabsf(z[j + 1]));
     return m;
   };
 
-  __syncthreads();
 #pragma unroll 1
-  for (int i = 0; i < s.chunk; i++) {
-    if (!((s_starts[i >> 5] >> (i & 31)) & 1)) continue;
-    const int64_t t0 = t_first + i, b = a.slot[t0] >> a.log2_bs;
+  for (; starts; starts &= starts - 1) {
+    const int first = __ffs(starts) - 1;
+    const int64_t t0 = t_first + first, slot0 = __shfl_sync(ALL, mine, first), b = slot0 >> a.log2_bs;
     const float old = scales[b * s.hk];
-    __syncthreads();  // the last run's shared words have been read
-    if (tid < 4) s_placed[tid] = 0;
-    if (tid == 0) {
-      s_top = 0;
-      s_rows = INT32_MAX;
-    }
-    __syncthreads();
+    // A run of a prompt goes on to the block's end or the request's: up to there rows are on their way before the slots
+    // have told how many they are.
+    if (W > 1) load(t0, 0, (int)min((int64_t)(within + 1 - (slot0 & within)), a.T - t0));
     // the run's rows and places
-    for (int64_t n = 0;; n += APPEND_THREADS) {
-      const bool in = block_of(t0 + n + tid) == b;
-      const uint32_t out = __ballot_sync(0xffffffffu, !in);
-      if (out && lane == 0) atomicMin(&s_rows, (int)min(n + warp * 32 + __ffs(out) - 1, (int64_t)INT32_MAX - 1));
-      if (__syncthreads_or(out != 0)) break;
+    int rows = 0;
+    uint32_t placed[4] = {0, 0, 0, 0};
+    for (uint32_t in = ALL; in == ALL; ) {
+      const int64_t x = slot_of(t0 + rows + lane);
+      in = __ballot_sync(ALL, (x >> a.log2_bs) == b);
+      const int n = in == ALL ? 32 : __ffs(~in) - 1, place = (int)(x & within);
+      rows += n;
+#pragma unroll
+      for (int i = 0; i < 4; i++) placed[i] |= __reduce_or_sync(ALL, lane < n && place >> 5 == i ? 1u << (place & 31) : 0u);
     }
-    const int rows = s_rows;
-    for (int r = tid; r < rows; r += APPEND_THREADS) {
-      const int place = (int)(a.slot[t0 + r] & within);
-      atomicOr(&s_placed[place >> 5], 1u << (place & 31));
-    }
-    float y0[8], y1[8], m = 0.f;
-    for (int r = warp * G; r < rows; r += STEP) {
-      row(t0 + r + g, r + g < rows, y0, y1);
-      m = fmaxf(m, top_of(y0, y1));
-    }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    if (lane == 0 && top) atomicMax(&s_top, top);
-    __syncthreads();
-    const bool begun = s_placed[0] & 1;
-    // 448 = 1.75 2^8
-    const int e = (int)(s_top >> 23) - 8 + ((s_top & 0x7fffff) > 0x600000);
-    const float need = e < 27 ? STORE8_LEAST : __uint_as_float((uint32_t)e << 23);
-    const float scale = begun ? need : fmaxf(need, old);
-    const bool pow2 = (__float_as_uint(scale) & 0x7fffff) == 0;
-    const float inv = 1.f / scale;
-    uint8_t* to = pool + b * a.s_block;
-    for (int r = warp * G; r < rows; r += STEP) {
-      if (rows > STEP) row(t0 + r + g, r + g < rows, y0, y1);
-      if (r + g < rows && in_dim) {
-        uint8_t* dst = to + (a.slot[t0 + r + g] & within) * a.s_token;
-        *reinterpret_cast<uint2*>(dst + e0) = to_e4m3(y0, scale, inv, pow2);
-        *reinterpret_cast<uint2*>(dst + e1) = to_e4m3(y1, scale, inv, pow2);
+    // (rows that did not come in ahead: a run may be longer if its places do not ascend)
+    const bool again = rows > BATCH * STEP || W == 1 || rows > within + 1 - (int)(slot0 & within);
+    float m = 0.f;
+    for (int r0 = 0; r0 < rows; r0 += BATCH * STEP) {
+      if (again) load(t0, r0, rows);
+      turn(r0, rows);
+#pragma unroll
+      for (int k = 0; k < BATCH; k++) {
+        if (r0 + k * STEP + sub * G + g >= rows) break;
+        float x = largest(y[k]) * inv[k];
+        if (!(x < INFINITY)) {  // nor do infinities
+          x = 0.f;
+#pragma unroll
+          for (int j = 0; j < 16; j++) {
+            const float z = fabsf(y[k][j] * inv[k]);
+            if (z < INFINITY) x = fmaxf(x, z);
+          }
+        }
+        m = fmaxf(m, x);
       }
     }
+    uint32_t top = __reduce_max_sync(ALL, __float_as_uint(m));
+    if (W > 1) {
+      if (lane == 0) s_top[sub] = __uint_as_float(top);
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < W; w++) top = max(top, __float_as_uint(s_top[w]));
+    }
+    const bool begun = placed[0] & 1;
+    // 448 = 1.75 2^8
+    const int e = (int)(top >> 23) - 8 + ((top & 0x7fffff) > 0x600000);
+    const float need = e < 27 ? STORE8_LEAST : __uint_as_float((uint32_t)e << 23);
+    const float scale = begun ? need : fmaxf(need, old), per_scale = 1.f / scale;
+    const bool pow2 = (__float_as_uint(scale) & 0x7fffff) == 0;
+    uint8_t* to = pool + b * a.s_block;
+    for (int r0 = 0; r0 < rows; r0 += BATCH * STEP) {
+      if (rows > BATCH * STEP) {
+        load(t0, r0, rows);
+        turn(r0, rows);
+      }
+#pragma unroll
+      for (int k = 0; k < BATCH; k++) {
+        const int r = r0 + k * STEP + sub * G + g;
+        if (r >= rows || !in_dim) break;
+        uint8_t* dst = to + (a.slot[t0 + r] & within) * a.s_token;
+        const float by = inv[k] * per_scale;
+        // exact if the scale is a power of two and the factor a normal number
+        if (pow2 && by >= 1.17549435e-38f && largest(y[k]) * inv[k] < INFINITY) {
+          *reinterpret_cast<uint2*>(dst + e0) = to_e4m3<true>(y[k], by, 1.f);
+          *reinterpret_cast<uint2*>(dst + e1) = to_e4m3<true>(y[k] + 8, by, 1.f);
+        } else {
+          *reinterpret_cast<uint2*>(dst + e0) = to_e4m3<false>(y[k], inv[k], scale);
+          *reinterpret_cast<uint2*>(dst + e1) = to_e4m3<false>(y[k] + 8, inv[k], scale);
+        }
+      }
+    }
+    // older rows of a block whose scale has grown
     if (!begun && scale != old) {
       const float ratio = old / scale;
-      const int chunks = a.dim / 16;
-      for (int x = tid; x < (within + 1) * chunks; x += APPEND_THREADS) {
-        const int place = x / chunks;
-        if ((s_placed[place >> 5] >> (place & 31)) & 1) continue;
-        uint4* at = reinterpret_cast<uint4*>(to + place * a.s_token + (x - place * chunks) * 16);
-        const uint4 w = *at;
-        *at = make_uint4(rescale_e4m3(w.x, ratio), rescale_e4m3(w.y, ratio), rescale_e4m3(w.z, ratio), rescale_e4m3(w.w, ratio));
+#pragma unroll 1
+      for (int place = sub * G + g; place <= within; place += STEP) {
+        const int word = place >> 5;
+        const uint32_t there = word == 0 ? placed[0] : word == 1 ? placed[1] : word == 2 ? placed[2] : placed[3];
+        if ((there >> (place & 31)) & 1 || !in_dim) continue;
+        uint4* at = reinterpret_cast<uint4*>(to + place * a.s_token + l * 16);
+        const uint4 z = *at;
+        *at = make_uint4(rescale_e4m3(z.x, ratio), rescale_e4m3(z.y, ratio), rescale_e4m3(z.z, ratio), rescale_e4m3(z.w, ratio));
       }
     }
-    if (tid == 0) scales[b * s.hk] = scale;  // all have read the old one
+    if (W > 1) __syncthreads();  // all have read s_top and the old scale
+    if (sub == 0 && lane == 0) scales[b * s.hk] = scale;
   }
 }
 
+// The queries, as append_rows does them (a third of its instructions, which bound it: 79.6 M for 32k rows of 32 heads).
 template <class T, int LANES, bool NEIGHBOURS>
-__global__ void __launch_bounds__(APPEND_THREADS, 5) k_kv_append8(Store8Args s) {
+__device__ __forceinline__ void store8_queries(const Store8Args& s, uint4 (*s_x)[APPEND_FLIGHT][2][32], int cta) {
+  constexpr int G = 32 / LANES;
+  const AppendArgs& a = s.a;
+  const int lane = threadIdx.x & 31, l = lane % LANES, g = lane / LANES;
+  const int64_t w = ((int64_t)cta * APPEND_THREADS + threadIdx.x) >> 5, t = w / a.chunks;
+  if (t >= a.T) return;
+  const int half = a.rot >> 1;
+  const bool in_dim = l * 16 < a.dim, turned = l * 16 < a.rot, apart = !NEIGHBOURS && turned;
+  const int e0 = apart ? l * 8 : l * 16, e1 = apart ? e0 + half : e0 + 8;
+  const int first = (int)(w - t * a.chunks) * a.passes, last = min(first + a.passes, (a.hq + G - 1) / G);
+  uint4(*mine)[2][32] = s_x[threadIdx.x >> 5];
+  const int at = (first * G + g) * a.dim;
+  const T* src = static_cast<const T*>(a.qkv) + t * a.row_stride + at;
+  T* dst = static_cast<T*>(a.q) + t * a.hq * a.dim + at;
+  const bool some = in_dim && first * G + g < a.hq;
+  int heads = some ? a.hq - first * G - g : 0;  // from this pass's on
+  int ahead = heads;
+  uint32_t slot = 0;
+  const uint32_t s_mine = smem_addr(&mine[0][0][lane]);
+  auto fetch = [&](uint32_t into) {
+    if (ahead > 0) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s_mine + into * 1024), "l"(src + e0) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s_mine + into * 1024 + 512), "l"(src + e1) : "memory");
+    }
+    src += G * a.dim;
+    ahead -= G;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (last < first + a.passes) ahead = min(ahead, (last - first) * G);
+  else ahead = min(ahead, a.passes * G);
+#pragma unroll
+  for (uint32_t i = 0; i < APPEND_FLIGHT; i++) fetch(i);
+  Turn8<NEIGHBOURS> turn;
+  {
+    const int64_t p = turned ? a.pos[t] : 0;
+    const bool known = p >= 0 && p < a.rope_len;
+    turn.set(in_dim ? a.q_gain : nullptr, e0, e1, turned ? reinterpret_cast<const float4*>(a.rope + ((known ? p : 0) * half + l * 8) * 2) : nullptr, known);
+  }
+#pragma unroll 1
+  for (int p = first; p < last; p++) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(APPEND_FLIGHT - 1) : "memory");
+    uint64_t x0[4], x1[4];
+    unpack8<T>(mine[slot][0][lane], x0);
+    unpack8<T>(mine[slot][1][lane], x1);
+    fetch(slot);
+    slot = (slot + 1) % APPEND_FLIGHT;
+    const float inv = a.q_gain ? norm8<LANES>(x0, x1, in_dim, s.per_dim, a.eps) : 1.f;
+    turn.apply(x0, x1, turned);
+    if (heads > 0) {
+      const uint64_t inv2 = pair64(inv, inv);
+      uint32_t y[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const float2 u = unpair64(mul2(j < 4 ? x0[j] : x1[j - 4], inv2));
+        const typename Pair<T>::type z = Pair<T>::down(u.x, u.y);
+        y[j] = *reinterpret_cast<const uint32_t*>(&z);
+      }
+      *reinterpret_cast<uint4*>(dst + e0) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(dst + e1) = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+    dst += G * a.dim;
+    heads -= G;
+  }
+}
+
+template <class T, int LANES, bool NEIGHBOURS, int W>
+__global__ void __launch_bounds__(APPEND_THREADS, W == 1 ? 5 : 4) k_kv_append8(Store8Args s) {
   __shared__ uint4 s_x[APPEND_THREADS / 32][APPEND_FLIGHT][2][32];
-  if (blockIdx.x < s.store_ctas) store8_runs<T, LANES, NEIGHBOURS>(s);
-  else append_rows<T, LANES, NEIGHBOURS>(s.a, s_x, blockIdx.x - s.store_ctas);
+  // the two kinds alternate: runs wait for one load after the other, the queries' rows for memory alone
+  const int stores = min((int)((blockIdx.x + s.every - 1) / s.every), s.store_ctas);  // before this one
+  if (blockIdx.x % s.every == 0 && stores < s.store_ctas) store8_runs<T, LANES, NEIGHBOURS, W>(s, stores);
+  else store8_queries<T, LANES, NEIGHBOURS>(s, s_x, blockIdx.x - stores);
 }
 
 template <class T, int LANES>
@@ -724,11 +908,24 @@ static unsigned append_split(AppendArgs& a, int sms) {
 template <class T, int LANES>
 static void append8_launch(Store8Args& s, bool neighbours, int sms, cudaStream_t st) {
   const unsigned grid = append_split<T, LANES>(s.a, sms);
-  // a CTA for every token while that is no more than 16 for each SM
-  s.chunk = (int)std::max<int64_t>(1, std::min<int64_t>(STORE8_CHUNK, s.a.T * 2 * s.hk / ((int64_t)sms * 16)));
-  s.store_ctas = (int)((s.a.T + s.chunk - 1) / s.chunk) * 2 * s.hk;
-  if (neighbours) k_kv_append8<T, LANES, true><<<s.store_ctas + grid, APPEND_THREADS, 0, st>>>(s);
-  else k_kv_append8<T, LANES, false><<<s.store_ctas + grid, APPEND_THREADS, 0, st>>>(s);
+  const int64_t enough = (int64_t)sms * 16;
+  auto launch = [&](auto kernel, int warps) {
+    const int64_t items = (s.a.T + s.chunk - 1) / s.chunk * 2 * s.hk;
+    s.store_ctas = (int)((items * warps * 32 + APPEND_THREADS - 1) / APPEND_THREADS);
+    s.every = (s.store_ctas + grid) / s.store_ctas;
+    kernel<<<s.store_ctas + grid, APPEND_THREADS, 0, st>>>(s);
+  };
+  // A warp for every token and head while that is no more than 16 for each SM twice over: a decode step.  More tokens
+  // are taken for chunks of prompts, whose runs are longer.
+  if (s.a.T * s.hk <= enough) {
+    s.chunk = 1;
+    if (neighbours) launch(k_kv_append8<T, LANES, true, 1>, 1);
+    else launch(k_kv_append8<T, LANES, false, 1>, 1);
+  } else {
+    s.chunk = (int)std::max<int64_t>(1, std::min<int64_t>(STORE8_CHUNK, s.a.T * 2 * s.hk / enough));
+    if (neighbours) launch(k_kv_append8<T, LANES, true, 4>, 4);
+    else launch(k_kv_append8<T, LANES, false, 4>, 4);
+  }
 }
 
 template <class T>
@@ -930,7 +1127,7 @@ extern "C" int tk_kv_append(const tk_kv_cache* cache, const void* d_qkv, int64_t
     a.hk = 0;
     a.k = a.v = nullptr;
     Store8Args s = {a, cache->n_heads, static_cast<uint8_t*>(cache->k), static_cast<uint8_t*>(cache->v), cache->k_scale,
-                    cache->v_scale, 0, 0};
+                    cache->v_scale, 1.f / cache->head_dim, 1, 0, 1};
     if (cache->type == TK_BF16) append8_lanes<__nv_bfloat16>(s, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);
     else append8_lanes<__half>(s, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);
   } else if (cache->type == TK_BF16) append_lanes<__nv_bfloat16>(a, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);
