@@ -96,7 +96,7 @@ struct AttendShape {
   static constexpr int N_BARS = RINGS * (2 * STAGES + 2 * AT_PIECES) + 2 * 10 + RINGS * 2 * RAWS;  // and full and empty of the raw stages
   static constexpr int RAW_BARS = BARS + 8 * (RINGS * (2 * STAGES + 2 * AT_PIECES) + 2 * 10);
   static constexpr int PIECES = BARS + 8 * N_BARS;
-  // scales of a tile's groups, keys' and values'; more tiles than are on their way
+  // scales of a tile's groups, keys' and log2 of values'; more tiles than are on their way
   static constexpr int GROUPS = KEYS / 16, SCALED = 16;
   static constexpr int SCALES = PIECES + RINGS * AT_PIECES * (int)sizeof(Piece);
   static constexpr int SMALL = SCALES + (E8 ? RINGS * SCALED * GROUPS * 8 : 0);
@@ -261,9 +261,9 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       auto at_key = [&](int tile) { return WIN && tile >= head ? tile + skip : tile; };  // in tiles from key 0 on
       auto id_of = [&](int b) { return b < boxes ? __ldg(row + (b >> per_page)) : 0; };
       auto scale_of = [&](int id) {
-        if (id < 0 || id >= a.n_blocks) return make_float2(0.f, 0.f);
+        if (id < 0 || id >= a.n_blocks) return make_float2(0.f, -INFINITY);
         const int64_t at = (int64_t)id * a.hk + h;
-        return make_float2(__ldg(a.k_scale + at), __ldg(a.v_scale + at));
+        return make_float2(__ldg(a.k_scale + at), log2f(__ldg(a.v_scale + at)));
       };
       auto load = [&](const CUtensorMap* map, Ids& ids, int tile, bool keys) {
         const int box0 = at_key(tile) * ppt;
@@ -283,7 +283,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         if (E8 && keys) {
           const float ks = __shfl_sync(0xffffffffu, ids.scale.x, (box0 + my_box) & 31),
                       vs = __shfl_sync(0xffffffffu, ids.scale.y, (box0 + my_box) & 31);
-          if (my_box < L::GROUPS) s_scale[(scaled % L::SCALED) * L::GROUPS + my_box] = my_box < nb ? make_float2(ks, vs) : make_float2(0.f, 0.f);
+          if (my_box < L::GROUPS) s_scale[(scaled % L::SCALED) * L::GROUPS + my_box] = my_box < nb ? make_float2(ks, vs) : make_float2(0.f, -INFINITY);
           scaled++;
           __syncwarp();
         }
@@ -387,9 +387,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           advance();
           const uint32_t sk = st;
           const bool more = t + BUFS < n;
+          // (E8: these keys may be turned into fp16 only where the last tile's values were)
           if (more) {
-            if (!(ok = full())) break;
-            advance();
+            if (!E8 && !(ok = full())) break;
+            if (!E8) advance();
           }
           const uint32_t v = mma_desc(s_ring + sv * L::STAGE, KEYS * 128);
           if (!(ok = wait(b_p + 8 * buf, (nt / BUFS) & 1))) break;
@@ -403,10 +404,20 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
             mma_commit(b_v);
             mma_commit(b_empty + 8 * sv);
             if (t == n - 1) mma_commit(b_o);
-            if (more) scores(buf, sk);
-            if (turn) bar_arrive(b_turn);
+            if (!E8 && more) scores(buf, sk);
+            if (turn && !(E8 && more)) bar_arrive(b_turn);
           }
           __syncwarp();
+          if (E8 && more) {
+            if (!(ok = full())) break;
+            advance();
+            tmem_fence_after();
+            if (elect_one()) {
+              scores(buf, sk);
+              if (turn) bar_arrive(b_turn);
+            }
+            __syncwarp();
+          }
         }
         units++;
       }
@@ -570,7 +581,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       float m = -INFINITY, mc = 0.f, l = 0.f, l_full = 0.f;  // mc = m c - UP, or 0 while the row has seen nothing
       const int lo = p.lo;
       const uint64_t c2 = pair64(c, c);
-      int E = -1000;  // E8
+      float E = -1000.f;  // E8
 
       // of the scores of a group; with the least normal number a hidden key's -infinity stays that
       const float cq = c * qs, unit = E8 ? 1.f : c;
@@ -648,7 +659,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           [[maybe_unused]] const float2* scales = s_scale + ((scaled0 + t) % L::SCALED) * L::GROUPS;
           if constexpr (E8) {
             mx = -INFINITY;
-            float largest = 0.f;
+            float largest = -INFINITY;
 #pragma unroll
             for (int g = 0; g < L::GROUPS; g++) {
               float x = max3(__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1]), __uint_as_float(s[16 * g + 2]));
@@ -662,9 +673,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
               mx = fmaxf(mx, x * factor(scales[g].x));
               largest = fmaxf(largest, scales[g].y);
             }
-            const int e = largest > 0.f ? (int)((__float_as_uint(largest) >> 23) & 255) - 126 : -1000;
-            if (e > E) {
-              shrink = E < -500 ? 0.f : exp2f((float)(E - e));
+            // a whole number above every log2 of a scale so far
+            if (largest >= E) {
+              const float e = floorf(largest) + 1.f;
+              shrink = E < -500.f ? 0.f : exp2f(E - e);
               E = e;
             }
           } else {
@@ -702,30 +714,30 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           }
           const uint64_t mc2 = pair64(-mc, -mc);
           if constexpr (E8) {
-            uint64_t full[4] = {0, 0, 0, 0};
-            // 2^-E in two factors: it may be below the least normal number
-            const float down = E < -500 ? 0.f : __uint_as_float((uint32_t)(127 - E / 2) << 23),
-                        down2 = E < -500 ? 0.f : __uint_as_float((uint32_t)(127 - (E - E / 2)) << 23);
+            // w = p vs 2^-E = 2^(x - m + 7 + v), v = log2(vs) - E; p itself is a group's sum of w times 2^-v.  With v at
+            // least -60 nothing is left of w in fp16, and all of it in fp32.
+            float all[2] = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < KEYS / 64; i++) {
               uint32_t w[32];
 #pragma unroll
               for (int g = 0; g < 4; g++) {
-                const float f = factor(scales[4 * i + g].x), vn = scales[4 * i + g].y * down * down2;
-                const uint64_t f2 = pair64(f, f), vn2 = pair64(vn, vn);
+                const float f = factor(scales[4 * i + g].x), v = fmaxf(scales[4 * i + g].y - E, -60.f);
+                const uint64_t f2 = pair64(f, f), to = pair64(v - mc, v - mc);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int e = 8 * g; e < 8 * g + 8; e++) {
-                  const float2 x = unpair64(fma2(pair64(s[64 * i + 2 * e], s[64 * i + 2 * e + 1]), f2, mc2));
-                  const uint64_t p2 = pair64(exp2_fast(x.x), exp2_fast(x.y));
-                  full[e & 3] = add2(full[e & 3], p2);
-                  const float2 y = unpair64(mul2(p2, vn2));
-                  w[e] = pack2<__half>(y.x, y.y);
+                  const float2 x = unpair64(fma2(pair64(s[64 * i + 2 * e], s[64 * i + 2 * e + 1]), f2, to));
+                  const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
+                  sum[e & 1] = add2(sum[e & 1], pair64(p0, p1));
+                  w[e] = pack2<__half>(p0, p1);
                 }
+                const float2 sum2 = unpair64(add2(sum[0], sum[1]));
+                all[g & 1] = fmaf(sum2.x + sum2.y, exp2_fast(-v), all[g & 1]);
               }
               tmem_st32(t_s + buf * KEYS + 32 * i, w);
             }
-            const float2 l2 = unpair64(add2(add2(full[0], full[1]), add2(full[2], full[3])));
-            l += l2.x + l2.y;
+            l += all[0] + all[1];
           } else {
             float sum[4] = {0.f, 0.f, 0.f, 0.f};  // of the rounded weights, which the product has
             uint64_t full[2] = {0, 0};            // of the weights
@@ -780,7 +792,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       float* part = part_at<D>(a.part, me, p.lo == 0);
       const int64_t o_at = (int64_t)(p.t0 + tok) * a.hq + p.h * a.group + (gr - tok * a.group);
       if (active) {
-        const float inv = l == 0.f ? 0.f : (E8 ? exp2f((float)max(E, -140)) : 1.f) / l;
+        const float inv = l == 0.f ? 0.f : (E8 ? exp2f(fmaxf(E, -140.f)) : 1.f) / l;
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t x[32];
