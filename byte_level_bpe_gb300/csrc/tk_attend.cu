@@ -103,7 +103,8 @@ static int kv_attend(const char* where, const tk_kv_cache* cache, tk_kv_workspac
   AttendArgs a = {d_q, q_stride, n_q_heads, cache->n_heads, group, d_off, R, T, max_new, d_len, d_table, table_stride,
                   table_width, d_mask, scale * 1.4426950408889634f, d_out, d_lse, ws->status,
                   cache->v, cache->n_blocks, cache->stride[0], cache->stride[1],
-                  cache->stride[2], cache->log2_block, ws->part, ws->counters, window, sinks, cache->k_scale, cache->v_scale};
+                  cache->stride[2], cache->log2_block, ws->part, ws->counters, window, sinks, cache->k_scale, cache->v_scale,
+                  group == 1 ? 0 : UINT64_MAX / group + 1};
   cudaStream_t st = (cudaStream_t)cuda_stream;
   const int64_t rows = std::min(max_new, T) * group;  // of a request and key head
   const cudaError_t e = cache->k_scale ? attend8(a, cache, rows, ws->sms, st)

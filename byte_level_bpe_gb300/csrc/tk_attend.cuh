@@ -28,7 +28,11 @@ struct AttendArgs {
   int window, sinks;   // tilings with WIN: a token sees the `window` places up to its own, and the first `sinks`
   const float* k_scale;  // of a cache in 8 bits
   const float* v_scale;
+  uint64_t per_group;  // 2^64 / group rounded up, 0 for a group of 1
 };
+
+// x / a.group, x from 0 on: 2^64 / group is off by less than 1, so x times it by less than 2^32.
+__device__ __forceinline__ int by_group(const AttendArgs& a, int x) { return a.per_group ? (int)__umul64hi((uint64_t)x, a.per_group) : x; }
 
 // A request as the schedule sees it.
 struct Request {
@@ -75,9 +79,9 @@ template <class S>
 __device__ __forceinline__ Span unit_span(const AttendArgs& a, const Request& q, int row0) {
   Span x = {q.len, 0, 0};
   if (!q.good) return x;
-  if (!a.mask) x.keys = q.ctx + (min(q.n * a.group, row0 + S::ROWS) - 1) / a.group + 1;
+  if (!a.mask) x.keys = q.ctx + by_group(a, min(q.n * a.group, row0 + S::ROWS) - 1) + 1;
   if (S::WIN) {
-    const int low = q.ctx + (a.mask ? 0 : row0 / a.group) + 1 - a.window;
+    const int low = q.ctx + (a.mask ? 0 : by_group(a, row0)) + 1 - a.window;
     x.head = (a.sinks + S::STEP - 1) / S::STEP;
     x.skip = max(0, low / S::STEP - x.head);
   }
@@ -108,19 +112,30 @@ struct Plan {
 struct UnitSum {
   int length, units, longest;
 };
-template <class S>
+// Of LANES neighbouring lanes that share the request, each some of its row tiles; all get the sum.
+template <class S, int LANES>
 __device__ __forceinline__ UnitSum request_work(const AttendArgs& a, const Request& q, const Plan& plan) {
   UnitSum w = {0, 0, 0};
   int64_t length = 0;
-  const int rows = q.n * a.group;
+  const int rows = q.n * a.group, lane = threadIdx.x % LANES;
   const bool same = a.mask || !q.good || rows <= S::ROWS;  // every row tile has the request's keys
-  for (int row0 = 0; row0 < rows; row0 += S::ROWS) {
-    const int cost = span_tiles<S>(unit_span<S>(a, q, row0)) + S::UNIT_COST;
+  for (int64_t row0 = (int64_t)lane * S::ROWS; row0 < rows; row0 += LANES * S::ROWS) {
+    const int cost = span_tiles<S>(unit_span<S>(a, q, (int)row0)) + S::UNIT_COST;
     const int tiles = same ? (rows + S::ROWS - 1) / S::ROWS : 1;
     length += (int64_t)(plan.padded ? ((unsigned)(cost + plan.share - 1) / (unsigned)plan.share) * plan.share : cost) * tiles;
     w.units += tiles;
     w.longest = max(w.longest, cost);
     if (same) break;
+  }
+  if (same && lane > 0) {  // the first lane has them all
+    length = 0;
+    w = {0, 0, 0};
+  }
+#pragma unroll
+  for (int o = 1; o < LANES; o *= 2) {
+    length += __shfl_xor_sync(0xffffffffu, length, o);
+    w.units += __shfl_xor_sync(0xffffffffu, w.units, o);
+    w.longest = max(w.longest, __shfl_xor_sync(0xffffffffu, w.longest, o));
   }
   w.length = (int)min(length * a.hk, (int64_t)INT32_MAX);
   w.units *= a.hk;
@@ -156,6 +171,42 @@ struct Walk {
       pieces = (unsigned)(cost + plan.share - 1) / (unsigned)plan.share;
       size = (unsigned)(cost + pieces - 1) / (unsigned)pieces;
       length = pieces * plan.share;
+    }
+  }
+  // A whole warp, before its first piece: on to the row tile of the first request in which the worker's part
+  // begins, 32 of them at a time (a prompt of 2,000 tokens has 63, one after the other they took 10 us).
+  __device__ __forceinline__ void seek(const AttendArgs& a) {
+    if (u >= to || r >= a.R) return;
+    q = load_request(a, r);
+    if (q.n <= 0) return;
+    loaded = true;
+    row0 = h = 0;
+    const int lane = threadIdx.x & 31, rows = q.n * a.group;
+    for (int64_t first = 0; first < rows; first += 32 * S::ROWS) {
+      const int64_t mine = first + lane * S::ROWS;
+      int all = 0;
+      if (mine < rows) {
+        row0 = (int)mine;
+        row_tile(a);
+        all = length * a.hk;
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) all += x;
+      }
+      const uint32_t there = __ballot_sync(0xffffffffu, mine < rows && u + all > from);
+      const int at = there ? __ffs(there) - 1 : 31;
+      const int passed = __shfl_sync(0xffffffffu, all, there ? max(at - 1, 0) : 31);
+      if (!there || at > 0) u += passed;
+      row0 = (int)min(first + at * S::ROWS, (int64_t)INT32_MAX);
+      if (there) break;
+    }
+    if (row0 < rows) {
+      row_tile(a);
+    } else {  // never: the request holds what the worker begins with
+      r++;
+      loaded = false;
     }
   }
   __device__ __forceinline__ bool next(const AttendArgs& a, Piece& x) {
@@ -196,9 +247,9 @@ struct Walk {
       x.n = q.n;
       x.ctx = q.ctx;
       x.len = q.len;
-      x.open = !q.good ? 0 : a.mask ? q.ctx : q.ctx + row0 / a.group + 1;
+      x.open = !q.good ? 0 : a.mask ? q.ctx : q.ctx + by_group(a, row0) + 1;
       if (S::WIN) {
-        x.shut = q.ctx + (a.mask ? min(q.n, KV_TREE_MAX) : (row0 + x.rows - 1) / a.group + 1) - a.window;
+        x.shut = q.ctx + (a.mask ? min(q.n, KV_TREE_MAX) : by_group(a, row0 + x.rows - 1) + 1) - a.window;
         x.head = span.head;
         x.skip = span.skip;
       }
@@ -247,8 +298,13 @@ __device__ __forceinline__ int make_plan(const AttendArgs& a, Plan& plan, int* s
   int* s_coarse = s_longest + THREADS / 32;
   plan = {1, false};
   int total;
-  const int R = (int)a.R, per = (R + THREADS - 1) / THREADS;
-  const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
+  // few requests are a warp's each, which counts their row tiles together; of many a thread has a run
+  const int R = (int)a.R;
+  const bool few = R <= THREADS / 32;
+  const int per = (R + THREADS - 1) / THREADS;
+  const int r0 = few ? min(R, warp) : min(R, tid * per), r1 = few ? min(R, warp + 1) : min(R, r0 + per);
+  const bool counts = !few || lane == 0;
+  auto work = [&](const Request& q) { return few ? request_work<S, 32>(a, q, plan) : request_work<S, 1>(a, q, plan); };
   int mine = 0, units = 0, longest = 0, before, coarse = 0;
   const int64_t head = R ? a.off[0] : 0, tail = R ? a.off[R] : 0;
   for (int r = r0; r < r1; r++) {
@@ -257,8 +313,9 @@ __device__ __forceinline__ int make_plan(const AttendArgs& a, Plan& plan, int* s
       coarse = 1 << 21;
       break;
     }
-    if (!q.good && blockIdx.x == 0 && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = r;
-    const UnitSum w = request_work<S>(a, q, plan);
+    if (!q.good && blockIdx.x == 0 && counts && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = r;
+    const UnitSum w = work(q);
+    if (!counts) break;
     mine += w.length;
     units += w.units;
     longest = max(longest, w.longest);
@@ -329,7 +386,10 @@ __device__ __forceinline__ int make_plan(const AttendArgs& a, Plan& plan, int* s
       plan.share = share;
       plan.padded = true;
       mine = 0;
-      for (int r = r0; r < r1; r++) mine += request_work<S>(a, load_request(a, r), plan).length;
+      for (int r = r0; r < r1; r++) {
+        const int c = work(load_request(a, r)).length;
+        if (counts) mine += c;
+      }
       __syncthreads();  // s_sum has been read
       before = scan(mine, total);
     }
@@ -339,7 +399,7 @@ __device__ __forceinline__ int make_plan(const AttendArgs& a, Plan& plan, int* s
     if (x < before || x >= before + mine) continue;
     int r = r0, at = before;
     for (; r < r1 - 1; r++) {
-      const int c = request_work<S>(a, load_request(a, r), plan).length;
+      const int c = request_work<S, 1>(a, load_request(a, r), plan).length;  // (of few requests r0 is the last)
       if (x < at + c) break;
       at += c;
     }

@@ -182,7 +182,7 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
   auto fetch = [&](const Piece& x) {
 #pragma unroll
     for (int r = 0; r < NR; r++) {
-      const int rr = r * 8 + g, gr = x.row0 + rr, tok = gr / a.group;
+      const int rr = r * 8 + g, gr = x.row0 + rr, tok = by_group(a, gr);
       const T* src = static_cast<const T*>(a.q) + (x.t0 + tok) * a.q_stride + (x.h * a.group + gr - tok * a.group) * D + t4 * (D / 4);
       uint4 v[D / 32];
 #pragma unroll
@@ -311,7 +311,7 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
           for (int e = 0; e < 2; e++) {
             const int rr = r * 8 + 2 * t4 + e;
             Seen<WIN> seen;
-            seen.set(a, p, rr < p.rows, rr < p.rows ? (p.row0 + rr) / a.group : 0);
+            seen.set(a, p, rr < p.rows, rr < p.rows ? by_group(a, p.row0 + rr) : 0);
             bits[r][e] = seen.bits(k0) >> g;
             if (!(bits[r][e] & 1)) s[r][e] = -INFINITY;
             if (!(bits[r][e] & 256)) s[r][2 + e] = -INFINITY;
@@ -461,7 +461,7 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
         y = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
         const float log2sum = none ? -INFINITY : (top == -INFINITY ? 0.f : top - A8_UP) + log2f(sum);
         if (whole) {
-          const int gr = p.row0 + rr, tok = gr / a.group;
+          const int gr = p.row0 + rr, tok = by_group(a, gr);
           const int64_t at = (int64_t)(p.t0 + tok) * a.hq + p.h * a.group + (gr - tok * a.group);
           *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * D + col) = make_uint2(pack2<T>(y.x, y.y), pack2<T>(y.z, y.w));
           if (a.lse && col == 0) a.lse[at] = log2sum * 0.69314718055994531f;
@@ -518,7 +518,7 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
             }
           }
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          const int gr = p.row0 + rr, tok = gr / a.group;
+          const int gr = p.row0 + rr, tok = by_group(a, gr);
           const int64_t at = (int64_t)(p.t0 + tok) * a.hq + p.h * a.group + (gr - tok * a.group);
           *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * D + col) =
               make_uint2(pack2<T>(y.x * inv, y.y * inv), pack2<T>(y.z * inv, y.w * inv));
