@@ -112,14 +112,17 @@ struct Plan {
 struct UnitSum {
   int length, units, longest;
 };
-// Of LANES neighbouring lanes that share the request, each some of its row tiles; all get the sum.
-template <class S, int LANES>
-__device__ __forceinline__ UnitSum request_work(const AttendArgs& a, const Request& q, const Plan& plan) {
+// shared: a whole warp has the request, each lane some of its row tiles, and all get the sum.
+template <class S>
+__device__ __forceinline__ UnitSum request_work(const AttendArgs& a, const Request& q, const Plan& plan, bool shared) {
   UnitSum w = {0, 0, 0};
   int64_t length = 0;
-  const int rows = q.n * a.group, lane = threadIdx.x % LANES;
+  const int rows = q.n * a.group;
   const bool same = a.mask || !q.good || rows <= S::ROWS;  // every row tile has the request's keys
-  for (int64_t row0 = (int64_t)lane * S::ROWS; row0 < rows; row0 += LANES * S::ROWS) {
+  shared = shared && !same;
+  const int step = shared ? 32 * S::ROWS : S::ROWS;
+#pragma unroll 1
+  for (int64_t row0 = shared ? threadIdx.x % 32 * S::ROWS : 0; row0 < rows; row0 += step) {
     const int cost = span_tiles<S>(unit_span<S>(a, q, (int)row0)) + S::UNIT_COST;
     const int tiles = same ? (rows + S::ROWS - 1) / S::ROWS : 1;
     length += (int64_t)(plan.padded ? ((unsigned)(cost + plan.share - 1) / (unsigned)plan.share) * plan.share : cost) * tiles;
@@ -127,15 +130,13 @@ __device__ __forceinline__ UnitSum request_work(const AttendArgs& a, const Reque
     w.longest = max(w.longest, cost);
     if (same) break;
   }
-  if (same && lane > 0) {  // the first lane has them all
-    length = 0;
-    w = {0, 0, 0};
-  }
-#pragma unroll
-  for (int o = 1; o < LANES; o *= 2) {
-    length += __shfl_xor_sync(0xffffffffu, length, o);
-    w.units += __shfl_xor_sync(0xffffffffu, w.units, o);
-    w.longest = max(w.longest, __shfl_xor_sync(0xffffffffu, w.longest, o));
+  if (shared) {
+#pragma unroll 1
+    for (int o = 1; o < 32; o *= 2) {
+      length += __shfl_xor_sync(0xffffffffu, length, o);
+      w.units += __shfl_xor_sync(0xffffffffu, w.units, o);
+      w.longest = max(w.longest, __shfl_xor_sync(0xffffffffu, w.longest, o));
+    }
   }
   w.length = (int)min(length * a.hk, (int64_t)INT32_MAX);
   w.units *= a.hk;
@@ -178,10 +179,10 @@ struct Walk {
   __device__ __forceinline__ void seek(const AttendArgs& a) {
     if (u >= to || r >= a.R) return;
     q = load_request(a, r);
-    if (q.n <= 0) return;
+    const int lane = threadIdx.x & 31, rows = q.n * a.group;
+    if (rows <= S::ROWS) return;
     loaded = true;
     row0 = h = 0;
-    const int lane = threadIdx.x & 31, rows = q.n * a.group;
     for (int64_t first = 0; first < rows; first += 32 * S::ROWS) {
       const int64_t mine = first + lane * S::ROWS;
       int all = 0;
@@ -190,7 +191,7 @@ struct Walk {
         row_tile(a);
         all = length * a.hk;
       }
-#pragma unroll
+#pragma unroll 1
       for (int o = 1; o < 32; o *= 2) {
         const int x = __shfl_up_sync(0xffffffffu, all, o);
         if (lane >= o) all += x;
@@ -304,7 +305,6 @@ __device__ __forceinline__ int make_plan(const AttendArgs& a, Plan& plan, int* s
   const int per = (R + THREADS - 1) / THREADS;
   const int r0 = few ? min(R, warp) : min(R, tid * per), r1 = few ? min(R, warp + 1) : min(R, r0 + per);
   const bool counts = !few || lane == 0;
-  auto work = [&](const Request& q) { return few ? request_work<S, 32>(a, q, plan) : request_work<S, 1>(a, q, plan); };
   int mine = 0, units = 0, longest = 0, before, coarse = 0;
   const int64_t head = R ? a.off[0] : 0, tail = R ? a.off[R] : 0;
   for (int r = r0; r < r1; r++) {
@@ -314,7 +314,7 @@ __device__ __forceinline__ int make_plan(const AttendArgs& a, Plan& plan, int* s
       break;
     }
     if (!q.good && blockIdx.x == 0 && counts && atomicCAS(&a.status->code, 0, TK_E_LIMIT) == 0) a.status->request = r;
-    const UnitSum w = work(q);
+    const UnitSum w = request_work<S>(a, q, plan, few);
     if (!counts) break;
     mine += w.length;
     units += w.units;
@@ -387,7 +387,7 @@ __device__ __forceinline__ int make_plan(const AttendArgs& a, Plan& plan, int* s
       plan.padded = true;
       mine = 0;
       for (int r = r0; r < r1; r++) {
-        const int c = work(load_request(a, r)).length;
+        const int c = request_work<S>(a, load_request(a, r), plan, few).length;
         if (counts) mine += c;
       }
       __syncthreads();  // s_sum has been read
@@ -399,7 +399,7 @@ __device__ __forceinline__ int make_plan(const AttendArgs& a, Plan& plan, int* s
     if (x < before || x >= before + mine) continue;
     int r = r0, at = before;
     for (; r < r1 - 1; r++) {
-      const int c = request_work<S, 1>(a, load_request(a, r), plan).length;  // (of few requests r0 is the last)
+      const int c = request_work<S>(a, load_request(a, r), plan, false).length;  // (of few requests r0 is the last)
       if (x < at + c) break;
       at += c;
     }

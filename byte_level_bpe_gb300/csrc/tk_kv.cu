@@ -332,12 +332,13 @@ struct AppendArgs {
 // the passes of a warp arrive ahead in shared memory, each lane's elements in its own place
 // (in registers, two passes ahead, 32,768 rows of 48 heads took 163 us instead of 140).
 template <class T, int LANES, bool NEIGHBOURS>
-__device__ __forceinline__ void append_rows(const AppendArgs& a, uint4 (*s_x)[APPEND_FLIGHT][2][32], int64_t cta) {
+__global__ void __launch_bounds__(APPEND_THREADS, 5) k_kv_append(AppendArgs a) {
   using P = Pair<T>;
   using T2 = typename P::type;
   constexpr int HEADS = 32 / LANES;
+  __shared__ uint4 s_x[APPEND_THREADS / 32][APPEND_FLIGHT][2][32];
   const int lane = threadIdx.x & 31, l = lane % LANES, g = lane / LANES;
-  const int64_t w = (cta * APPEND_THREADS + threadIdx.x) >> 5;
+  const int64_t w = ((int64_t)blockIdx.x * APPEND_THREADS + threadIdx.x) >> 5;
   const int64_t t = w / a.chunks;
   if (t >= a.T) return;
   // the lane's two runs of 8 elements: pairs are (e0 + i, e1 + i), or neighbours in each
@@ -479,12 +480,6 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, uint4 (*s_x)[AP
       *reinterpret_cast<uint4*>(dst + e1) = x1.u;
     }
   }
-}
-
-template <class T, int LANES, bool NEIGHBOURS>
-__global__ void __launch_bounds__(APPEND_THREADS, 5) k_kv_append(AppendArgs a) {
-  __shared__ uint4 s_x[APPEND_THREADS / 32][APPEND_FLIGHT][2][32];
-  append_rows<T, LANES, NEIGHBOURS>(a, s_x, blockIdx.x);
 }
 
 // Into 8-bit blocks: a value stands for e4m3 * scale of its block and head, for keys and values apart.
@@ -647,7 +642,7 @@ __device__ __forceinline__ void store8_runs(const Store8Args& s, int cta) {
   const int64_t mine = slot_of(t_first + lane), before = slot_of(t_first + lane - 1);
   uint32_t starts = __ballot_sync(ALL, lane < s.chunk && mine >= 0 && mine >> a.log2_bs != before >> a.log2_bs);
 
-  // the lane's elements, as append_rows has them
+  // the lane's elements, as k_kv_append has them
   const bool key = part < s.hk, normed = key && a.k_gain;
   uint8_t* pool = (key ? s.k : s.v) + h * a.s_head;
   float* scales = (key ? s.k_scale : s.v_scale) + h;
@@ -817,7 +812,7 @@ __device__ __forceinline__ void store8_runs(const Store8Args& s, int cta) {
   }
 }
 
-// The queries, as append_rows does them (a third of its instructions, which bound it: 79.6 M for 32k rows of 32 heads).
+// The queries, as k_kv_append does them, in fewer instructions (101 us for 32k rows of 32 heads, 121 with its own loop).
 template <class T, int LANES, bool NEIGHBOURS>
 __device__ __forceinline__ void store8_queries(const Store8Args& s, uint4 (*s_x)[APPEND_FLIGHT][2][32], int cta) {
   constexpr int G = 32 / LANES;

@@ -311,15 +311,16 @@ class KVCache:
         elif out.shape != q.shape or out.dtype is not self.dtype or not out.is_contiguous() or out.get_device() != index:
             raise ValueError("out must be a contiguous tensor of q's shape and type")
         sums = torch.empty((T, hq), dtype=torch.float32, device=self.device) if lse else None
-        common = (self._h, workspace._h, q.data_ptr(), _row_stride(step, T, hq * d, "q"), hq, p_off, R, T,
-                  T if max_new is None else max_new, p_len, p_table, stride, W, p_mask)
-        rest = (d ** -0.5 if scale is None else scale, out.data_ptr(), sums.data_ptr() if lse else None, _raw_stream(index))
+        step, most, rate = _row_stride(step, T, hq * d, "q"), T if max_new is None else max_new, d ** -0.5 if scale is None else scale
+        p_lse = sums.data_ptr() if lse else None
         if window is None:
             if sinks:
                 raise ValueError("sinks go with a window")
-            rc = native.load().tk_kv_attend(*common, *rest)
+            rc = native.load().tk_kv_attend(self._h, workspace._h, q.data_ptr(), step, hq, p_off, R, T, most, p_len, p_table,
+                                            stride, W, p_mask, rate, out.data_ptr(), p_lse, _raw_stream(index))
         else:
-            rc = native.load().tk_kv_attend_window(*common, window, sinks, *rest)
+            rc = native.load().tk_kv_attend_window(self._h, workspace._h, q.data_ptr(), step, hq, p_off, R, T, most, p_len, p_table,
+                                                   stride, W, p_mask, window, sinks, rate, out.data_ptr(), p_lse, _raw_stream(index))
         if rc:
             native.check(rc, "tk_kv_attend" if window is None else "tk_kv_attend_window")
         return (out, sums) if lse else out
