@@ -429,7 +429,7 @@ struct Seen {
       if (x.n < 64) mask &= (1ull << x.n) - 1;
       at = x.ctx + __popcll(mask & ~(1ull << tok));
     }
-    low = WIN ? at + 1 - a.window : 0;
+    low = WIN ? max(0, at + 1 - a.window) : 0;
     sinks = WIN ? a.sinks : 0;
   }
   static __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }

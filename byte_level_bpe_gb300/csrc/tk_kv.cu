@@ -1088,6 +1088,7 @@ extern "C" int tk_kv_cache_create8(void* d_k, void* d_v, float* d_k_scale, float
                                    int n_heads, int block_size, int head_dim, const int64_t* stride, tk_kv_cache** out) {
   const char* where = "tk_kv_cache_create8";
   if (!d_k_scale || !d_v_scale) return kv_arg(where, "null pointer");
+  if (d_k_scale == d_v_scale) return kv_arg(where, "keys and values have the same scales");
   if ((((uintptr_t)d_k_scale | (uintptr_t)d_v_scale) & 3) != 0) return kv_arg(where, "scales are not 4-byte aligned");
   return kv_create(where, d_k, d_v, d_k_scale, d_v_scale, type, n_blocks, n_heads, block_size, head_dim, stride, out);
 }

@@ -210,6 +210,7 @@ class KVCache:
                 _need(x is not None and x.dtype is torch.float32 and x.shape == k.shape[:2] and x.is_contiguous()
                       and x.get_device() == k.get_device(),
                       "k_scale and v_scale must be contiguous float32[n_blocks, kv_heads] tensors on k's device")
+            _need(k_scale.data_ptr() != v_scale.data_ptr(), "k_scale and v_scale must be two tensors")
         else:
             _need(k_scale is None and v_scale is None and dtype in (None, k.dtype),
                   "scales and a type of their own go with float8_e4m3fn keys and values only")
@@ -248,7 +249,8 @@ class KVCache:
             raise ValueError(f"qkv must be {self.dtype}[T, (q_heads + 2 kv_heads) * head_dim] on cuda:{index}, "
                              "rows contiguous")
         if (qkv.requires_grad or (q_gain is not None and q_gain.requires_grad)
-                or (k_gain is not None and k_gain.requires_grad) or (rope is not None and rope.requires_grad)):
+                or (k_gain is not None and k_gain.requires_grad) or (rope is not None and rope.requires_grad)
+                or (self.k_scale is not None and (self.k_scale.requires_grad or self.v_scale.requires_grad))):
             _no_gradient("append")
         f32 = torch.float32
         p_qg = _vector(q_gain, "q_gain", f32, d, index) if q_gain is not None else None
@@ -299,7 +301,8 @@ class KVCache:
         if (width != d or q.dtype is not self.dtype or q.get_device() != index or unit != 1
                 or (head != d and hq > 1)):
             raise ValueError(f"q must be {self.dtype}[T, q_heads, head_dim] on cuda:{index}, the heads of a token contiguous")
-        if q.requires_grad or self.k.requires_grad or self.v.requires_grad:
+        if (q.requires_grad or self.k.requires_grad or self.v.requires_grad
+                or (self.k_scale is not None and (self.k_scale.requires_grad or self.v_scale.requires_grad))):
             _no_gradient("attend")
         R = lengths.numel()
         p_table, stride, W = _table(table, R, torch.int32, index)

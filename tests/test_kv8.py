@@ -49,33 +49,46 @@ def test_create8_refusals_are_host_side():
     from byte_level_bpe_gb300 import native
     lib = native.load()
 
-    def create(k=1 << 20, v=1 << 20, ks=1 << 20, vs=1 << 20, type=1, stride=None):
+    def create(k=1 << 20, v=1 << 20, ks=1 << 20, vs=1 << 21, type=1, stride=None):
         h = ctypes.c_void_p()
         st = (ctypes.c_int64 * 3)(*stride) if stride else None
         return lib.tk_kv_cache_create8(k, v, ks, vs, type, 4, 2, 16, 64, st, ctypes.byref(h))
 
-    for bad in (dict(k=None), dict(v=None), dict(ks=None), dict(vs=None), dict(ks=(1 << 20) + 2), dict(type=3), dict(k=(1 << 20) + 8),
+    for bad in (dict(k=None), dict(v=None), dict(ks=None), dict(vs=None), dict(vs=1 << 20), dict(ks=(1 << 20) + 2), dict(type=3), dict(k=(1 << 20) + 8),
                 dict(stride=(2048, 1024, 72)), dict(stride=(2048, 1024, 48))):
         assert create(**bad) == native.TK_E_ARG, bad
 
 
 def test_cache_arguments(tk, host):
     x = host_inputs()
-    k, s = x["k"].to(E4M3), on_cuda(torch.ones(8, 2))
-    k = on_cuda(k)
-    tk.KVCache(k, k, s, s)
-    tk.KVCache(k, k, s, s, torch.float16)
+    k, s, z = (on_cuda(y) for y in (x["k"].to(E4M3), torch.ones(8, 2), torch.ones(8, 2)))
+    tk.KVCache(k, k, s, z)
+    tk.KVCache(k, k, s, z, torch.float16)
     assert [a[4] for n, a in host.calls if n == "tk_kv_cache_create8"] == [tk.native.TK_BF16, tk.native.TK_F16]
     seen = len(host.calls)
-    for bad in (lambda: tk.KVCache(k, k), lambda: tk.KVCache(k, k, s), lambda: tk.KVCache(k, k, s, s, torch.float32),
+    for bad in (lambda: tk.KVCache(k, k), lambda: tk.KVCache(k, k, s), lambda: tk.KVCache(k, k, s, z, torch.float32),
                 lambda: tk.KVCache(k, k, s, on_cuda(s.half())), lambda: tk.KVCache(k, k, s, on_cuda(torch.ones(8, 3))),
-                lambda: tk.KVCache(k, k, on_cuda(torch.ones(2, 8)).t(), s), lambda: tk.KVCache(k, x["v"], s, s),
-                lambda: tk.KVCache(x["k"], x["v"], s, s), lambda: tk.KVCache(x["k"], x["v"], dtype=torch.float16)):
+                lambda: tk.KVCache(k, k, on_cuda(torch.ones(2, 8)).t(), s), lambda: tk.KVCache(k, x["v"], s, z),
+                lambda: tk.KVCache(k, k, s, s), lambda: tk.KVCache(x["k"], x["v"], s, z),
+                lambda: tk.KVCache(x["k"], x["v"], dtype=torch.float16)):
         with pytest.raises(ValueError):
             bad()
     assert [n for n, _ in host.calls[seen:] if "free" not in n] == []
     with pytest.raises(ValueError):  # rows and queries have the cache's dtype
-        tk.KVCache(k, k, s, s, torch.float16).append(x["qkv"], x["pos"], x["slots"], x["hq"])
+        tk.KVCache(k, k, s, z, torch.float16).append(x["qkv"], x["pos"], x["slots"], x["hq"])
+
+
+def test_scales_that_require_a_gradient_are_refused(tk, host):
+    x = host_inputs()
+    k, z = on_cuda(x["k"].to(E4M3)), on_cuda(torch.ones(8, 2))
+    cache, ws = tk.KVCache(k, k, on_cuda(torch.ones(8, 2).requires_grad_()), z), tk.KVWorkspace()
+    calls = (lambda: cache.append(x["qkv"], x["pos"], x["slots"], x["hq"]),
+             lambda: cache.attend(x["q"], x["off"], x["ctx"], x["table"], ws))
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+        with torch.no_grad():
+            call()
 
 
 def test_side_streams_keep_the_scales(tk, host, monkeypatch):
@@ -134,7 +147,11 @@ CASES = [  # new tokens and cached ones of each request, heads, head_dim, rotate
     ([130], [7], 8, 1, 128, 128, True, 64, True), ([70, 300], [50, 127], 12, 3, 128, 64, False, 128, True),
     ([1] * 64, list(range(64)), 32, 8, 128, 128, False, 16, True), ([3], [1], 2, 2, 256, 256, False, 16, True),
     ([19, 200], [100, 3], 6, 2, 240, 112, True, 128, True), ([11], [4], 5, 1, 80, 0, False, 16, True),
-    ([2], [14], 1, 1, 48, 48, True, 16, False), ([700, 2, 900], [0, 33, 70], 3, 1, 112, 112, False, 32, True)]
+    ([2], [14], 1, 1, 48, 48, True, 16, False), ([700, 2, 900], [0, 33, 70], 3, 1, 112, 112, False, 32, True),
+    # more rows times key heads than a decode step has: runs of four warps, of one row, of a block, of more than stay in registers
+    ([150, 1, 1, 1, 90, 160], [0, 5, 63, 64, 70, 3], 16, 8, 128, 128, False, 64, True), ([1] * 320, [7] * 320, 8, 8, 64, 64, True, 16, True),
+    ([300, 0, 40], [100, 5, 127], 8, 8, 256, 128, False, 128, True), ([200, 140], [0, 31], 10, 10, 96, 32, True, 32, False),
+    ([2600], [3], 1, 1, 16, 0, False, 128, True)]
 
 
 @pytest.mark.gpu
@@ -216,6 +233,52 @@ def test_append_of_extremes(tk):
     assert empty.shape == (0, hq, d)
     cache.append(x, pos, torch.full_like(slots, -1), hq)
     assert all(torch.equal(a, b) for a, b in zip(state, [k.view(torch.uint8), v.view(torch.uint8), ks, vs]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [1, 100])
+def test_append_in_any_order_of_places(tk, heads):
+    """A block's rows follow one another in the call, in any order of their places: whole blocks backwards, and every other place."""
+    d, bs, gen = 16, 32, torch.Generator().manual_seed(heads)
+    slots = torch.tensor(list(range(63, 31, -1)) + list(range(97, 128, 2)) + [5], dtype=torch.int64)
+    T = len(slots)
+    x = (torch.randn(T, 3 * heads * d, generator=gen) * torch.exp(2 * torch.randn(T, 1, generator=gen))).half()
+    pool = (60 * torch.randn(2, 5, heads, bs, d, generator=gen)).clamp(-448, 448).to(E4M3).cuda()
+    before, scales = pool.double().cpu(), torch.exp2(torch.randint(-9, 0, (2, 5, heads), generator=gen).float())
+    on = [s.cuda().contiguous() for s in scales]
+    tk.KVCache(pool[0], pool[1], *on, torch.float16).append(x.cuda(), torch.zeros(T, dtype=torch.int32, device="cuda"), slots.cuda(), heads)
+    y = x.double().view(T, 3, heads, d)
+    for i in (0, 1):
+        want, near, scale = store_oracle(before[i], scales[i].double(), y[:, 1 + i], 2.0 ** -30 * y[:, 1 + i].abs() + 1e-300, slots, bs)
+        assert torch.equal(on[i].double().cpu(), scale)
+        _e4m3_close(pool[i], want, near, i)
+
+
+@pytest.mark.gpu
+def test_append_goes_by_no_order(tk):
+    """The same call twice gives the same bits, alone and captured."""
+    d, hk, bs, T = 128, 4, 32, 900
+    gen = torch.Generator("cuda").manual_seed(4)
+    x = torch.randn(T, 3 * hk * d, generator=gen, device="cuda").bfloat16()
+    slots, pos = torch.arange(T, device="cuda") + 5, torch.arange(T, device="cuda").int()
+    rope, gain = tk.rope_table(T, d), torch.rand(d, generator=gen, device="cuda")
+    start = (60 * torch.randn(2, 30, hk, bs, d, generator=gen, device="cuda")).clamp(-448, 448).to(E4M3).view(torch.uint8)
+    pool, scales = start.clone(), torch.full((2, 30, hk), 2.0 ** -9, device="cuda")
+    cache = tk.KVCache(pool[0].view(E4M3), pool[1].view(E4M3), scales[0], scales[1])
+
+    def step():
+        return cache.append(x, pos, slots, hk, q_gain=gain, k_gain=gain, rope=rope)
+
+    q = step()
+    want = pool.clone(), scales.clone(), q.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q = step()
+    for _ in range(3):
+        pool.copy_(start)
+        scales.fill_(2.0 ** -9)
+        graph.replay()
+        assert torch.equal(pool, want[0]) and torch.equal(scales, want[1]) and torch.equal(q, want[2])
 
 
 @pytest.mark.gpu
@@ -359,6 +422,58 @@ def test_attend_divided(tk, dtype, new, ctx, hq, hk, d, bs, tree):
     gen = torch.Generator().manual_seed(sum(ctx))
     case = case8(gen, new, ctx, hq, hk, d, bs, dtype)
     check8(tk, *case, masks=_tree_masks(gen, new) if tree else None, max_new=max(new))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hi", [2, 30])
+def test_attend_many_requests(tk, hi):
+    """More requests than a block has threads; empty ones among them."""
+    gen = torch.Generator().manual_seed(6)
+    R = 1500 if hi == 2 else 300
+    new = torch.randint(0, hi, (R,), generator=gen).tolist()
+    ctx = torch.randint(0, 60, (R,), generator=gen).tolist()
+    check8(tk, *case8(gen, new, ctx, 2, 1, 64, 16, torch.float16), max_new=hi)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_long_cache_past_32_bits(tk, n):
+    """Blocks more than 2^32 elements into the pool, stored there and read, by a request of 70,001 tokens; with a window too."""
+    bs, hk, d = 128, 2, 128
+    blocks = (1 << 32) // (hk * bs * d) + 600
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    k, v = (torch.empty(blocks, hk, bs, d, dtype=E4M3, device="cuda") for _ in "kv")
+    ks, vs = (torch.full((blocks, hk), float("nan"), device="cuda") for _ in "kv")
+    L = 70001
+    used = -(-L // bs)
+    table = torch.arange(blocks - 1, blocks - 1 - used, -1, dtype=torch.int32, device="cuda")[None]
+    place = torch.arange(L, device="cuda")
+    slots = table[0].long()[place // bs] * bs + place % bs
+    qkv = torch.randn(L, (4 + 2 * hk) * d, generator=gen, device="cuda").bfloat16()
+    cache, ws = tk.KVCache(k, v, ks, vs), tk.KVWorkspace()
+    q = cache.append(qkv, place.int(), slots, 4)[-n:].contiguous()
+    assert torch.equal(q, qkv[-n:, :4 * d].view(n, 4, d))
+    off, lens = torch.tensor([0, n], device="cuda"), torch.tensor([L], dtype=torch.int32, device="cuda")
+    lo = blocks - used
+    values = [(x[lo:].float() * s[lo:, :, None, None]).flip(0).transpose(0, 1).reshape(hk, -1, d)[:, :L].double() for x, s in ((k, ks), (v, vs))]
+    x = qkv.view(L, -1, d).transpose(0, 1).double()
+    for got, want in zip(values, (x[4:6], x[6:8])):
+        assert float((got - want).norm() / want.norm()) < 2.0 ** -4
+    for window in (None, 5000):
+        got = cache.attend(q, off, lens, table, ws, max_new=n, window=window, sinks=0 if window is None else 7).double()
+        ws.status()
+        for i in range(0, n, 13):
+            own = L - n + i
+            seen = place <= own
+            if window is not None:
+                seen &= (place > own - window) | (place < 7)
+            for h in range(4):
+                kk, vv = (y[h // 2, seen] for y in values)
+                s = kk @ q[i, h].double() * d ** -0.5
+                w = torch.softmax(s, 0)
+                o, a = w @ vv, w @ vv.abs()
+                big = (kk.abs() @ q[i, h].double().abs()).max() * d ** -0.5
+                _close(got[i, h], o, (1.02 * U[torch.bfloat16] * o.abs() + (2.0 ** -11 + 2.0 ** -15 * (1 + big)) * a + 2.0 ** -20).cpu(), (i, h))
 
 
 @pytest.mark.gpu

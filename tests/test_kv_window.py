@@ -116,7 +116,7 @@ def test_oracle_without_a_window():
             assert all(torch.allclose(x, y, rtol=1e-12, atol=1e-12) for x, y in zip(got, want))
 
 
-WINDOWS = [(64, 0), (64, 4), (65, 1), (127, 16), (128, 130), (200, 64), (1000, 3), (1 << 40, 0)]
+WINDOWS = [(64, 0), (64, 4), (65, 1), (127, 16), (128, 130), (200, 64), (1000, 3), (2 ** 31 - 2, 1), (1 << 40, 1 << 40)]
 SHAPES = [([1, 1, 1], [0, 199, 700], 4, 2, 16), ([3, 0, 17], [5, 9, 600], 4, 2, 64), ([64, 1, 33], [130, 1000, 2], 8, 1, 32),
           ([2] * 12, list(range(0, 720, 60)), 2, 2, 16), ([7, 40], [1500, 64], 5, 5, 128), ([64], [500], 20, 4, 16)]
 
@@ -195,7 +195,7 @@ def test_divided(tk, new, ctx, hq, hk):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("shape", range(len(SHAPES)))
-@pytest.mark.parametrize("window,sinks", [(64, 0), (65, 1), (128, 130), (200, 64), (1000, 3)])
+@pytest.mark.parametrize("window,sinks", [(64, 0), (65, 1), (128, 130), (200, 64), (1000, 3), (2 ** 31 - 2, 1)])
 def test_window_in_8_bits(tk, dtype, tree, shape, window, sinks):
     from test_kv8 import case8, check8
     new, ctx, hq, hk, bs = SHAPES[shape]
