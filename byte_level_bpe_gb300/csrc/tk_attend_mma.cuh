@@ -599,7 +599,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         const int k0 = at_key(lo + t);
         const bool hidden = decltype(some_hidden)::value && (MODE == 2 || !seen_by_all(k0));
         if (hidden) {
-          // Values of keys past the request's end become 0; so do infinities and NaN of
+          // Values of keys past the unit's become 0 (what is not loaded there may be anything, and is no reason to
+          // look for infinities below); so do infinities and NaN of
           // keys that only some rows see: 0 * inf in a product would reach the others.
           // (Rows that do see them get them back below.)  Streams that share a tile leave it to the first.
           if (MODE != 2 || stream == 0) {
@@ -616,7 +617,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
 #pragma unroll 4
               for (int i = part * (D / 8 / PARTS); i < (part + 1) * (D / 8 / PARTS); i++) {
                 uint4* x = reinterpret_cast<uint4*>(v + (i >> 3) * (KEYS * 128) + (((i & 7) ^ (kr & 7)) << 4));
-                if (key >= p.len) {
+                if (key >= p.keys) {
                   *x = make_uint4(0, 0, 0, 0);
                 } else {
                   uint4 y = *x;
