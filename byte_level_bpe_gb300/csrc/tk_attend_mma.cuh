@@ -74,6 +74,10 @@ __device__ __forceinline__ uint32_t nonfinite2<__half>(uint32_t w) {
 template <int D, int MODE, bool E8 = false>
 struct AttendShape {
   static constexpr int THREADS = E8 ? 512 : 384;
+  // E8, registers of a thread: 512 x 128 at launch = 128 x REGS_LOAD + 128 x REGS_TURN + 256 x REGS_SOFTMAX.  Eight tokens of
+  // 64 requests over 6k, 64 rows a key head: 276 us with 88, 88 and 168, 272 so; MODE 2 with 184 for the softmax loses 5%.
+  static constexpr int REGS_LOAD = MODE == 2 ? 80 : 112, REGS_TURN = MODE == 2 ? 48 : 64, REGS_SOFTMAX = MODE == 2 ? 192 : 168;
+  static_assert(REGS_LOAD + REGS_TURN + 2 * REGS_SOFTMAX == 4 * 128, "no more than the CTA has");
   static constexpr int RINGS = MODE == 2 ? 1 : 2, ROWS = MODE == 0 ? 32 : MODE == 1 ? 128 : 256;
   static constexpr int Q_ROWS = MODE == 0 ? 32 : 128;  // of a stream
   static constexpr int KEYS = MODE == 2 ? 128 : 64, BUFS = 128 / KEYS;  // keys of a tile; tiles' scores in tensor memory
@@ -216,9 +220,9 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
   };
 
   // registers: 384 x 168 at launch = 128 x 104 + 256 x 200, where a softmax thread holds 128 scores;
-  // E8: 512 x 128 = 256 x 64 + 256 x 192, or 256 x 88 + 256 x 168
+  // E8: see AttendShape
   if (warp < 4) {
-    if (E8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(MODE == 2 ? 64 : 88));
+    if (E8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::REGS_LOAD));
     else if (MODE == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 0 || (warp == 3 && MODE != 2)) {
       // ---- loads, in the order of their use: K0 K1 V0 K2 V1 K3 ... with two tiles' scores, K0 V0 K1 V1 ... with one
@@ -431,7 +435,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     }
     __syncwarp();
   } else if (E8 && warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(MODE == 2 ? 64 : 88));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::REGS_TURN));
     // ---- 8 bits to fp16, stage by stage.  A thread has 16 elements of a key at a time, the lanes of a
     // quarter-warp eight keys that follow one another: neither side meets a bank twice.
     constexpr int WARPS = MODE == 2 ? 4 : 2, CHUNKS = D / 16;
@@ -482,7 +486,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
     }
     __syncwarp();
   } else {
-    if (E8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(MODE == 2 ? 192 : 168));
+    if (E8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::REGS_SOFTMAX));
     else if (MODE == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax
     const int wq = warp & 3, row = wq * 32 + lane;  // row = also its lane of tensor memory
