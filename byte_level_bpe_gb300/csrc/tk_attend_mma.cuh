@@ -613,33 +613,34 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
             // stages ago. With three stages that is this tile's keys, which its scores are the sign of.
             if (NST < 4 && BUFS == 2) wait(b_s + 8 * (nt % BUFS), (nt / BUFS) & 1);
             wait(b_full + 8 * (at % NST), (at / NST) & 1);
-            constexpr int PARTS = 128 / KEYS;  // threads of a row
-            const int kr = row % KEYS, part = row / KEYS, key = k0 + kr;
-            if (seen_by_some(key)) {
-              uint8_t* v = smem + (s_ring - base) + (at % NST) * L::STAGE + kr * 128;
-              bool bad = false;
+            // 16 bytes a thread at a time, eight or sixteen keys a pass: those that every row sees are passed over
+            constexpr int CHUNKS = D / 8;
+            uint8_t* v = smem + (s_ring - base) + (at % NST) * L::STAGE;
+            bool bad = false;
 #pragma unroll 4
-              for (int i = part * (D / 8 / PARTS); i < (part + 1) * (D / 8 / PARTS); i++) {
-                uint4* x = reinterpret_cast<uint4*>(v + (i >> 3) * (KEYS * 128) + (((i & 7) ^ (kr & 7)) << 4));
-                if (key >= p.keys) {
-                  *x = make_uint4(0, 0, 0, 0);
-                } else {
-                  uint4 y = *x;
-                  uint32_t* z = reinterpret_cast<uint32_t*>(&y);
-                  if (nonfinite2<H>(z[0]) | nonfinite2<H>(z[1]) | nonfinite2<H>(z[2]) | nonfinite2<H>(z[3])) {
-                    bad = true;
+            for (int i = row; i < KEYS * CHUNKS; i += 128) {
+              const int kr = i / CHUNKS, ch = i % CHUNKS, key = k0 + kr;
+              if (!seen_by_some(key)) continue;
+              uint4* x = reinterpret_cast<uint4*>(v + (ch >> 3) * (KEYS * 128) + kr * 128 + (((ch & 7) ^ (kr & 7)) << 4));
+              // no row sees those past the unit's and before the first one's window
+              if (key >= p.keys || (WIN && key >= a.sinks && key < open - a.window)) {
+                *x = make_uint4(0, 0, 0, 0);
+              } else {
+                uint4 y = *x;
+                uint32_t* z = reinterpret_cast<uint32_t*>(&y);
+                if (nonfinite2<H>(z[0]) | nonfinite2<H>(z[1]) | nonfinite2<H>(z[2]) | nonfinite2<H>(z[3])) {
+                  bad = true;
 #pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                      const uint32_t b = nonfinite2<H>(z[e]);
-                      if (b & 0x8000u) z[e] &= 0xffff0000u;
-                      if (b & 0x80000000u) z[e] &= 0x0000ffffu;
-                    }
-                    *x = y;
+                  for (int e = 0; e < 4; e++) {
+                    const uint32_t b = nonfinite2<H>(z[e]);
+                    if (b & 0x8000u) z[e] &= 0xffff0000u;
+                    if (b & 0x80000000u) z[e] &= 0x0000ffffu;
                   }
+                  *x = y;
                 }
               }
-              if (bad) s_bad[taken & 7] = 1;
             }
+            if (bad) s_bad[taken & 7] = 1;
             fence_async_smem();
           }
           if (MODE == 2 && p.rows > 128) asm volatile("bar.sync 3, 256;" ::: "memory");
