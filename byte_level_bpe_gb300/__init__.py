@@ -9,7 +9,7 @@ For Million Token Agentic Workloads", "One native call for the whole serving
 path"; no Python lists of ids are ever built).
 
 `kv_plan`, `KVCache.append` and `KVCache.attend` (kv.py) take the encode's
-device ids and offsets on into a paged key/value cache.
+device ids and offsets on into a paged key/value cache of 16 or 8 bits.
 
 torch provides device memory and the current stream; every encode step runs
 in libtk's CUDA kernels. Without a built libtk.so or a CUDA device the calls

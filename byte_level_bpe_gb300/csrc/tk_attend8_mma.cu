@@ -1,4 +1,6 @@
-// tk_attend8_mma.cu -- the kernels of tk_attend_mma.cuh over a cache in 8 bits.
+// tk_attend8_mma.cu -- the kernels of tk_attend_mma.cuh over a cache in 8 bits, for more than 16 rows.
+// Up to 128 rows are units of a stream of their own, more go 256 to a pair: four prompts of 2,000 tokens with a window of
+// 1,024 take 420 us so and 444 as units of 128.
 #include "tk_attend_mma.cuh"
 
 namespace tk {

@@ -21,7 +21,13 @@
 // 3.25 GB: 488 us, 6.7 TB/s); above, the tensor cores and the latency of the chain from one
 // tile's scores to the next one's (64 drafted tokens over 131k, 512 rows a head: 219 us,
 // 1.25 PFLOP/s; 202 with the keys in L2 from the call before); a short call its chain of
-// first accesses (200 keys: 12 us).
+// first accesses (200 keys: 12 us).  With a window: HBM for single tokens (64 requests, 4,096 of 14k
+// each: 180 us, 6.0 TB/s), for prompts the starts and masked tiles of short units (2,000 tokens
+// of 4 requests with a window of 1,024: 241 us, 0.61 PFLOP/s; with 4,096 1.10; without one 1.32).
+// Over a cache in 8 bits 17 to 128 rows are bound by shared memory: for 64 keys of head_dim 128 a stream
+// has 16 KB written by TMA, read again, 32 KB written as fp16, and 64 KB read by the products, which is 76% of what two streams'
+// time has room for (eight tokens of 64 requests over 6k: 272 us; without turning the tiles 232).  More rows as above:
+// 64 drafted tokens over 131k 260 us, without the exponentials 231.
 #pragma once
 #include <type_traits>
 

@@ -1,5 +1,5 @@
 // tk_kv.cu -- placing requests in a paged key/value cache (tk_kv_plan) and
-// storing their rows there (tk_kv_append).
+// storing their rows there in 16 or 8 bits (tk_kv_append).
 #include <algorithm>
 #include <new>
 
@@ -493,6 +493,11 @@ __global__ void __launch_bounds__(APPEND_THREADS, 5) k_kv_append(AppendArgs a) {
 // prompts; 64 rows of up to 128 elements stay in registers between the search for the largest and the store, more are
 // read again.  W = 1: a decode step's few rows, each of which is a block's only one.  The runs of a warp or CTA
 // are those that begin among `chunk` tokens.
+// Bounds: 32k rows of 48 heads take 198 us, 1.7 times what their 777 MB need; the runs alone 114 (one load after the other:
+// slots, rows, positions, angles), the queries alone 101, and together they wait for issue slots, not memory.  64 rows
+// take 4.8 us, a launch and four loads that follow one another.
+// Other ways, 32k rows and 64 (us): a warp for each run 234 and 4.9; rows staged in shared memory and looked at
+// twice 237 and 6.9; all heads of a row by one warp 243 and 6.2; a CTA for each run with rows loaded twice 292 and 7.6.
 struct Store8Args {
   AppendArgs a;  // its hk is 0: its heads are the queries
   int hk;

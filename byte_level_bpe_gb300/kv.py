@@ -4,6 +4,9 @@
     q = cache.append(qkv, plan.positions, plan.slots, q_heads, ...)       # norm, rotate, store
     out = cache.attend(q, offsets, plan.lengths, table, workspace)        # read the cache
 
+The cache's blocks hold 16 bits or, over float8_e4m3fn tensors with a scale for each block and head, 8; a layer with a
+window reads with `attend(..., window=, sinks=)`.
+
 `offsets` has an entry where each request's tokens begin, and the end: what
 `encode_device` / `encode_segments` returned if a request is one segment. The
 encode counts segments, so for requests of several it is `offsets[first]`, with
