@@ -493,11 +493,12 @@ __global__ void __launch_bounds__(APPEND_THREADS, 5) k_kv_append(AppendArgs a) {
 // prompts; 64 rows of up to 128 elements stay in registers between the search for the largest and the store, more are
 // read again.  W = 1: a decode step's few rows, each of which is a block's only one.  The runs of a warp or CTA
 // are those that begin among `chunk` tokens.
-// Bounds: 32k rows of 48 heads take 198 us, 1.7 times what their 777 MB need; the runs alone 114 (one load after the other:
-// slots, rows, positions, angles), the queries alone 101, and together they wait for issue slots, not memory.  64 rows
+// Bounds: 32k rows of 48 heads take 175 us, 1.5 times what their 777 MB need: the runs wait for one load after the other
+// (slots, rows, positions, angles), the queries alone take 101, and together they wait for issue slots, not memory.  64 rows
 // take 4.8 us, a launch and four loads that follow one another.
 // Other ways, 32k rows and 64 (us): a warp for each run 234 and 4.9; rows staged in shared memory and looked at
-// twice 237 and 6.9; all heads of a row by one warp 243 and 6.2; a CTA for each run with rows loaded twice 292 and 7.6.
+// twice 237 and 6.9; all heads of a row by one warp 243 and 6.2; a CTA for each run and head with rows loaded twice 292 and
+// 7.6, once 198 and 4.8.
 struct Store8Args {
   AppendArgs a;  // its hk is 0: its heads are the queries
   int hk;
@@ -507,9 +508,11 @@ struct Store8Args {
   float* v_scale;
   float per_dim;          // 1 / head_dim
   int chunk;              // tokens
+  int heads, groups;      // heads of a warp or CTA, one after the other; groups of as many that keys' and values' come to
   int store_ctas, every;  // CTAs 0, every, 2 every, .. store; the others have the queries
 };
 constexpr int STORE8_CHUNK = 32;  // most tokens: their starts are a word
+constexpr int STORE8_HEADS = 2;  // 32k rows of 48 heads: 203 us with 1, 175 with 2, 179 with 4, 174 with 8
 constexpr float STORE8_LEAST = 7.888609052210118e-31f;  // 2^-100, the scale of zeros
 
 // What turns a lane's 16 elements, two runs of 8 of a head: z0 = x0 f00 + x1 f01, z1 = x1 f11 + x0 f10, or with the
@@ -635,8 +638,8 @@ __device__ __forceinline__ void store8_runs(const Store8Args& s, int cta) {
   __shared__ float s_top[W];
   const AppendArgs& a = s.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LANES, g = lane / LANES, sub = W == 1 ? 0 : warp;
-  const int item = W == 1 ? cta * WARPS + warp : cta, part = item % (2 * s.hk), h = part % s.hk;
-  const int64_t t_first = (int64_t)(item / (2 * s.hk)) * s.chunk;
+  const int item = W == 1 ? cta * WARPS + warp : cta, part0 = item % s.groups * s.heads, part1 = min(part0 + s.heads, 2 * s.hk);
+  const int64_t t_first = (int64_t)(item / s.groups) * s.chunk;
   if (t_first >= a.T) return;
   const int within = (1 << a.log2_bs) - 1;
   auto slot_of = [&](int64_t t) {  // -1: none
@@ -647,14 +650,21 @@ __device__ __forceinline__ void store8_runs(const Store8Args& s, int cta) {
   const int64_t mine = slot_of(t_first + lane), before = slot_of(t_first + lane - 1);
   uint32_t starts = __ballot_sync(ALL, lane < s.chunk && mine >= 0 && mine >> a.log2_bs != before >> a.log2_bs);
 
-  // the lane's elements, as k_kv_append has them
-  const bool key = part < s.hk, normed = key && a.k_gain;
-  uint8_t* pool = (key ? s.k : s.v) + h * a.s_head;
-  float* scales = (key ? s.k_scale : s.v_scale) + h;
+  // the lane's elements, as k_kv_append has them; of the head (of keys, then of values) that is `part` below
   const int half = a.rot >> 1;
-  const bool in_dim = l * 16 < a.dim, turned = key && l * 16 < a.rot, apart = !NEIGHBOURS && turned;
-  const int e0 = apart ? l * 8 : l * 16, e1 = apart ? e0 + half : e0 + 8;
-  const T* src = static_cast<const T*>(a.qkv) + (int64_t)(a.hq + part) * a.dim;
+  const bool in_dim = l * 16 < a.dim;
+  bool normed, turned;
+  int e0, e1;
+  const T* src;
+  auto head = [&](int part) {
+    const bool key = part < s.hk;
+    normed = key && a.k_gain;
+    turned = key && l * 16 < a.rot;
+    const bool apart = !NEIGHBOURS && turned;
+    e0 = apart ? l * 8 : l * 16;
+    e1 = apart ? e0 + half : e0 + 8;
+    src = static_cast<const T*>(a.qkv) + (int64_t)(a.hq + part) * a.dim;
+  };
   uint4 raw[BATCH][2];
   int32_t pos[BATCH];
   float y[BATCH][16], inv[BATCH];
@@ -728,92 +738,104 @@ __device__ __forceinline__ void store8_runs(const Store8Args& s, int cta) {
   for (; starts; starts &= starts - 1) {
     const int first = __ffs(starts) - 1;
     const int64_t t0 = t_first + first, slot0 = __shfl_sync(ALL, mine, first), b = slot0 >> a.log2_bs;
-    const float old = scales[b * s.hk];
+    head(part0);
     // A run of a prompt goes on to the block's end or the request's: up to there rows are on their way before the slots
     // have told how many they are.
     if (W > 1) load(t0, 0, (int)min((int64_t)(within + 1 - (slot0 & within)), a.T - t0));
-    // the run's rows and places
+    // the run's rows, and whether the block's first place is one of theirs
     int rows = 0;
-    uint32_t placed[4] = {0, 0, 0, 0};
+    bool begun = false;
     for (uint32_t in = ALL; in == ALL; ) {
       const int64_t x = slot_of(t0 + rows + lane);
       in = __ballot_sync(ALL, (x >> a.log2_bs) == b);
-      const int n = in == ALL ? 32 : __ffs(~in) - 1, place = (int)(x & within);
+      const int n = in == ALL ? 32 : __ffs(~in) - 1;
       rows += n;
-#pragma unroll
-      for (int i = 0; i < 4; i++) placed[i] |= __reduce_or_sync(ALL, lane < n && place >> 5 == i ? 1u << (place & 31) : 0u);
+      begun = begun || __any_sync(ALL, lane < n && (x & within) == 0);
     }
     // (rows that did not come in ahead: a run may be longer if its places do not ascend)
-    const bool again = rows > BATCH * STEP || W == 1 || rows > within + 1 - (int)(slot0 & within);
-    float m = 0.f;
-    for (int r0 = 0; r0 < rows; r0 += BATCH * STEP) {
-      if (again) load(t0, r0, rows);
-      turn(r0, rows);
+    const bool more = rows > BATCH * STEP || W == 1 || rows > within + 1 - (int)(slot0 & within);
+#pragma unroll 1
+    for (int part = part0; part < part1; part++) {
+      if (part > part0) head(part);
+      const int h = part < s.hk ? part : part - s.hk;
+      uint8_t* to = (part < s.hk ? s.k : s.v) + h * a.s_head + b * a.s_block;
+      float* at_scale = (part < s.hk ? s.k_scale : s.v_scale) + b * s.hk + h;
+      const float old = *at_scale;
+      const bool again = more || part > part0;
+      float m = 0.f;
+      for (int r0 = 0; r0 < rows; r0 += BATCH * STEP) {
+        if (again) load(t0, r0, rows);
+        turn(r0, rows);
 #pragma unroll
-      for (int k = 0; k < BATCH; k++) {
-        if (r0 + k * STEP + sub * G + g >= rows) break;
-        float x = largest(y[k]) * inv[k];
-        if (!(x < INFINITY)) {  // nor do infinities
-          x = 0.f;
+        for (int k = 0; k < BATCH; k++) {
+          if (r0 + k * STEP + sub * G + g >= rows) break;
+          float x = largest(y[k]) * inv[k];
+          if (!(x < INFINITY)) {  // nor do infinities
+            x = 0.f;
 #pragma unroll
-          for (int j = 0; j < 16; j++) {
-            const float z = fabsf(y[k][j] * inv[k]);
-            if (z < INFINITY) x = fmaxf(x, z);
+            for (int j = 0; j < 16; j++) {
+              const float z = fabsf(y[k][j] * inv[k]);
+              if (z < INFINITY) x = fmaxf(x, z);
+            }
+          }
+          m = fmaxf(m, x);
+        }
+      }
+      uint32_t top = __reduce_max_sync(ALL, __float_as_uint(m));
+      if (W > 1) {
+        if (lane == 0) s_top[sub] = __uint_as_float(top);
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; w++) top = max(top, __float_as_uint(s_top[w]));
+      }
+      // 448 = 1.75 2^8
+      const int e = (int)(top >> 23) - 8 + ((top & 0x7fffff) > 0x600000);
+      const float need = e < 27 ? STORE8_LEAST : __uint_as_float((uint32_t)e << 23);
+      const float scale = begun ? need : fmaxf(need, old), per_scale = 1.f / scale;
+      const bool pow2 = (__float_as_uint(scale) & 0x7fffff) == 0;
+      for (int r0 = 0; r0 < rows; r0 += BATCH * STEP) {
+        if (rows > BATCH * STEP) {
+          load(t0, r0, rows);
+          turn(r0, rows);
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; k++) {
+          const int r = r0 + k * STEP + sub * G + g;
+          if (r >= rows || !in_dim) break;
+          uint8_t* dst = to + (a.slot[t0 + r] & within) * a.s_token;
+          const float by = inv[k] * per_scale;
+          // exact if the scale is a power of two and the factor a normal number
+          if (pow2 && by >= 1.17549435e-38f && largest(y[k]) * inv[k] < INFINITY) {
+            *reinterpret_cast<uint2*>(dst + e0) = to_e4m3<true>(y[k], by, 1.f);
+            *reinterpret_cast<uint2*>(dst + e1) = to_e4m3<true>(y[k] + 8, by, 1.f);
+          } else {
+            *reinterpret_cast<uint2*>(dst + e0) = to_e4m3<false>(y[k], inv[k], scale);
+            *reinterpret_cast<uint2*>(dst + e1) = to_e4m3<false>(y[k] + 8, inv[k], scale);
           }
         }
-        m = fmaxf(m, x);
       }
-    }
-    uint32_t top = __reduce_max_sync(ALL, __float_as_uint(m));
-    if (W > 1) {
-      if (lane == 0) s_top[sub] = __uint_as_float(top);
-      __syncthreads();
+      // older rows of a block whose scale has grown
+      if (!begun && scale != old) {
+        const float ratio = old / scale;
+        uint32_t placed[4] = {0, 0, 0, 0};  // the run's places
+        for (int first = 0; first < rows; first += 32) {
+          const int place = first + lane < rows ? (int)(a.slot[t0 + first + lane] & within) : -1;
 #pragma unroll
-      for (int w = 0; w < W; w++) top = max(top, __float_as_uint(s_top[w]));
-    }
-    const bool begun = placed[0] & 1;
-    // 448 = 1.75 2^8
-    const int e = (int)(top >> 23) - 8 + ((top & 0x7fffff) > 0x600000);
-    const float need = e < 27 ? STORE8_LEAST : __uint_as_float((uint32_t)e << 23);
-    const float scale = begun ? need : fmaxf(need, old), per_scale = 1.f / scale;
-    const bool pow2 = (__float_as_uint(scale) & 0x7fffff) == 0;
-    uint8_t* to = pool + b * a.s_block;
-    for (int r0 = 0; r0 < rows; r0 += BATCH * STEP) {
-      if (rows > BATCH * STEP) {
-        load(t0, r0, rows);
-        turn(r0, rows);
-      }
-#pragma unroll
-      for (int k = 0; k < BATCH; k++) {
-        const int r = r0 + k * STEP + sub * G + g;
-        if (r >= rows || !in_dim) break;
-        uint8_t* dst = to + (a.slot[t0 + r] & within) * a.s_token;
-        const float by = inv[k] * per_scale;
-        // exact if the scale is a power of two and the factor a normal number
-        if (pow2 && by >= 1.17549435e-38f && largest(y[k]) * inv[k] < INFINITY) {
-          *reinterpret_cast<uint2*>(dst + e0) = to_e4m3<true>(y[k], by, 1.f);
-          *reinterpret_cast<uint2*>(dst + e1) = to_e4m3<true>(y[k] + 8, by, 1.f);
-        } else {
-          *reinterpret_cast<uint2*>(dst + e0) = to_e4m3<false>(y[k], inv[k], scale);
-          *reinterpret_cast<uint2*>(dst + e1) = to_e4m3<false>(y[k] + 8, inv[k], scale);
+          for (int i = 0; i < 4; i++) placed[i] |= __reduce_or_sync(ALL, place >= 0 && place >> 5 == i ? 1u << (place & 31) : 0u);
+        }
+#pragma unroll 1
+        for (int place = sub * G + g; place <= within; place += STEP) {
+          const int word = place >> 5;
+          const uint32_t there = word == 0 ? placed[0] : word == 1 ? placed[1] : word == 2 ? placed[2] : placed[3];
+          if ((there >> (place & 31)) & 1 || !in_dim) continue;
+          uint4* at = reinterpret_cast<uint4*>(to + place * a.s_token + l * 16);
+          const uint4 z = *at;
+          *at = make_uint4(rescale_e4m3(z.x, ratio), rescale_e4m3(z.y, ratio), rescale_e4m3(z.z, ratio), rescale_e4m3(z.w, ratio));
         }
       }
+      if (W > 1) __syncthreads();  // all have read s_top and the old scale
+      if (sub == 0 && lane == 0) *at_scale = scale;
     }
-    // older rows of a block whose scale has grown
-    if (!begun && scale != old) {
-      const float ratio = old / scale;
-#pragma unroll 1
-      for (int place = sub * G + g; place <= within; place += STEP) {
-        const int word = place >> 5;
-        const uint32_t there = word == 0 ? placed[0] : word == 1 ? placed[1] : word == 2 ? placed[2] : placed[3];
-        if ((there >> (place & 31)) & 1 || !in_dim) continue;
-        uint4* at = reinterpret_cast<uint4*>(to + place * a.s_token + l * 16);
-        const uint4 z = *at;
-        *at = make_uint4(rescale_e4m3(z.x, ratio), rescale_e4m3(z.y, ratio), rescale_e4m3(z.z, ratio), rescale_e4m3(z.w, ratio));
-      }
-    }
-    if (W > 1) __syncthreads();  // all have read s_top and the old scale
-    if (sub == 0 && lane == 0) scales[b * s.hk] = scale;
   }
 }
 
@@ -910,7 +932,8 @@ static void append8_launch(Store8Args& s, bool neighbours, int sms, cudaStream_t
   const unsigned grid = append_split<T, LANES>(s.a, sms);
   const int64_t enough = (int64_t)sms * 16;
   auto launch = [&](auto kernel, int warps) {
-    const int64_t items = (s.a.T + s.chunk - 1) / s.chunk * 2 * s.hk;
+    s.groups = (2 * s.hk + s.heads - 1) / s.heads;
+    const int64_t items = (s.a.T + s.chunk - 1) / s.chunk * s.groups;
     s.store_ctas = (int)((items * warps * 32 + APPEND_THREADS - 1) / APPEND_THREADS);
     s.every = (s.store_ctas + grid) / s.store_ctas;
     kernel<<<s.store_ctas + grid, APPEND_THREADS, 0, st>>>(s);
@@ -918,10 +941,12 @@ static void append8_launch(Store8Args& s, bool neighbours, int sms, cudaStream_t
   // A warp for every token and head while that is no more than 16 for each SM twice over: a decode step.  More tokens
   // are taken for chunks of prompts, whose runs are longer.
   if (s.a.T * s.hk <= enough) {
-    s.chunk = 1;
+    s.heads = s.chunk = 1;
     if (neighbours) launch(k_kv_append8<T, LANES, true, 1>, 1);
     else launch(k_kv_append8<T, LANES, false, 1>, 1);
   } else {
+    // (many rows: several heads for each run that has been looked up)
+    s.heads = (int)std::max<int64_t>(1, std::min<int64_t>(STORE8_HEADS, s.a.T * 2 * s.hk / (enough * 32)));
     s.chunk = (int)std::max<int64_t>(1, std::min<int64_t>(STORE8_CHUNK, s.a.T * 2 * s.hk / enough));
     if (neighbours) launch(k_kv_append8<T, LANES, true, 4>, 4);
     else launch(k_kv_append8<T, LANES, false, 4>, 4);
@@ -1128,7 +1153,7 @@ extern "C" int tk_kv_append(const tk_kv_cache* cache, const void* d_qkv, int64_t
     a.hk = 0;
     a.k = a.v = nullptr;
     Store8Args s = {a, cache->n_heads, static_cast<uint8_t*>(cache->k), static_cast<uint8_t*>(cache->v), cache->k_scale,
-                    cache->v_scale, 1.f / cache->head_dim, 1, 0, 1};
+                    cache->v_scale, 1.f / cache->head_dim, 1, 1, 1, 0, 1};
     if (cache->type == TK_BF16) append8_lanes<__nv_bfloat16>(s, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);
     else append8_lanes<__half>(s, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);
   } else if (cache->type == TK_BF16) append_lanes<__nv_bfloat16>(a, neighbours != 0, cache->sms, (cudaStream_t)cuda_stream);

@@ -151,7 +151,9 @@ CASES = [  # new tokens and cached ones of each request, heads, head_dim, rotate
     # more rows times key heads than a decode step has: runs of four warps, of one row, of a block, of more than stay in registers
     ([150, 1, 1, 1, 90, 160], [0, 5, 63, 64, 70, 3], 16, 8, 128, 128, False, 64, True), ([1] * 320, [7] * 320, 8, 8, 64, 64, True, 16, True),
     ([300, 0, 40], [100, 5, 127], 8, 8, 256, 128, False, 128, True), ([200, 140], [0, 31], 10, 10, 96, 32, True, 32, False),
-    ([2600], [3], 1, 1, 16, 0, False, 128, True)]
+    ([2600], [3], 1, 1, 16, 0, False, 128, True),
+    # so many that a run's heads are taken two at a time, the last key head with the first of the values
+    ([1000, 240], [5, 17], 63, 63, 16, 16, True, 32, True)]
 
 
 @pytest.mark.gpu
