@@ -552,7 +552,7 @@ static cudaError_t attend8_launch(const AttendArgs& a, const tk_kv_cache* cache,
     if (e != cudaSuccess) return e;
     if (cache->device < 64) set[cache->device] = true;
   }
-  k_kv_attend8<T, D, NR, WIN><<<grid, Attend8Shape<D, NR>::THREADS, bytes, st>>>(a, cache->map_k, cache->map_v);
+  k_kv_attend8<T, D, NR, WIN><<<grid, Attend8Shape<D, NR>::THREADS, bytes, st>>>(a, cache->map_k16, cache->map_v16);
   return cudaGetLastError();
 }
 

@@ -252,11 +252,11 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         at++;
       };
       // a box is 64 elements of a page's keys, at most 64 of them; a lane loads one box
-      // (E8: all elements of 16 of them)
-      const int log2_box = E8 ? 4 : min(a.log2_bs, 6), per_page = a.log2_bs - log2_box, ppt = KEYS >> log2_box;
+      // (E8: of all elements)
+      const int log2_box = min(a.log2_bs, 6), per_page = a.log2_bs - log2_box, ppt = KEYS >> log2_box;
       const int my_box = E8 ? lane : lane / HALVES, my_half = E8 ? 0 : lane % HALVES;
-      const uint32_t my_dst = E8 ? s_raw + my_box * (16 * D) : s_ring + my_half * (KEYS * 128) + (my_box * 128 << log2_box);
-      const uint32_t box_bytes = E8 ? 16 * D : HALVES * 128u << log2_box;
+      const uint32_t my_dst = E8 ? s_raw + (my_box * D << log2_box) : s_ring + my_half * (KEYS * 128) + (my_box * 128 << log2_box);
+      const uint32_t box_bytes = E8 ? (uint32_t)D << log2_box : HALVES * 128u << log2_box;
       constexpr int NLD = E8 ? L::RAWS : NST, LD = E8 ? L::RAW : L::STAGE;  // the stages that are loaded
       const uint32_t b_land = E8 ? b_raw : b_full, b_left = E8 ? b_used : b_empty;
       uint32_t scaled = 0;  // tiles whose scales have been handed over
@@ -291,9 +291,9 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         const int nb = max(0, min(ppt, boxes - box0));
         const int id = __shfl_sync(0xffffffffu, ids.now, (box0 + my_box) & 31);
         if (E8 && keys) {
-          const float ks = __shfl_sync(0xffffffffu, ids.scale.x, (box0 + my_box) & 31),
-                      vs = __shfl_sync(0xffffffffu, ids.scale.y, (box0 + my_box) & 31);
-          if (my_box < L::GROUPS) s_scale[(scaled % L::SCALED) * L::GROUPS + my_box] = my_box < nb ? make_float2(ks, vs) : make_float2(0.f, -INFINITY);
+          const int of = lane >> (log2_box - 4);  // the box of group `lane`
+          const float ks = __shfl_sync(0xffffffffu, ids.scale.x, (box0 + of) & 31), vs = __shfl_sync(0xffffffffu, ids.scale.y, (box0 + of) & 31);
+          if (lane < L::GROUPS) s_scale[(scaled % L::SCALED) * L::GROUPS + lane] = of < nb ? make_float2(ks, vs) : make_float2(0.f, -INFINITY);
           scaled++;
           __syncwarp();
         }

@@ -1031,9 +1031,9 @@ extern "C" int tk_kv_plan(const int64_t* d_off, const int32_t* d_ctx, int64_t R,
 }
 
 // The cache as a tensor (element, token, head, block).  16 bits: its box is 64 elements of one head's
-// block, or of half of one of 128 tokens: 128-byte rows, swizzled as the tensor cores read them.  8 bits: 16
-// tokens of all elements, swizzled so that eight lanes that read 16 bytes of eight rows meet no bank twice.
-static bool kv_map(const tk_kv_cache* c, void* mem, CUtensorMap* map) {
+// block, or of half of one of 128 tokens: 128-byte rows, swizzled as the tensor cores read them.  8 bits: all elements
+// of as many tokens, or of 16, swizzled so that eight lanes that read 16 bytes of eight rows meet no bank twice.
+static bool kv_map(const tk_kv_cache* c, void* mem, int tokens, CUtensorMap* map) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -1046,7 +1046,7 @@ static bool kv_map(const tk_kv_cache* c, void* mem, CUtensorMap* map) {
   const cuuint64_t size = e8 ? 1 : 2;
   const cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->block_size, (cuuint64_t)c->n_heads, (cuuint64_t)c->n_blocks};
   const cuuint64_t strides[3] = {(cuuint64_t)c->stride[2] * size, (cuuint64_t)c->stride[1] * size, (cuuint64_t)c->stride[0] * size};
-  const cuuint32_t box[4] = {e8 ? (cuuint32_t)c->head_dim : 64u, e8 ? 16u : (cuuint32_t)std::min(c->block_size, 64), 1, 1},
+  const cuuint32_t box[4] = {e8 ? (cuuint32_t)c->head_dim : 64u, (cuuint32_t)std::min(c->block_size, tokens), 1, 1},
                    step[4] = {1, 1, 1, 1};
   return reinterpret_cast<Encode>(fn)(map,
                                       e8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -1099,7 +1099,8 @@ static int kv_create(const char* where, void* d_k, void* d_v, float* d_k_scale, 
   c->k_scale = d_k_scale;
   c->v_scale = d_v_scale;
   if (head_dim == 64 || head_dim == 128) {
-    if (!kv_map(c, d_k, &c->map_k) || !kv_map(c, d_v, &c->map_v)) {
+    if (!kv_map(c, d_k, 64, &c->map_k) || !kv_map(c, d_v, 64, &c->map_v) ||
+        (d_k_scale && (!kv_map(c, d_k, 16, &c->map_k16) || !kv_map(c, d_v, 16, &c->map_v16)))) {
       delete c;
       tk_set_error("%s: the driver takes no tensor map of this layout", where);
       return TK_E_CUDA;

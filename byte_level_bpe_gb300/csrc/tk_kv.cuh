@@ -54,6 +54,7 @@ struct tk_kv_cache {
   float* k_scale;  // [n_blocks][n_heads] of a cache in 8 bits, else null
   float* v_scale;
   CUtensorMap map_k, map_v;  // for tk_kv_attend; head_dim 64 and 128 only
+  CUtensorMap map_k16, map_v16;  // in 8 bits: boxes of 16 tokens
 };
 
 struct tk_kv_workspace {
