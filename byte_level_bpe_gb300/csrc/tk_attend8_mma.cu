@@ -1,13 +1,18 @@
 // tk_attend8_mma.cu -- the kernels of tk_attend_mma.cuh over a cache in 8 bits, for more than 16 rows.
-// Up to 128 rows are units of a stream of their own, more go 256 to a pair: four prompts of 2,000 tokens with a window of
-// 1,024 take 420 us so and 444 as units of 128.
+// Units of 128 rows for each stream, or for more rows of head_dim 128 of 256 for the pair (us, 256 and 128 rows):
+// 64 drafted tokens over 131k 256 and 340, chunks of 700 over 9k 281 and 324, four prompts of 2,000 tokens with a window
+// of 1,024 415 and 425, 94 trees of up to 56 tokens, 448 rows, 438 and 420.  Of head_dim 64, whose products are short beside what a
+// unit's start and end take, the same are 221 and 235, 221 and 213, 361 and 319, 375 and 276.
 #include "tk_attend_mma.cuh"
 
 namespace tk {
 
 template <class T, int D, bool WIN>
 static cudaError_t attend8_rows(const AttendArgs& a, const tk_kv_cache* cache, int64_t rows, int grid, cudaStream_t st) {
-  return rows <= 128 ? attend_launch<T, D, 1, true, WIN, true>(a, cache, grid, st) : attend_launch<T, D, 2, true, WIN, true>(a, cache, grid, st);
+  if constexpr (D == 128) {
+    if (rows > 128) return attend_launch<T, D, 2, true, WIN, true>(a, cache, grid, st);
+  }
+  return attend_launch<T, D, 1, true, WIN, true>(a, cache, grid, st);
 }
 
 template <class T, int D>
