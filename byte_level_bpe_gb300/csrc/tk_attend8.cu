@@ -24,7 +24,7 @@
 // here, the same case: rows as the products' 16, 8 warps 337 us; steps of 32 keys 298; 12 warps 332; rows as
 // their 8, 16 warps 267; a dearer unit 254.
 // More rows go to the 5th-generation tensor cores (tk_attend8_mma.cu): 24 trees of up to 17 rows over 1.5k
-// (head_dim 64) took 49 us there, and 71 here with another 16 rows.
+// (head_dim 64) take 44 us there, and took 66 here with another 16 rows.
 #include "tk_attend.cuh"
 
 namespace tk {
