@@ -19,10 +19,10 @@
 // key's 16 bytes as they are, four neighbouring elements being one thread's share of a product of 16, which may be any
 // 16 as long as the queries take the same; of the values a thread has four keys' 16 bytes, whose bytes it pairs
 // up.  Nothing is written to shared memory but what TMA brings.
-// One token of 128 requests over 6k, 1.63 GB: 254 us, 6.4 TB/s, 94% of a copy's rate.  16 rows take 107 us for 400 MB
-// (3.7 TB/s): the chain of a step's instructions, with half the warps for each row's registers.  Of the way
+// One token of 128 requests over 6k, 1.63 GB: 251 us, 6.5 TB/s, 96% of a copy's rate.  16 rows take 97 us for 400 MB
+// (4.1 TB/s): the chain of a step's instructions, with half the warps for each row's registers.  Of the way
 // here, the same case: rows as the products' 16, 8 warps 337 us; steps of 32 keys 298; 12 warps 332; rows as
-// their 8, 16 warps 267; a dearer unit 254.
+// their 8, 16 warps 267; a dearer unit 251.
 // More rows go to the 5th-generation tensor cores (tk_attend8_mma.cu): 24 trees of up to 17 rows over 1.5k
 // (head_dim 64) take 44 us there, and took 66 here with another 16 rows.
 #include "tk_attend.cuh"
@@ -30,9 +30,6 @@
 namespace tk {
 
 constexpr int A8_STEP = 16;  // keys of a step, one warp's: they lie in one block
-// In tiles of a step for every warp: with a unit cost of 1 one token of 128 requests over 6k takes 269 us instead of 253, and
-// of 32 over 3k (head_dim 64) 40 instead of 38; one over 200 the same.
-constexpr int A8_UNIT_COST = 2, A8_MIN_SHARE = 4, A8_SNAP = 2;
 constexpr float A8_UP = 7.f;
 
 // NR: 8 rows each.  The work on 16 keys is a chain of instructions that wait for one another, so there are as many
@@ -50,8 +47,13 @@ struct Attend8Shape {
   static constexpr int SMALL = BARS + 8 * WARPS * STAGES;
   static constexpr int PIECES = SMALL + 16 + 4 * WARPS * 4 + 16;  // this one and the next one; the walk
   static constexpr int TOTAL = PIECES + 2 * (int)sizeof(Piece) + 192;
+  // What starting a unit costs, in tiles of a step for every warp; half of a worker's least share, and no cut is nearer to
+  // a unit's ends.  Up to 8 rows, one token of 128 requests over 6k, of 64 over 1k and of 8 over 2k (us): 1: 269, 48, 19.2; 2:
+  // 254, 46, 19.7; 3: 251, 45, 19.9; 4: 251, 44, 20.6; 6: 255, 47, 21.4.  Up to 16, one of 64 requests over 6k with 16 rows and
+  // three with 12: 2: 106, 190; 4: 98, 176; 6: 97, 173; 8: 100, 174.
+  static constexpr int UNIT_COST = NR == 1 ? 3 : 6;
   template <bool WIN>
-  using Tiles = Tiling<ROWS, A8_STEP, WARPS, WIN, A8_UNIT_COST, A8_MIN_SHARE, A8_SNAP, 2, true>;
+  using Tiles = Tiling<ROWS, A8_STEP, WARPS, WIN, UNIT_COST, 2 * UNIT_COST, UNIT_COST, 2, true>;
   static_assert(SMALL % 8 == 0 && PIECES % 8 == 0 && TOTAL <= 227 * 1024, "shared memory of one CTA");
 };
 
