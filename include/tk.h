@@ -385,7 +385,7 @@ int tk_kv_cache_create8(void* d_k, void* d_v, float* d_k_scale, float* d_v_scale
  * scale to that if it is less, and rounds the block's older elements once more.  Infinities
  * and NaN are stored as NaN and do not count for the scale.  The rows of one block follow one another
  * in the call, as tk_kv_plan places them; of blocks whose rows do not, the scale and the elements are unspecified, and
- * so are those of a place that two rows name.
+ * so are those of a place that two rows name.  T times the cache's heads is at most 2^33 there.
  */
 int tk_kv_append(const tk_kv_cache* cache, const void* d_qkv, int64_t row_stride, int64_t T,
                  int n_q_heads, const float* d_q_gain, const float* d_k_gain, float eps,
