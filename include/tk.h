@@ -436,7 +436,8 @@ void tk_kv_workspace_free(tk_kv_workspace* ws);
  * A call whose offsets decrease gives them for every token, and so may one of too much
  * work: 2^30 tiles of keys or more, over all key heads and tiles of query rows, three
  * tiles more for each of these (64 keys and 32 or 128 rows a tile; 128 and 256 from
- * 129 rows a key head on; from 2^31 on it always does).
+ * 129 rows a key head on, but not with a window in 16 bits or head_dim 64 in 8; in 8 bits up to 16 rows 256 keys and 8 rows,
+ * or 192 and 16 with six tiles more; from 2^31 on it always does).
  * tk_kv_status waits for cuda_stream and gives what the workspace's calls
  * since the last tk_kv_status met first (a timeout before others): TK_OK,
  * TK_E_LIMIT (h_request: the request; -1 if nothing was done) or TK_E_TIMEOUT (a wait
