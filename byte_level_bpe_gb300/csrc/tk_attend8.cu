@@ -425,11 +425,14 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
       }
     if (lane == 0) s_e[warp] = E;
     if (warp != 0) asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+    // What is asked after a whole piece's last barrier is in registers: the first warp may have begun the next piece by
+    // then, and be writing the one after that over this one.
     const bool whole = p.pieces == 1;
+    const int groups = NR == 1 ? 1 : (p.rows + 7) / 8;
     float* part = part8_at<D, ROWS>(a.part, me, p.lo == 0);
 #pragma unroll
     for (int r = 0; r < NR; r++) {
-      if (r * 8 >= p.rows) break;
+      if (r >= groups) break;
 #pragma unroll
       for (int e = 0; e < 2; e++) {
         float* dst = s_o + (warp * 8 + 2 * t4 + e) * L::O_ROW + g * L::O_GROUP;
