@@ -804,8 +804,9 @@ __device__ __forceinline__ void store8_runs(const Store8Args& s, int cta) {
           if (r >= rows || !in_dim) break;
           uint8_t* dst = to + (a.slot[t0 + r] & within) * a.s_token;
           const float by = inv[k] * per_scale;
-          // exact if the scale is a power of two and the factor a normal number
-          if (pow2 && by >= 1.17549435e-38f && largest(y[k]) * inv[k] < INFINITY) {
+          // exact if the scale is a power of two and the factor a normal number; of a row of zeros with a small eps under the
+          // least scale it is infinite, and 0 times it no number
+          if (pow2 && by >= 1.17549435e-38f && by < INFINITY && largest(y[k]) * inv[k] < INFINITY) {
             *reinterpret_cast<uint2*>(dst + e0) = to_e4m3<true>(y[k], by, 1.f);
             *reinterpret_cast<uint2*>(dst + e1) = to_e4m3<true>(y[k] + 8, by, 1.f);
           } else {

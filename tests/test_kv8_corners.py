@@ -4,7 +4,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from test_kv import TYPES  # noqa: E402
-from test_kv8 import case8, check8  # noqa: E402
+from test_kv8 import E4M3, case8, check8  # noqa: E402
 from test_kv_ranges import tk  # noqa: E402,F401
 
 
@@ -26,3 +26,30 @@ def test_ragged_units_of_up_to_16_rows(tk, dtype, d, group, most):
     for _ in range(50):
         assert torch.equal(cache.attend(*args, ws, max_new=most), got)
     ws.status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,heads", [(1, 1), (40, 2), (3000, 1)])
+@pytest.mark.parametrize("eps", [1e-6, 2.0 ** -57, 1e-20, 1e-37])
+def test_append_of_zero_keys_with_a_norm(tk, T, heads, eps):
+    """0 / sqrt(0 + eps) is 0, however small eps is; rows of zeros beside others too."""
+    d, bs = 64, 16
+    blocks = T // bs + 2
+    k, v = (torch.full((blocks, heads, bs, d), 1.0, device="cuda").to(E4M3) for _ in "kv")
+    ks, vs = (torch.full((blocks, heads), 4.0, device="cuda") for _ in "kv")
+    cache = tk.KVCache(k, v, ks, vs)
+    x = torch.zeros(T, 3 * heads * d, dtype=torch.bfloat16, device="cuda")
+    pos, slots = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.arange(T, device="cuda") + bs
+    gain = torch.full((d,), 2.0, device="cuda")
+    q = cache.append(x, pos, slots, heads, q_gain=gain, k_gain=gain, eps=eps)
+    rows = lambda y: y.float().transpose(1, 2).flatten(0, 1)[bs:bs + T]  # noqa: E731
+    assert bool((q == 0).all()) and bool((rows(k) == 0).all()) and bool((rows(v) == 0).all())
+    used = slice(1, (T + bs - 1) // bs + 1)
+    assert bool((ks[used] == 2.0 ** -100).all()) and bool((vs[used] == 2.0 ** -100).all()) and bool((ks[0] == 4).all())
+    x[::3] = 0.5
+    cache.append(x, pos, slots, heads, q_gain=gain, k_gain=gain, eps=eps)
+    got = (k.float() * ks[..., None, None]).transpose(1, 2).flatten(0, 1)[bs:bs + T]
+    # 0.5 / sqrt(0.25 + eps) * 2: eps at most 1e-6
+    assert bool(((got[::3] - 2).abs() <= 2.0 ** -4 * 2).all())
+    got[::3] = 0
+    assert bool((got == 0).all())
