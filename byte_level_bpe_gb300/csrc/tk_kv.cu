@@ -1074,6 +1074,11 @@ static int kv_create(const char* where, void* d_k, void* d_v, float* d_k_scale, 
       return kv_arg(where, "a stride is below head_dim, no multiple of 16 bytes, or 2^38 and more");
   }
   if (!aligned16(d_k) || !aligned16(d_v)) return kv_arg(where, "keys or values are not 16-byte aligned");
+  if (d_k_scale) {
+    const uintptr_t ks = (uintptr_t)d_k_scale, vs = (uintptr_t)d_v_scale;
+    if ((ks < vs ? vs - ks : ks - vs) < (uintptr_t)n_blocks * n_heads * sizeof(float))
+      return kv_arg(where, "the scales of keys and values overlap");
+  }
   int dev = 0, sms = 1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -1120,7 +1125,6 @@ extern "C" int tk_kv_cache_create8(void* d_k, void* d_v, float* d_k_scale, float
                                    int n_heads, int block_size, int head_dim, const int64_t* stride, tk_kv_cache** out) {
   const char* where = "tk_kv_cache_create8";
   if (!d_k_scale || !d_v_scale) return kv_arg(where, "null pointer");
-  if (d_k_scale == d_v_scale) return kv_arg(where, "keys and values have the same scales");
   if ((((uintptr_t)d_k_scale | (uintptr_t)d_v_scale) & 3) != 0) return kv_arg(where, "scales are not 4-byte aligned");
   return kv_create(where, d_k, d_v, d_k_scale, d_v_scale, type, n_blocks, n_heads, block_size, head_dim, stride, out);
 }

@@ -213,7 +213,7 @@ class KVCache:
                 _need(x is not None and x.dtype is torch.float32 and x.shape == k.shape[:2] and x.is_contiguous()
                       and x.get_device() == k.get_device(),
                       "k_scale and v_scale must be contiguous float32[n_blocks, kv_heads] tensors on k's device")
-            _need(k_scale.data_ptr() != v_scale.data_ptr(), "k_scale and v_scale must be two tensors")
+            _need(abs(k_scale.data_ptr() - v_scale.data_ptr()) >= 4 * k_scale.numel(), "k_scale and v_scale must not overlap")
         else:
             _need(k_scale is None and v_scale is None and dtype in (None, k.dtype),
                   "scales and a type of their own go with float8_e4m3fn keys and values only")

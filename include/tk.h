@@ -355,7 +355,7 @@ void tk_kv_cache_free(tk_kv_cache* cache);
  *
  *   d_k, d_v: as above with one byte an element; strides multiples of 16 elements.
  *   d_k_scale, d_v_scale [n_blocks][n_heads]: finite, 0 or above (tk_kv_append writes powers of two; of
- *       blocks that hold nothing yet they need not be set).
+ *       blocks that hold nothing yet they need not be set).  The two do not overlap.
  *   type: of the rows, queries and outputs of the calls (TK_BF16 or TK_F16).
  */
 int tk_kv_cache_create8(void* d_k, void* d_v, float* d_k_scale, float* d_v_scale, int type, int64_t n_blocks,

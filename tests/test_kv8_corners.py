@@ -1,11 +1,35 @@
 """Corners of the paged cache in 8 bits (KVCache over float8_e4m3fn blocks), against plain forms in 64 bits."""
+import ctypes
+
 import pytest
 
 torch = pytest.importorskip("torch")
 
 from test_kv import TYPES  # noqa: E402
 from test_kv8 import E4M3, case8, check8  # noqa: E402
-from test_kv_ranges import tk  # noqa: E402,F401
+from test_kv_ranges import host, host_inputs, on_cuda, tk  # noqa: E402,F401
+
+
+@pytest.mark.parametrize("shift", [-28, -4, 4, 28])
+def test_scales_that_overlap_are_refused(shift):
+    """Of 4 blocks of 2 heads: a block's scale of the values would be another's of the keys."""
+    from byte_level_bpe_gb300 import native
+    lib, h = native.load(), ctypes.c_void_p()
+    for apart, what in ((shift, b"overlap"), (0, b"overlap")):
+        rc = lib.tk_kv_cache_create8(1 << 20, 1 << 21, 1 << 22, (1 << 22) + apart, 1, 4, 2, 16, 64, None, ctypes.byref(h))
+        assert rc == native.TK_E_ARG and what in lib.tk_last_error()
+
+
+def test_views_of_scales_that_overlap_are_refused(tk, host):
+    x = host_inputs()
+    k, both = on_cuda(x["k"].to(E4M3)), on_cuda(torch.ones(20, 2))
+    for a, b in ((0, 1), (7, 0), (5, 5)):
+        with pytest.raises(ValueError):
+            tk.KVCache(k, k, both[a:a + 8], both[b:b + 8])
+    assert [n for n, _ in host.calls if "free" not in n] == []
+    tk.KVCache(k, k, both[:8], both[8:16])
+    tk.KVCache(k, k, both[8:16], both[:8])
+    assert [n for n, _ in host.calls if "free" not in n] == ["tk_kv_cache_create8"] * 2
 
 
 @pytest.mark.gpu
