@@ -466,8 +466,10 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
           y.w = fmaf(fe, z.w, y.w);
         }
         const bool none = sum == 0.f;
-        const float inv = none ? 0.f : exp2f((float)max(Emax, -140)) / sum;
-        y = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+        // (2^E in two factors: of scales from 2^127 on it is 2^128)
+        const float half = exp2f(0.5f * (float)max(Emax, -140)), inv = none ? 0.f : half / sum;
+        y = none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                 : make_float4(y.x * inv * half, y.y * inv * half, y.z * inv * half, y.w * inv * half);
         const float log2sum = none ? -INFINITY : (top == -INFINITY ? 0.f : top - A8_UP) + log2f(sum);
         if (whole) {
           const int gr = p.row0 + rr, tok = by_group(a, gr);

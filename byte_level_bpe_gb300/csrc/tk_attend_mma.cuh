@@ -805,7 +805,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       float* part = part_at<D>(a.part, me, p.lo == 0);
       const int64_t o_at = (int64_t)(p.t0 + tok) * a.hq + p.h * a.group + (gr - tok * a.group);
       if (active) {
-        const float inv = l == 0.f ? 0.f : (E8 ? exp2f(fmaxf(E, -140.f)) : 1.f) / l;
+        // (E8: 2^E in two factors: of scales from 2^127 on it is 2^128)
+        const float half = E8 ? exp2f(0.5f * fmaxf(E, -140.f)) : 1.f, inv = l == 0.f ? 0.f : half / l;
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t x[32];
@@ -814,7 +815,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
           if (live) {
             float o[32];
 #pragma unroll
-            for (int e = 0; e < 32; e++) o[e] = l == 0.f ? 0.f : __uint_as_float(x[e]) * inv;
+            for (int e = 0; e < 32; e++) o[e] = l == 0.f ? 0.f : E8 ? __uint_as_float(x[e]) * inv * half : __uint_as_float(x[e]) * inv;
             if (whole) {
               T* dst = static_cast<T*>(a.out) + o_at * D + d;
 #pragma unroll

@@ -5,9 +5,10 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_kv import TYPES  # noqa: E402
+from test_kv import TYPES, U, _attend_case, _close  # noqa: E402
 from test_kv8 import E4M3, case8, check8  # noqa: E402
 from test_kv_ranges import host, host_inputs, on_cuda, tk  # noqa: E402,F401
+from test_kv_window import sees  # noqa: E402
 
 
 @pytest.mark.parametrize("shift", [-28, -4, 4, 28])
@@ -77,3 +78,73 @@ def test_append_of_zero_keys_with_a_norm(tk, T, heads, eps):
     assert bool(((got[::3] - 2).abs() <= 2.0 ** -4 * 2).all())
     got[::3] = 0
     assert bool((got == 0).all())
+
+
+# What a result may be off by, from the kernels' formulas: o = sum w_j v8_j / sum p_j, p_j = exp(s_j), W_j = p_j vs_j.
+#   The product's weight is W_j in fp16, relative to a maximum M of the row's own W that is within 2^8 of the largest, at 2^7: half
+#   a step is 2^-11 of it, or, of one that is subnormal there, 2^-25 of M / 2^7: 2^-32 of the row's largest W.
+#   Exponents, of scores as large as `big` and log2 of scales up to 2^7, and sums are fp32's: 2^-15 (1 + big) of the sum of |W_j v8_j|.
+#   The result is rounded once, and fp16's least step is 2^-24.
+def exact_rows(q, eight, off, lens, table, scale, masks=None, window=None, sinks=0):
+    """(o, tolerance, lse, big) in 64 bits of nothing but the places that a row sees."""
+    k8, v8, ks, vs = (x.double() for x in eight)
+    T, hq, d = q.shape
+    hk, bs = k8.shape[1], k8.shape[2]
+    o, tol = torch.zeros(T, hq, d, dtype=torch.float64), torch.zeros(T, hq, d, dtype=torch.float64)
+    lse, big = torch.full((T, hq), -float("inf"), dtype=torch.float64), torch.zeros(T, hq, dtype=torch.float64)
+    for r in range(len(lens)):
+        n, L = int(off[r + 1] - off[r]), int(lens[r])
+        for i in range(n):
+            t = int(off[r]) + i
+            mask = None if masks is None else int(masks[t]) & (2 ** 64 - 1)
+            seen = torch.tensor([j for j in range(L) if sees(j, i, n, L, mask, window, sinks)], dtype=torch.long)
+            if not len(seen):
+                continue
+            b, place = table[r].long()[seen // bs], seen % bs
+            for h in range(hq):
+                g = h // (hq // hk)
+                kk, vv = k8[b, g, place] * ks[b, g, None], v8[b, g, place]
+                s = kk @ q[t, h].double() * scale
+                lse[t, h] = torch.logsumexp(s, 0)
+                w = torch.exp(s - lse[t, h]) * vs[b, g]
+                o[t, h] = w @ vv
+                big[t, h] = float((kk.abs() @ q[t, h].double().abs()).max()) * scale
+                tol[t, h] = ((1.02 * 2.0 ** -11 + 2.0 ** -15 * (1 + big[t, h])) * (w @ vv.abs()) + 1.02 * 2.0 ** -32 * w.max() * vv.abs().sum(0)
+                             + 1.02 * U[q.dtype] * o[t, h].abs() + (2.0 ** -25 if q.dtype == torch.float16 else 2.0 ** -134))
+    return o, tol, lse, big
+
+
+def exactly(tk, q, eight, off, lens, table, masks=None, max_new=None, window=None, sinks=0):
+    scale = q.shape[2] ** -0.5
+    o, tol, lse, big = exact_rows(q, eight, off, lens, table, scale, masks, window, sinks)
+    c = lambda x: None if x is None else x.cuda()  # noqa: E731
+    cache, ws = tk.KVCache(*(c(x) for x in eight), q.dtype), tk.KVWorkspace()
+    got, got_lse = cache.attend(c(q), c(off), c(lens), c(table), ws, masks=c(masks), max_new=max_new, lse=True, window=window, sinks=sinks)
+    ws.status()
+    _close(got, o, tol, "out")
+    fin = torch.isfinite(lse)
+    assert torch.equal(torch.isneginf(got_lse.cpu()), torch.isneginf(lse))
+    assert bool(((got_lse.cpu().double() - lse).abs()[fin] <= (2.0 ** -16 * (1 + big))[fin]).all())
+    return got
+
+
+def spread_case(gen, new, ctx, hq, hk, d, bs, dtype):
+    """Blocks that all have values of every size and the value scale 2^-16; of blocks with a larger one `loud` makes values that
+    a 16-bit result can hold."""
+    q, k, v, off, lens, table = _attend_case(gen, new, ctx, hq, hk, d, bs, dtype, poison=False)
+    k8, v8 = k.float().to(E4M3), (40 * v.float()).clamp(-448, 448).to(E4M3)
+    ks, vs = torch.full(k.shape[:2], 0.7), torch.full(k.shape[:2], 2.0 ** -16)
+    return q, (k8, v8, ks, vs), off, lens, table
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,group", [(1, 4), (3, 5), (30, 1), (150, 2)])
+@pytest.mark.parametrize("scales", [(2.0 ** 127, 1.9 * 2.0 ** 127, 2.0 ** 126), (2.0 ** 127, 1.0, 2.0 ** -120), (2.0 ** -110, 1.5 * 2.0 ** -120, 0.0)])
+def test_largest_and_smallest_scales(tk, d, n, group, scales):
+    """Scales of every finite size, where the result is finite."""
+    gen = torch.Generator().manual_seed(n)
+    q, eight, off, lens, table = spread_case(gen, [n, 1], [1700, 20], group, 1, d, 16, torch.bfloat16)
+    eight[1].copy_((0.01 * torch.randn(eight[1].shape, generator=gen)).clamp(-0.0625, 0.0625).to(E4M3))
+    eight[3].copy_(torch.tensor(scales)[torch.randint(0, 3, eight[3].shape, generator=gen)])
+    exactly(tk, q, eight, off, lens, table, max_new=n)
