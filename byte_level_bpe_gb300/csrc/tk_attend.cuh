@@ -448,6 +448,13 @@ struct Seen {
   }
 };
 
+// Over 8 bits, see tk_attend8.cu: the bounds M and R of what a row has seen, before it has seen anything, the exponent of
+// a weight at R, and d.
+constexpr float E8_MOST = 3.402823466e38f, E8_TOP = 15.f;
+__device__ __forceinline__ float e8_shift(float log2_vs, float M, float R) {
+  return fminf(fmaxf(log2_vs + (M - R + E8_TOP), -60.f), 300.f);
+}
+
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const typename Pair<T>::type p = Pair<T>::down(a, b);

@@ -5,11 +5,17 @@
 // queries' type.  Queries of bf16 become fp16 with a power of two for each row that brings their largest element to
 // 2^14: exact but for elements 2^-28 below it, which lose less than fp32's sums do.  The scales
 // stay outside: the keys' is a factor of the scores (16 keys lie in one block), the
-// values' of the weights, relative to the largest so far:
-//   x_j = c ks_j (q.k_j), c = scale log2(e);  p_j = 2^(x_j - m + 7), l += p_j;
-//   w_j = p_j vs_j 2^-E rounded to fp16 (a choice: the products' other type, bf16, has 3 bits less), O += w_j v_j; o = 2^E O / l.
-// m is a running maximum that the weights may pass by 2^8, E the exponent of the largest vs so far: w < 2^15.
-// A weight that fp16 loses is 2^-31 of the largest and less.
+// values' of the weights.  Of each row
+//   x_j = c ks_j (q.k_j), c = scale log2(e);  y_j = x_j + log2(vs_j);  l += 2^(x_j - M);
+//   w_j = 2^(y_j - R + 15) rounded to fp16 (a choice: the products' other type, bf16, has 3 bits less), O += w_j v_j;
+//   o = 2^(R - 15 - M) O / l.
+// M and R are bounds of the x and the y that the row has seen: one that is passed is put 8 above what passed it, so that few
+// steps pass it again; w is 2^7 at least of the row's largest y, and 2^15 at most.  What fp16 loses, its half step of 2^-25,
+// is 2^-32 of the row's largest weight times scale and less: of both, so neither a block that the row
+// does not see nor one of large scale and no weight takes anything from the others.
+// l is summed from the same exponentials: with d = log2(vs) + M - R + 15, the same for a step's 16 keys, w = 2^(x - M + d)
+// and its part of l is 2^-d of w.  d from -60 on leaves nothing of w in fp16 and all of it in fp32, above 300 nothing of l; so it is
+// kept between the two, and finite for scales of any kind in places that nobody sees.
 //
 // The kernel here takes up to 16 rows (query heads of a key head x tokens), where memory is the bound by far, and the
 // operands of tcgen05 would cost more shared memory traffic than the keys and values themselves (the two
@@ -30,7 +36,6 @@
 namespace tk {
 
 constexpr int A8_STEP = 16;  // keys of a step, one warp's: they lie in one block
-constexpr float A8_UP = 7.f;
 
 // NR: 8 rows each.  The work on 16 keys is a chain of instructions that wait for one another, so there are as many
 // warps as their registers allow.  A warp has a ring of its own: STAGES steps of keys and values.
@@ -42,8 +47,8 @@ struct Attend8Shape {
   // the stores and loads of a quarter-warp meet no bank twice
   static constexpr int O_GROUP = D / 8 + 4, O_ROW = 8 * O_GROUP + 4;
   static constexpr int O = WARPS * STAGES * STAGE;
-  static constexpr int STATS = O + WARPS * 8 * O_ROW * 4;  // [ROWS][warp] m, l; [warp] E
-  static constexpr int BARS = STATS + (2 * ROWS + 2) * WARPS * 4;
+  static constexpr int STATS = O + WARPS * 8 * O_ROW * 4;  // [ROWS][warp] M, l, R
+  static constexpr int BARS = STATS + 3 * ROWS * WARPS * 4;
   static constexpr int SMALL = BARS + 8 * WARPS * STAGES;
   static constexpr int PIECES = SMALL + 16 + 4 * WARPS * 4 + 16;  // this one and the next one; the walk
   static constexpr int TOTAL = PIECES + 2 * (int)sizeof(Piece) + 192;
@@ -98,7 +103,7 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
   float* s_o = reinterpret_cast<float*>(smem + L::O);
   float* s_m = reinterpret_cast<float*>(smem + L::STATS);
   float* s_l = s_m + ROWS * WARPS;
-  int* s_e = reinterpret_cast<int*>(s_l + ROWS * WARPS);
+  float* s_r = s_l + ROWS * WARPS;
   int* s_walk = reinterpret_cast<int*>(smem + L::SMALL);
   int* s_sum = s_walk + 4;
   volatile int* abort = s_sum + 4 * WARPS;
@@ -141,7 +146,7 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
   bool ok = true;                 // no wait has given up: else the warp has no more steps
   int step0 = 0, n = 0, next = 0, window = 0;
   int id0 = 0, id1 = 0, id2 = 0;  // block ids of steps `window`, + 32 and + 64 + lane
-  float2 sc0 = {0.f, 0.f}, sc1 = {0.f, 0.f};  // (ks, vs) of the first two
+  float2 sc0 = {0.f, 0.f}, sc1 = {0.f, 0.f};  // (ks, log2 of vs) of the first two
   const int32_t* row = nullptr;
   auto key_of = [&](const Piece& x, int i) {
     const int step = step0 + WARPS * i;
@@ -150,9 +155,9 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
   auto id_of = [&](const Piece& x, int i) { return i + lane < n ? __ldg(row + (key_of(x, i + lane) >> a.log2_bs)) : -1; };
   // (of a block outside the cache zeros are read)
   auto scales_of = [&](const Piece& x, int id) {
-    if (id < 0 || id >= a.n_blocks) return make_float2(0.f, 0.f);
+    if (id < 0 || id >= a.n_blocks) return make_float2(0.f, -INFINITY);
     const int64_t at = (int64_t)id * a.hk + x.h;
-    return make_float2(__ldg(a.k_scale + at), __ldg(a.v_scale + at));
+    return make_float2(__ldg(a.k_scale + at), log2f(__ldg(a.v_scale + at)));
   };
   auto issue = [&](const Piece& x) {
     const int i = next - window;
@@ -237,14 +242,11 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
       asm volatile("bar.arrive 1, %0;" ::"n"(THREADS) : "memory");
     }
     // columns g * D / 8 + 2 j, + 1 of rows 2 t4, + 1
-    float o[NR][KS][4], m[NR][2], l[NR][2];
-    float up[NR][2];  // 7 - m, or 0 while the row has seen nothing
-    int E = -1000;
-    float vs_now = -1.f, vn = 0.f;  // the last step's vs, and that times 2^-E
+    float o[NR][KS][4], m[NR][2], l[NR][2], top[NR][2];  // m is M, top R
 #pragma unroll
     for (int r = 0; r < NR; r++) {
-      m[r][0] = m[r][1] = -INFINITY;
-      l[r][0] = l[r][1] = up[r][0] = up[r][1] = 0.f;
+      m[r][0] = m[r][1] = top[r][0] = top[r][1] = -E8_MOST;
+      l[r][0] = l[r][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < KS; j++) o[r][j][0] = o[r][j][1] = o[r][j][2] = o[r][j][3] = 0.f;
     }
@@ -259,7 +261,7 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
         sc1 = scales_of(p, id1);
         id2 = id_of(p, i + 64);
       }
-      const float ks = __shfl_sync(0xffffffffu, sc0.x, i & 31), vs = __shfl_sync(0xffffffffu, sc0.y, i & 31);
+      const float ks = __shfl_sync(0xffffffffu, sc0.x, i & 31), lv = __shfl_sync(0xffffffffu, sc0.y, i & 31);
       const int k0 = key_of(p, i);
       const bool hidden = !(k0 + A8_STEP <= p.open && (!WIN || k0 >= p.shut || k0 + A8_STEP <= a.sinks));
       const uint32_t st = used % NST, s_k = ring + st * L::STAGE, s_v = s_k + L::TILE;
@@ -298,17 +300,6 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
       __syncwarp();  // the stage has been read
       if (next < n) issue(p);
 
-      float shrink = 1.f;
-      if (vs != vs_now) {
-        const int ev = vs > 0.f ? (int)((__float_as_uint(vs) >> 23) & 255) - 126 : -1000;  // vs <= 2^ev
-        if (ev > E) {
-          shrink = E < -500 ? 0.f : exp2f((float)(E - ev));
-          E = ev;
-        }
-        // 2^-E in two factors: it may be below the least normal number
-        vn = E < -500 ? 0.f : vs * __uint_as_float((uint32_t)(127 - E / 2) << 23) * __uint_as_float((uint32_t)(127 - (E - E / 2)) << 23);
-        vs_now = vs;
-      }
       uint32_t bits[NR][2];  // keys g and g + 8: bits 0 and 8
       if (hidden) {
 #pragma unroll
@@ -329,26 +320,22 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
         // with the least normal number a hidden key's -infinity stays that
         const float c0 = fmaxf(cq[r][0] * ks, 1.17549435e-38f), c1 = fmaxf(cq[r][1] * ks, 1.17549435e-38f);
         float x0 = fmaxf(s[r][0], s[r][2]) * c0, x1 = fmaxf(s[r][1], s[r][3]) * c1;
-        const bool above = (x0 > m[r][0] && !(x0 - m[r][0] <= 8.f)) || (x1 > m[r][1] && !(x1 - m[r][1] <= 8.f));
-        if (__any_sync(0xffffffffu, above || shrink != 1.f)) {
+        if (__any_sync(0xffffffffu, x0 > m[r][0] || x1 > m[r][1] || x0 + lv > top[r][0] || x1 + lv > top[r][1])) {
 #pragma unroll
           for (int e = 4; e < 32; e *= 2) {
             x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, e));
             x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, e));
           }
-          const bool grow0 = x0 > m[r][0] && !(x0 - m[r][0] <= 8.f), grow1 = x1 > m[r][1] && !(x1 - m[r][1] <= 8.f);
-          const float by0 = grow0 ? exp2_fast(m[r][0] - x0) : 1.f, by1 = grow1 ? exp2_fast(m[r][1] - x1) : 1.f;
-          if (grow0) {
-            m[r][0] = x0;
-            up[r][0] = A8_UP - x0;
-          }
-          if (grow1) {
-            m[r][1] = x1;
-            up[r][1] = A8_UP - x1;
-          }
-          l[r][0] *= by0;
-          l[r][1] *= by1;
-          const float f0 = by0 * shrink, f1 = by1 * shrink;
+          // the factor that a new bound brings with it
+          auto pass = [](float x, float& bound) {
+            if (!(x > bound)) return 1.f;
+            const float was = bound;
+            bound = x + 8.f;
+            return exp2_fast(was - bound);
+          };
+          l[r][0] *= pass(x0, m[r][0]);
+          l[r][1] *= pass(x1, m[r][1]);
+          const float f0 = pass(x0 + lv, top[r][0]), f1 = pass(x1 + lv, top[r][1]);
 #pragma unroll
           for (int j = 0; j < KS; j++) {
             o[r][j][0] *= f0;
@@ -357,12 +344,14 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
             o[r][j][3] *= f1;
           }
         }
-        const float p0 = exp2_fast(fmaf(s[r][0], c0, up[r][0])), p1 = exp2_fast(fmaf(s[r][1], c1, up[r][1])),
-                    p2 = exp2_fast(fmaf(s[r][2], c0, up[r][0])), p3 = exp2_fast(fmaf(s[r][3], c1, up[r][1]));
-        l[r][0] += p0 + p2;
-        l[r][1] += p1 + p3;
-        pb[r][0] = transpose8x8(pack2<__half>(p0 * vn, p1 * vn));
-        pb[r][1] = transpose8x8(pack2<__half>(p2 * vn, p3 * vn));
+        const float d0 = e8_shift(lv, m[r][0], top[r][0]), d1 = e8_shift(lv, m[r][1], top[r][1]);
+        const float to0 = d0 - m[r][0], to1 = d1 - m[r][1];
+        const float p0 = exp2_fast(fmaf(s[r][0], c0, to0)), p1 = exp2_fast(fmaf(s[r][1], c1, to1)),
+                    p2 = exp2_fast(fmaf(s[r][2], c0, to0)), p3 = exp2_fast(fmaf(s[r][3], c1, to1));
+        l[r][0] = fmaf(p0 + p2, exp2_fast(-d0), l[r][0]);
+        l[r][1] = fmaf(p1 + p3, exp2_fast(-d1), l[r][1]);
+        pb[r][0] = transpose8x8(pack2<__half>(p0, p1));
+        pb[r][1] = transpose8x8(pack2<__half>(p2, p3));
       }
 
       // values of keys that a row does not see have no influence on it: NaN become 0, and come
@@ -421,9 +410,9 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
         if (g == 0) {
           s_m[(r * 8 + 2 * t4 + e) * WARPS + warp] = m[r][e];
           s_l[(r * 8 + 2 * t4 + e) * WARPS + warp] = x;
+          s_r[(r * 8 + 2 * t4 + e) * WARPS + warp] = top[r][e];
         }
       }
-    if (lane == 0) s_e[warp] = E;
     if (warp != 0) asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
     // What is asked after a whole piece's last barrier is in registers: the first warp may have begun the next piece by
     // then, and be writing the one after that over this one.
@@ -442,35 +431,33 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
       }
       if (r == 0 && nx.valid) start(nx);
       __syncthreads();
-      int Emax = -1000;
-#pragma unroll
-      for (int w = 0; w < WARPS; w++) Emax = max(Emax, s_e[w]);
       for (int x = tid; x < min(p.rows - r * 8, 8) * (D / 4); x += THREADS) {
         const int in = x / (D / 4), rr = r * 8 + in, col = (x % (D / 4)) * 4;
-        float top = -INFINITY, sum = 0.f;
+        float M = -E8_MOST, R = -E8_MOST, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; w++) top = fmaxf(top, s_m[rr * WARPS + w]);
+        for (int w = 0; w < WARPS; w++) {
+          M = fmaxf(M, s_m[rr * WARPS + w]);
+          R = fmaxf(R, s_r[rr * WARPS + w]);
+        }
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < WARPS; w++) {
           const float lw = s_l[rr * WARPS + w];
           if (lw == 0.f) continue;  // the warp saw nothing
-          const float mw = s_m[rr * WARPS + w], f = top == mw || mw == -INFINITY ? 1.f : exp2_fast(mw - top);
-          sum = fmaf(f, lw, sum);
-          if (s_e[w] < -500) continue;
-          const float fe = f * exp2_fast((float)max(s_e[w] - Emax, -200));
+          sum = fmaf(exp2_fast(s_m[rr * WARPS + w] - M), lw, sum);
+          const float f = exp2_fast(s_r[rr * WARPS + w] - R);
           const float4 z = *reinterpret_cast<const float4*>(s_o + (w * 8 + in) * L::O_ROW + col / (D / 8) * L::O_GROUP + col % (D / 8));
-          y.x = fmaf(fe, z.x, y.x);
-          y.y = fmaf(fe, z.y, y.y);
-          y.z = fmaf(fe, z.z, y.z);
-          y.w = fmaf(fe, z.w, y.w);
+          y.x = fmaf(f, z.x, y.x);
+          y.y = fmaf(f, z.y, y.y);
+          y.z = fmaf(f, z.z, y.z);
+          y.w = fmaf(f, z.w, y.w);
         }
         const bool none = sum == 0.f;
-        // (2^E in two factors: of scales from 2^127 on it is 2^128)
-        const float half = exp2f(0.5f * (float)max(Emax, -140)), inv = none ? 0.f : half / sum;
+        // (in two factors: of scales from 2^127 on it may be more than fp32 has)
+        const float half = exp2f(0.5f * (R - E8_TOP - M)), inv = none ? 0.f : half / sum;
         y = none ? make_float4(0.f, 0.f, 0.f, 0.f)
                  : make_float4(y.x * inv * half, y.y * inv * half, y.z * inv * half, y.w * inv * half);
-        const float log2sum = none ? -INFINITY : (top == -INFINITY ? 0.f : top - A8_UP) + log2f(sum);
+        const float log2sum = none ? -INFINITY : M + log2f(sum);
         if (whole) {
           const int gr = p.row0 + rr, tok = by_group(a, gr);
           const int64_t at = (int64_t)(p.t0 + tok) * a.hq + p.h * a.group + (gr - tok * a.group);

@@ -5,7 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_kv import TYPES, U, _attend_case, _close  # noqa: E402
+from test_kv import TYPES, U, _attend_case, _close, _tree_masks  # noqa: E402
 from test_kv8 import E4M3, case8, check8  # noqa: E402
 from test_kv_ranges import host, host_inputs, on_cuda, tk  # noqa: E402,F401
 from test_kv_window import sees  # noqa: E402
@@ -147,4 +147,86 @@ def test_largest_and_smallest_scales(tk, d, n, group, scales):
     q, eight, off, lens, table = spread_case(gen, [n, 1], [1700, 20], group, 1, d, 16, torch.bfloat16)
     eight[1].copy_((0.01 * torch.randn(eight[1].shape, generator=gen)).clamp(-0.0625, 0.0625).to(E4M3))
     eight[3].copy_(torch.tensor(scales)[torch.randint(0, 3, eight[3].shape, generator=gen)])
+    exactly(tk, q, eight, off, lens, table, max_new=n)
+
+
+def loud(gen, eight, b, scale):
+    _, v8, _, vs = eight
+    v8[b] = torch.exp2(-8 + 4 * torch.rand(v8[b].shape, generator=gen)).to(E4M3)
+    vs[b] = scale
+
+
+ROWS = [(8, 1), (2, 4), (16, 1), (3, 5)]  # new tokens, query heads a key head
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,group", ROWS)
+@pytest.mark.parametrize("ctx", [0, 14, 60, 3005])
+def test_scales_of_later_blocks(tk, dtype, d, n, group, ctx):
+    """A block that a chunk's later tokens begin has no influence on the earlier ones, whatever its scale."""
+    gen = torch.Generator().manual_seed(n + ctx)
+    q, eight, off, lens, table = spread_case(gen, [n, 1], [ctx, 33], group, 1, d, 16, dtype)
+    for i, place in enumerate((ctx + 1, ctx + n // 2, ctx + n - 1)):
+        if place // 16 > ctx // 16:
+            loud(gen, eight, int(table[0, place // 16]), 2.0 ** (5 + 7 * i))
+    exactly(tk, q, eight, off, lens, table, max_new=n)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,group", [(8, 1), (5, 3)])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (70, 3)])
+def test_scales_of_drafted_tokens_that_a_mask_hides(tk, d, n, group, window, sinks):
+    gen = torch.Generator().manual_seed(n)
+    q, eight, off, lens, table = spread_case(gen, [n, 2], [121, 0], group, 1, d, 16, torch.bfloat16)
+    masks = _tree_masks(gen, [n, 2])
+    for i in range(n):  # what lies in the last block is seen by few
+        if 121 + i >= (120 + n) // 16 * 16:
+            loud(gen, eight, int(table[0, (121 + i) // 16]), 2.0 ** 30)
+    exactly(tk, q, eight, off, lens, table, masks, n, window, sinks)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,group", [(1, 4)] + ROWS)
+@pytest.mark.parametrize("bad", [1e38, 3.4e38, float("inf"), float("nan")])
+def test_scales_outside_the_window(tk, dtype, d, n, group, bad):
+    """Blocks that lie between the first tokens and the window may have any scales, unset ones too; a block that the window
+    leaves behind has no more influence."""
+    gen = torch.Generator().manual_seed(n)
+    window, sinks, ctx = 100, 5, 516
+    q, eight, off, lens, table = spread_case(gen, [n, 1], [ctx, 33], group, 1, d, 16, dtype)
+    low = ctx + 1 - window
+    for b in range((sinks + 15) // 16, low // 16):
+        for s in eight[2:]:
+            s[int(table[0, b])] = bad
+    if n > 1:
+        loud(gen, eight, int(table[0, low // 16]), 2.0 ** 19)
+    exactly(tk, q, eight, off, lens, table, None, n, window, sinks)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,group", [(1, 1), (1, 8), (2, 6), (9, 1)])
+@pytest.mark.parametrize("ctx", [300, 4000])
+def test_large_scales_of_small_weights(tk, d, n, group, ctx):
+    """Scores and scales of blocks far apart: what counts is their product, whichever of the two is large."""
+    gen = torch.Generator().manual_seed(n + group)
+    q, eight, off, lens, table = spread_case(gen, [n], [ctx], group, 1, d, 16, torch.bfloat16)
+    k8, v8, ks, vs = eight
+    q[..., 0] = d ** 0.5  # scores are 0.7 times a key's first element, and something
+    q[..., 1:] *= 0.2
+    at = torch.randint(0, 4, (len(k8),), generator=gen)
+    k8[..., 0] = torch.tensor([0.0, -20.0, -60.0, -88.0])[at][:, None, None].to(E4M3)
+    vs[:, 0] = torch.exp2(torch.tensor([-30.0, -5.0, 0.0, 30.0, 60.0])[torch.randint(0, 5, (len(k8),), generator=gen)])
+    exactly(tk, q, eight, off, lens, table, max_new=n)
+    # one block has nearly all of the weight and the least scale
+    first = int(table[0, 2])
+    k8[..., 0] = torch.full(k8.shape[:3], -60.0).to(E4M3)
+    k8[first, :, :, 0] = torch.zeros(k8.shape[1:3]).to(E4M3)
+    vs[:] = 2.0 ** 30
+    vs[first] = 1.0
     exactly(tk, q, eight, off, lens, table, max_new=n)
