@@ -448,12 +448,11 @@ struct Seen {
   }
 };
 
-// Over 8 bits, see tk_attend8.cu: the bounds M and R of what a row has seen, before it has seen anything, the exponent of
-// a weight at R, and d.
-constexpr float E8_MOST = 3.402823466e38f, E8_TOP = 15.f;
-__device__ __forceinline__ float e8_shift(float log2_vs, float M, float R) {
-  return fminf(fmaxf(log2_vs + (M - R + E8_TOP), -60.f), 300.f);
-}
+// Over 8 bits, see tk_attend8.cu: the bounds M and R of a row that has seen nothing, the exponent of a weight at R, log2 of a
+// scale of 0; log2 of a values' scale, finite whatever is in a place that nobody sees; and d.
+constexpr float E8_MOST = 3.402823466e38f, E8_TOP = 15.f, E8_NONE = -1000.f;
+__device__ __forceinline__ float e8_log2(float vs) { return fmaxf(fminf(log2f(vs), 128.f), E8_NONE); }
+__device__ __forceinline__ float e8_shift(float lv, float M, float R) { return fmaxf(lv + (M - R + E8_TOP), -60.f); }
 
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {

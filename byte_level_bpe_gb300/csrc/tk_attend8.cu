@@ -14,8 +14,8 @@
 // is 2^-32 of the row's largest weight times scale and less: of both, so neither a block that the row
 // does not see nor one of large scale and no weight takes anything from the others.
 // l is summed from the same exponentials: with d = log2(vs) + M - R + 15, the same for a step's 16 keys, w = 2^(x - M + d)
-// and its part of l is 2^-d of w.  d from -60 on leaves nothing of w in fp16 and all of it in fp32, above 300 nothing of l; so it is
-// kept between the two, and finite for scales of any kind in places that nobody sees.
+// and its part of l is 2^-d of w.  d is kept from falling below -60, where nothing of w is left in fp16 and all of it in fp32;
+// log2(vs) is finite whatever the scales of places that nobody sees are, so that these have the weight 0.
 //
 // The kernel here takes up to 16 rows (query heads of a key head x tokens), where memory is the bound by far, and the
 // operands of tcgen05 would cost more shared memory traffic than the keys and values themselves (the two
@@ -155,9 +155,9 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
   auto id_of = [&](const Piece& x, int i) { return i + lane < n ? __ldg(row + (key_of(x, i + lane) >> a.log2_bs)) : -1; };
   // (of a block outside the cache zeros are read)
   auto scales_of = [&](const Piece& x, int id) {
-    if (id < 0 || id >= a.n_blocks) return make_float2(0.f, -INFINITY);
+    if (id < 0 || id >= a.n_blocks) return make_float2(0.f, E8_NONE);
     const int64_t at = (int64_t)id * a.hk + x.h;
-    return make_float2(__ldg(a.k_scale + at), log2f(__ldg(a.v_scale + at)));
+    return make_float2(__ldg(a.k_scale + at), e8_log2(__ldg(a.v_scale + at)));
   };
   auto issue = [&](const Piece& x) {
     const int i = next - window;
@@ -242,10 +242,10 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
       asm volatile("bar.arrive 1, %0;" ::"n"(THREADS) : "memory");
     }
     // columns g * D / 8 + 2 j, + 1 of rows 2 t4, + 1
-    float o[NR][KS][4], m[NR][2], l[NR][2], top[NR][2];  // m is M, top R
+    float o[NR][KS][4], m[NR][2], l[NR][2], bound[NR][2];  // m is M, bound R
 #pragma unroll
     for (int r = 0; r < NR; r++) {
-      m[r][0] = m[r][1] = top[r][0] = top[r][1] = -E8_MOST;
+      m[r][0] = m[r][1] = bound[r][0] = bound[r][1] = -E8_MOST;
       l[r][0] = l[r][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < KS; j++) o[r][j][0] = o[r][j][1] = o[r][j][2] = o[r][j][3] = 0.f;
@@ -320,22 +320,22 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
         // with the least normal number a hidden key's -infinity stays that
         const float c0 = fmaxf(cq[r][0] * ks, 1.17549435e-38f), c1 = fmaxf(cq[r][1] * ks, 1.17549435e-38f);
         float x0 = fmaxf(s[r][0], s[r][2]) * c0, x1 = fmaxf(s[r][1], s[r][3]) * c1;
-        if (__any_sync(0xffffffffu, x0 > m[r][0] || x1 > m[r][1] || x0 + lv > top[r][0] || x1 + lv > top[r][1])) {
+        if (__any_sync(0xffffffffu, x0 > m[r][0] || x1 > m[r][1] || x0 + lv > bound[r][0] || x1 + lv > bound[r][1])) {
 #pragma unroll
           for (int e = 4; e < 32; e *= 2) {
             x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, e));
             x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, e));
           }
           // the factor that a new bound brings with it
-          auto pass = [](float x, float& bound) {
-            if (!(x > bound)) return 1.f;
-            const float was = bound;
-            bound = x + 8.f;
-            return exp2_fast(was - bound);
+          auto pass = [](float x, float& at) {
+            if (!(x > at)) return 1.f;
+            const float was = at;
+            at = x + 8.f;
+            return exp2_fast(was - at);
           };
           l[r][0] *= pass(x0, m[r][0]);
           l[r][1] *= pass(x1, m[r][1]);
-          const float f0 = pass(x0 + lv, top[r][0]), f1 = pass(x1 + lv, top[r][1]);
+          const float f0 = pass(x0 + lv, bound[r][0]), f1 = pass(x1 + lv, bound[r][1]);
 #pragma unroll
           for (int j = 0; j < KS; j++) {
             o[r][j][0] *= f0;
@@ -344,7 +344,7 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
             o[r][j][3] *= f1;
           }
         }
-        const float d0 = e8_shift(lv, m[r][0], top[r][0]), d1 = e8_shift(lv, m[r][1], top[r][1]);
+        const float d0 = e8_shift(lv, m[r][0], bound[r][0]), d1 = e8_shift(lv, m[r][1], bound[r][1]);
         const float to0 = d0 - m[r][0], to1 = d1 - m[r][1];
         const float p0 = exp2_fast(fmaf(s[r][0], c0, to0)), p1 = exp2_fast(fmaf(s[r][1], c1, to1)),
                     p2 = exp2_fast(fmaf(s[r][2], c0, to0)), p3 = exp2_fast(fmaf(s[r][3], c1, to1));
@@ -410,7 +410,7 @@ k_kv_attend8(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, cons
         if (g == 0) {
           s_m[(r * 8 + 2 * t4 + e) * WARPS + warp] = m[r][e];
           s_l[(r * 8 + 2 * t4 + e) * WARPS + warp] = x;
-          s_r[(r * 8 + 2 * t4 + e) * WARPS + warp] = top[r][e];
+          s_r[(r * 8 + 2 * t4 + e) * WARPS + warp] = bound[r][e];
         }
       }
     if (warp != 0) asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");

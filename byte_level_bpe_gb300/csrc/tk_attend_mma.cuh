@@ -75,8 +75,8 @@ __device__ __forceinline__ uint32_t nonfinite2<__half>(uint32_t w) {
 // E8: a cache in 8 bits.  Its tiles arrive as they are; four more warps turn them into fp16 for the products, which
 // e4m3 is a subset of, so nothing is lost; queries of bf16 become fp16 with a power of two for each row (see
 // tk_attend8.cu, which has the mathematics and takes calls of few rows).  The scales stay outside: a
-// group of 16 keys lies in one block, its keys' scale is a factor of the group's scores, its values' one of its weights,
-// which are relative to 2^E, the largest so far.
+// group of 16 keys lies in one block, its keys' scale is a factor of the group's scores, the log2 of its values' scale a summand
+// of the weights' exponents; m is the bound M there, bound the bound R.
 template <int D, int MODE, bool E8 = false>
 struct AttendShape {
   static constexpr int THREADS = E8 ? 512 : 384;
@@ -271,9 +271,9 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       auto at_key = [&](int tile) { return WIN && tile >= head ? tile + skip : tile; };  // in tiles from key 0 on
       auto id_of = [&](int b) { return b < boxes ? __ldg(row + (b >> per_page)) : 0; };
       auto scale_of = [&](int id) {
-        if (id < 0 || id >= a.n_blocks) return make_float2(0.f, -INFINITY);
+        if (id < 0 || id >= a.n_blocks) return make_float2(0.f, E8_NONE);
         const int64_t at = (int64_t)id * a.hk + h;
-        return make_float2(__ldg(a.k_scale + at), log2f(__ldg(a.v_scale + at)));
+        return make_float2(__ldg(a.k_scale + at), e8_log2(__ldg(a.v_scale + at)));
       };
       auto load = [&](const CUtensorMap* map, Ids& ids, int tile, bool keys) {
         const int box0 = at_key(tile) * ppt;
@@ -293,7 +293,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         if (E8 && keys) {
           const int of = lane >> (log2_box - 4);  // the box of group `lane`
           const float ks = __shfl_sync(0xffffffffu, ids.scale.x, (box0 + of) & 31), vs = __shfl_sync(0xffffffffu, ids.scale.y, (box0 + of) & 31);
-          if (lane < L::GROUPS) s_scale[(scaled % L::SCALED) * L::GROUPS + lane] = of < nb ? make_float2(ks, vs) : make_float2(0.f, -INFINITY);
+          if (lane < L::GROUPS) s_scale[(scaled % L::SCALED) * L::GROUPS + lane] = of < nb ? make_float2(ks, vs) : make_float2(0.f, E8_NONE);
           scaled++;
           __syncwarp();
         }
@@ -589,13 +589,14 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       const int gr = p.row0 + skip + row, tok = live ? by_group(a, gr) : 0;
       Seen<WIN> seen;
       seen.set(a, p, live, tok);
-      float m = -INFINITY, mc = 0.f, l = 0.f, l_full = 0.f;  // mc = m c - UP, or 0 while the row has seen nothing
+      float m = E8 ? -E8_MOST : -INFINITY, l = 0.f, l_full = 0.f;
+      float mc = 0.f;            // m c - UP, or 0 while the row has seen nothing
+      float bound = -E8_MOST;    // E8
       const int lo = p.lo;
       const uint64_t c2 = pair64(c, c);
-      float E = -1000.f;  // E8
 
       // of the scores of a group; with the least normal number a hidden key's -infinity stays that
-      const float cq = c * qs, unit = E8 ? 1.f : c;
+      const float cq = c * qs;
       auto factor = [&](float ks) { return fmaxf(cq * ks, 1.17549435e-38f); };
       const int head = p.head, jump = WIN ? p.skip : 0, shut = p.shut;
       auto at_key = [&](int tile) { return (WIN && tile >= head ? tile + jump : tile) * KEYS; };
@@ -668,11 +669,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
                 if (!((w >> e) & 1)) s[32 * i + e] = 0xff800000u;
             }
           }
-          float mx, shrink = 1.f;
           [[maybe_unused]] const float2* scales = s_scale + ((scaled0 + t) % L::SCALED) * L::GROUPS;
+          float mx, my = -INFINITY;  // the largest score; E8: and with its value's scale
           if constexpr (E8) {
             mx = -INFINITY;
-            float largest = -INFINITY;
 #pragma unroll
             for (int g = 0; g < L::GROUPS; g++) {
               float x = max3(__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1]), __uint_as_float(s[16 * g + 2]));
@@ -682,15 +682,9 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
                 x = max3(x, __uint_as_float(s[16 * g + i]), __uint_as_float(s[16 * g + i + 1]));
                 y = max3(y, __uint_as_float(s[16 * g + i + 2]), __uint_as_float(s[16 * g + i + 3]));
               }
-              x = max3(fmaxf(x, y), __uint_as_float(s[16 * g + 14]), __uint_as_float(s[16 * g + 15]));
-              mx = fmaxf(mx, x * factor(scales[g].x));
-              largest = fmaxf(largest, scales[g].y);
-            }
-            // a whole number above every log2 of a scale so far
-            if (largest >= E) {
-              const float e = floorf(largest) + 1.f;
-              shrink = E < -500.f ? 0.f : exp2f(E - e);
-              E = e;
+              x = max3(fmaxf(x, y), __uint_as_float(s[16 * g + 14]), __uint_as_float(s[16 * g + 15])) * factor(scales[g].x);
+              mx = fmaxf(mx, x);
+              my = fmaxf(my, x + scales[g].y);
             }
           } else {
             float top[4];
@@ -701,42 +695,51 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
               top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
             mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
           }
-          const bool grow = t == 0 || (live && mx > m && !((mx - m) * unit <= 8.f));
-          if (__any_sync(0xffffffffu, grow || (E8 && shrink != 1.f))) {
+          // E8: of the sum another factor than of the output
+          const bool grow = E8 ? live && my > bound : t == 0 || (live && mx > m && !((mx - m) * c <= 8.f));
+          if (E8 && live && mx > m) {
+            l *= exp2_fast(m - (mx + 8.f));
+            m = mx + 8.f;
+          }
+          if (__any_sync(0xffffffffu, grow)) {
             if (t > 0) {
               // the products of the tile before may still run
               wait(b_v, (nt + 1) & 1);
               tmem_fence_after();
-              const float f = grow ? exp2_fast((m - mx) * unit) : 1.f, fo = E8 ? f * shrink : f;
+              const float f = !grow ? 1.f : E8 ? exp2_fast(bound - (my + 8.f)) : exp2_fast((m - mx) * c);
 #pragma unroll 1
               for (int i = 0; i < D / 32; i++) {
                 uint32_t o[32];
                 tmem_ld32(o, t_o + 32 * i);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
+                for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                 tmem_st32(t_o + 32 * i, o);
               }
-              l *= f;
-              l_full *= f;
+              if (!E8) {
+                l *= f;
+                l_full *= f;
+              }
             }
             if (grow) {
-              m = mx;
-              mc = m == -INFINITY ? 0.f : fmaf(m, unit, -UP);
+              if (E8) bound = my + 8.f;
+              else {
+                m = mx;
+                mc = m == -INFINITY ? 0.f : fmaf(m, c, -UP);
+              }
             }
           }
           const uint64_t mc2 = pair64(-mc, -mc);
           if constexpr (E8) {
-            // w = p vs 2^-E = 2^(x - m + 7 + v), v = log2(vs) - E; p itself is a group's sum of w times 2^-v.  With v at
-            // least -60 nothing is left of w in fp16, and all of it in fp32.
+            // a group's part of the sum is 2^-d times that of its weights
             float all[2] = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < KEYS / 64; i++) {
               uint32_t w[32];
 #pragma unroll
               for (int g = 0; g < 4; g++) {
-                const float f = factor(scales[4 * i + g].x), v = fmaxf(scales[4 * i + g].y - E, -60.f);
-                const uint64_t f2 = pair64(f, f), to = pair64(v - mc, v - mc);
+                const float f = factor(scales[4 * i + g].x), d = e8_shift(scales[4 * i + g].y, m, bound);
+                const uint64_t f2 = pair64(f, f), to = pair64(d - m, d - m);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int e = 8 * g; e < 8 * g + 8; e++) {
@@ -746,7 +749,7 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
                   w[e] = pack2<__half>(p0, p1);
                 }
                 const float2 sum2 = unpair64(add2(sum[0], sum[1]));
-                all[g & 1] = fmaf(sum2.x + sum2.y, exp2_fast(-v), all[g & 1]);
+                all[g & 1] = fmaf(sum2.x + sum2.y, exp2_fast(-d), all[g & 1]);
               }
               tmem_st32(t_s + buf * KEYS + 32 * i, w);
             }
@@ -805,8 +808,8 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
       float* part = part_at<D>(a.part, me, p.lo == 0);
       const int64_t o_at = (int64_t)(p.t0 + tok) * a.hq + p.h * a.group + (gr - tok * a.group);
       if (active) {
-        // (E8: 2^E in two factors: of scales from 2^127 on it is 2^128)
-        const float half = E8 ? exp2f(0.5f * fmaxf(E, -140.f)) : 1.f, inv = l == 0.f ? 0.f : half / l;
+        // (E8: in two factors: of scales from 2^127 on it may be more than fp32 has)
+        const float half = E8 ? exp2f(0.5f * (bound - E8_TOP - m)) : 1.f, inv = l == 0.f ? 0.f : half / l;
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t x[32];
@@ -833,10 +836,10 @@ k_kv_attend(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const
         }
         if (live) {
           if (!whole) {
-            __stcg(part + 128 * D + row, l == 0.f ? -INFINITY : mc + log2f(l));
+            __stcg(part + 128 * D + row, l == 0.f ? -INFINITY : (E8 ? m : mc) + log2f(l));
             if (LSE) __stcg(part + 128 * D + 128 + row, l == 0.f || E8 ? 1.f : l_full / l);
           } else if (LSE && a.lse) {
-            a.lse[o_at] = l == 0.f ? -INFINITY : (mc + log2f(E8 ? l : l_full)) * 0.69314718055994531f;
+            a.lse[o_at] = l == 0.f ? -INFINITY : ((E8 ? m : mc) + log2f(E8 ? l : l_full)) * 0.69314718055994531f;
           }
         }
       }

@@ -421,8 +421,8 @@ void tk_kv_workspace_free(tk_kv_workspace* ws);
  *       Scores, softmax and sums are fp32; the weights are rounded to the
  *       cache's type for the product with the values (fp16: a weight below
  *       about 2^-32 of the row's largest counts as 0; over a cache in 8 bits weights times their block's scale are
- *       rounded to fp16, and one below about 2^-31 of the largest counts as 0).  Tokens that the mask
- *       hides, and cache places past d_len, have no influence, whatever they hold.
+ *       rounded to fp16, and one below about 2^-32 of the row's largest such product counts as 0).  Tokens that the mask
+ *       hides, and cache places past d_len, have no influence, whatever they and their blocks' scales hold.
  *
  * R <= 2^20, T <= 2^26, T * n_q_heads < 2^31.  The launch is cooperative (one CTA
  * for each SM; over a cache in 8 bits from 17 rows of a request and key head on, an ordinary one below); a call uses the workspace until it ends, so calls in flight at

@@ -156,7 +156,7 @@ def loud(gen, eight, b, scale):
     vs[b] = scale
 
 
-ROWS = [(8, 1), (2, 4), (16, 1), (3, 5)]  # new tokens, query heads a key head
+ROWS = [(8, 1), (2, 4), (16, 1), (3, 5), (40, 2), (64, 2), (200, 1), (90, 4)]  # new tokens, query heads a key head
 
 
 @pytest.mark.gpu
@@ -176,7 +176,7 @@ def test_scales_of_later_blocks(tk, dtype, d, n, group, ctx):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("n,group", [(8, 1), (5, 3)])
+@pytest.mark.parametrize("n,group", [(8, 1), (5, 3), (30, 2), (64, 4)])
 @pytest.mark.parametrize("window,sinks", [(None, 0), (70, 3)])
 def test_scales_of_drafted_tokens_that_a_mask_hides(tk, d, n, group, window, sinks):
     gen = torch.Generator().manual_seed(n)
@@ -210,7 +210,7 @@ def test_scales_outside_the_window(tk, dtype, d, n, group, bad):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("n,group", [(1, 1), (1, 8), (2, 6), (9, 1)])
+@pytest.mark.parametrize("n,group", [(1, 1), (1, 8), (2, 6), (9, 1), (20, 1), (50, 2), (150, 2)])
 @pytest.mark.parametrize("ctx", [300, 4000])
 def test_large_scales_of_small_weights(tk, d, n, group, ctx):
     """Scores and scales of blocks far apart: what counts is their product, whichever of the two is large."""
