@@ -25,12 +25,14 @@
 // key's 16 bytes as they are, four neighbouring elements being one thread's share of a product of 16, which may be any
 // 16 as long as the queries take the same; of the values a thread has four keys' 16 bytes, whose bytes it pairs
 // up.  Nothing is written to shared memory but what TMA brings.
-// One token of 128 requests over 6k, 1.63 GB: 251 us, 6.5 TB/s, 96% of a copy's rate.  16 rows take 97 us for 400 MB
-// (4.1 TB/s): the chain of a step's instructions, with half the warps for each row's registers.  Of the way
+// One token of 128 requests over 6k, 1.63 GB: 247 to 252 us, 6.5 TB/s, 96% of a copy's rate.  16 rows take 93 us for 400 MB
+// (4.3 TB/s): the chain of a step's instructions, with three quarters of the warps for twice the rows' registers (of head_dim 128
+// some are spilled: 148 to 268 bytes stored a thread, 80 to 88 loaded).  Of the way
 // here, the same case: rows as the products' 16, 8 warps 337 us; steps of 32 keys 298; 12 warps 332; rows as
-// their 8, 16 warps 267; a dearer unit 251.
+// their 8, 16 warps 267; a dearer unit 251; then weights relative to the largest scale of the values instead of
+// to the row's bounds, which was wrong where scales are far apart, the same (16 rows 98).
 // More rows go to the 5th-generation tensor cores (tk_attend8_mma.cu): 24 trees of up to 17 rows over 1.5k
-// (head_dim 64) take 44 us there, and took 66 here with another 16 rows.
+// (head_dim 64) take 47 us there, and took 66 here with another 16 rows.
 #include "tk_attend.cuh"
 
 namespace tk {
@@ -55,7 +57,8 @@ struct Attend8Shape {
   // What starting a unit costs, in tiles of a step for every warp; half of a worker's least share, and no cut is nearer to
   // a unit's ends.  Up to 8 rows, one token of 128 requests over 6k, of 64 over 1k and of 8 over 2k (us): 1: 269, 48, 19.2; 2:
   // 254, 46, 19.7; 3: 251, 45, 19.9; 4: 251, 44, 20.6; 6: 255, 47, 21.4.  Up to 16, one of 64 requests over 6k with 16 rows and
-  // three with 12: 2: 106, 190; 4: 98, 176; 6: 97, 173; 8: 100, 174.
+  // three with 12: 2: 106, 190; 4: 98, 176; 6: 97, 173; 8: 100, 174.  (Weights were relative to the scales' largest then; now 250,
+  // 43, 19.5, and 93, 165.)
   static constexpr int UNIT_COST = NR == 1 ? 3 : 6;
   template <bool WIN>
   using Tiles = Tiling<ROWS, A8_STEP, WARPS, WIN, UNIT_COST, 2 * UNIT_COST, UNIT_COST, 2, true>;

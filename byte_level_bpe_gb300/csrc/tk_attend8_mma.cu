@@ -1,8 +1,9 @@
 // tk_attend8_mma.cu -- the kernels of tk_attend_mma.cuh over a cache in 8 bits, for more than 16 rows.
 // Units of 128 rows for each stream, or for more rows of head_dim 128 of 256 for the pair (us, 256 and 128 rows):
-// 64 drafted tokens over 131k 256 and 340, chunks of 700 over 9k 281 and 324, four prompts of 2,000 tokens with a window
-// of 1,024 415 and 425, 94 trees of up to 56 tokens, 448 rows, 438 and 420.  Of head_dim 64, whose products are short beside what a
-// unit's start and end take, the same are 221 and 235, 221 and 213, 361 and 319, 375 and 276.
+// 64 drafted tokens over 131k 247 and 338, chunks of 700 over 9k 275 and 322, four prompts of 2,000 tokens with a window
+// of 1,024 403 and 437, 94 trees of up to 56 tokens, 448 rows, 442 and 459, the same in fp16 432 and 423.  Of head_dim 64, whose
+// products are short beside what a unit's start and end take, the same are 215 and 235, 219 and 212, 354 and 312, and the trees in
+// fp16 362 and 274.
 #include "tk_attend_mma.cuh"
 
 namespace tk {

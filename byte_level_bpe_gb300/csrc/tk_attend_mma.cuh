@@ -26,8 +26,9 @@
 // of 4 requests with a window of 1,024: 241 us, 0.61 PFLOP/s; with 4,096 1.10; without one 1.32).
 // Over a cache in 8 bits 17 to 128 rows are bound by shared memory: for 64 keys of head_dim 128 a stream
 // has 16 KB written by TMA, read again, 32 KB written as fp16, and 64 KB read by the products, which is 76% of what two streams'
-// time has room for (eight tokens of 64 requests over 6k: 270 us; without turning the tiles 232).  More rows as above:
-// 64 drafted tokens over 131k 256 us, without the exponentials 231.
+// time has room for (eight tokens of 64 requests over 6k: 268 us; without turning the tiles 232).  More rows as above:
+// 64 drafted tokens over 131k 247 us, without the exponentials 231.  (Both without a part when the whole took 270 and 256:
+// weights were relative to the scales' largest.)
 #pragma once
 #include <type_traits>
 

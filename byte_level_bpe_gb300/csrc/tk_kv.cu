@@ -493,9 +493,9 @@ __global__ void __launch_bounds__(APPEND_THREADS, 5) k_kv_append(AppendArgs a) {
 // prompts; 64 rows of up to 128 elements stay in registers between the search for the largest and the store, more are
 // read again.  W = 1: a decode step's few rows, each of which is a block's only one.  The runs of a warp or CTA
 // are those that begin among `chunk` tokens.
-// Bounds: 32k rows of 48 heads take 175 us, 1.5 times what their 777 MB need: the runs wait for one load after the other
-// (slots, rows, positions, angles), the queries alone take 101, and together they wait for issue slots, not memory.  64 rows
-// take 4.8 us, a launch and four loads that follow one another.
+// Bounds: 32k rows of 48 heads take 176 us, 1.5 times what their 777 MB need, with 45% of the issue slots and 46% of DRAM's
+// rate in use: neither is the bound, but the latency of a run's loads, one after the other (slots, rows, positions, angles), at
+// 16 warps an SM; the queries alone take 101.  64 rows take 4.8 us, a launch and four loads that follow one another.
 // Other ways, 32k rows and 64 (us): a warp for each run 234 and 4.9; rows staged in shared memory and looked at
 // twice 237 and 6.9; all heads of a row by one warp 243 and 6.2; a CTA for each run and head with rows loaded twice 292 and
 // 7.6, once 198 and 4.8.
@@ -939,8 +939,11 @@ static void append8_launch(Store8Args& s, bool neighbours, int sms, cudaStream_t
     s.every = (s.store_ctas + grid) / s.store_ctas;
     kernel<<<s.store_ctas + grid, APPEND_THREADS, 0, st>>>(s);
   };
-  // A warp for every token and head while that is no more than 16 for each SM twice over: a decode step.  More tokens
-  // are taken for chunks of prompts, whose runs are longer.
+  // A warp for every token and head while there are no more than 16 warps an SM of keys, and as many of values; more tokens are
+  // taken for chunks of prompts, whose runs are longer.  How long a run is, only the device knows.  One token of 64, 256 and 300
+  // requests (8 heads) takes 4.8, 8.1 and 8.9 us with a warp for each run, 7.6, 22 and 25 with four.  A chunk of a few hundred
+  // tokens falls in the first kind too, where it does worse: 300 tokens in blocks of 16, 64 and 128 11.7, 33 and 60 us, with four warps
+  // 10.6, 12 and 21; 2,400 tokens of 1 head 38 and 17.
   if (s.a.T * s.hk <= enough) {
     s.heads = s.chunk = 1;
     if (neighbours) launch(k_kv_append8<T, LANES, true, 1>, 1);

@@ -285,7 +285,7 @@ class KVCache:
         them for drafted trees, None = each token sees those before it. scale
         defaults to head_dim^-0.5; max_new: no request has more new tokens
         (T if not given; it chooses the kernel, so give it: a decode step with
-        max_new=1 can be a quarter faster). lse=True also returns
+        max_new=1 can be a quarter faster, and over 8 bits a prompt's chunk and single tokens are faster as two calls). lse=True also returns
         float32[T, q_heads]. Tokens of no request, and rows that see nothing, give
         0 and an lse of -inf; so do requests outside the call's limits, of which
         only workspace.status() tells.
