@@ -230,3 +230,54 @@ def test_large_scales_of_small_weights(tk, d, n, group, ctx):
     vs[:] = 2.0 ** 30
     vs[first] = 1.0
     exactly(tk, q, eight, off, lens, table, max_new=n)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,group", [(3, 1), (4, 4), (20, 2), (64, 4)])
+@pytest.mark.parametrize("window", [None, 64])
+def test_rows_that_see_nothing(tk, d, n, group, window):
+    """Empty masks without context give 0 and -infinity, beside rows that see some, whatever the scales of what is hidden."""
+    gen = torch.Generator().manual_seed(n)
+    q, eight, off, lens, table = spread_case(gen, [n, 2, n], [0, 50, 33], group, 1, d, 16, torch.bfloat16)
+    masks = _tree_masks(gen, [n, 2, n])
+    masks[:n:2] = 0  # of the first request
+    masks[n + 2] = 0
+    if n == 3:
+        for s in eight[2:]:
+            s[int(table[0, 0])] = 3.4e38
+        masks[:n] = 0
+    got = exactly(tk, q, eight, off, lens, table, masks, n, window, 2 if window else 0)
+    assert bool((got[:n:2] == 0).all()) and bool((got[n + 2] != 0).any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,group", [(4, 2), (3, 5), (30, 1), (150, 2)])
+def test_queries_that_are_not_finite(tk, dtype, d, n, group):
+    """They make their own row's result NaN or what they make it, and leave the bits of every other row."""
+    gen = torch.Generator().manual_seed(n)
+    q, eight, off, lens, table = spread_case(gen, [n, 1], [700, 30], group, 1, d, 16, dtype)
+    want = exactly(tk, q, eight, off, lens, table, max_new=n)
+    bad = q.clone()
+    bad[1, 0, 5], bad[2, group - 1, 0], bad[n, 0, 1] = float("inf"), float("nan"), -float("inf")
+    cache, ws = tk.KVCache(*(x.cuda() for x in eight), dtype), tk.KVWorkspace()
+    got = cache.attend(bad.cuda(), off.cuda(), lens.cuda(), table.cuda(), ws, max_new=n)
+    ws.status()
+    rows = torch.ones(n + 1, group, dtype=torch.bool)
+    rows[1, 0] = rows[2, group - 1] = rows[n, 0] = False
+    assert torch.equal(got[rows.cuda()], want[rows.cuda()]) and bool(torch.isnan(got[2, group - 1]).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,group", [(1, 4), (3, 5), (30, 2)])
+def test_scales_of_zero(tk, n, group):
+    """Keys' scales of 0 make all scores 0, values' the results."""
+    gen = torch.Generator().manual_seed(n)
+    q, eight, off, lens, table = spread_case(gen, [n, 1], [300, 30], group, 1, 128, 16, torch.bfloat16)
+    eight[2].zero_()
+    exactly(tk, q, eight, off, lens, table, max_new=n)
+    eight[2].fill_(0.7)
+    eight[3].zero_()
+    assert bool((exactly(tk, q, eight, off, lens, table, max_new=n) == 0).all())
